@@ -12,6 +12,11 @@ calls raise if the library is missing.
     cache.append(k_t, v_t)           # [B, H_kv, D]
     out = cache.decode(q)            # q [B, H_q, D] -> fp32 [B, H_q, D]
 
+    # rotary positions, before prefill/append/decode
+    inv_freq, m = rope_frequencies(D, theta=10000.0)
+    q, k = rope(q, k, positions, inv_freq, scale=m)   # [tokens, heads, D]
+
+
     # quantize-dequantize under another grouping (diagnostics, no cache)
     x_hat, sq_err = fake_quant(K, AXIS_PER_TOKEN, G=32, bits=2, symmetric=True)
 """
@@ -56,6 +61,19 @@ class _Bytes(ctypes.Structure):
                 ("total", ctypes.c_size_t)]
 
 
+class RopeTensor(ctypes.Structure):
+    """kivi_rope_tensor"""
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("heads", ctypes.c_int),
+                ("x_token", ctypes.c_longlong), ("x_head", ctypes.c_longlong),
+                ("y_token", ctypes.c_longlong), ("y_head", ctypes.c_longlong)]
+
+
+class RopeScaling(ctypes.Structure):
+    """kivi_rope_scaling"""
+    _fields_ = [("kind", ctypes.c_int), ("factor", ctypes.c_double), ("original", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double)]
+
+
 def lib():
     """Load the CUDA library (raises if it has not been built)."""
     global _lib
@@ -91,7 +109,9 @@ def lib():
     L.kivi_fake_quant.argtypes = [vp, i32, i64, i64, i32, i32, i32, i32, i32, i32, vp, vp, vp]
     L.kivi_fake_quant_levels.argtypes = [vp, i32, i64, i64, i32, i32, i32, i32, P(ctypes.c_double),
                                          vp, vp, vp, vp]
-    for name in ("kivi_cache_create", "kivi_cache_create_ex", "kivi_cache_required_bytes",
+    L.kivi_rope.argtypes = [P(RopeTensor), i32, i32, i64, i32, vp, i32, vp, i32, i32, ctypes.c_float, i32, i32, vp]
+    L.kivi_rope_frequencies.argtypes = [i32, ctypes.c_double, P(RopeScaling), P(ctypes.c_float), P(ctypes.c_float)]
+    for name in ("kivi_rope", "kivi_rope_frequencies", "kivi_cache_create", "kivi_cache_create_ex", "kivi_cache_required_bytes",
                  "kivi_prefill", "kivi_prefill_ragged", "kivi_cache_length_at", "kivi_append", "kivi_decode_attn", "kivi_decode_attn_noalloc",
                  "kivi_append_decode",
                  "kivi_cache_reset",
@@ -136,6 +156,23 @@ def _dtype_code(dtype) -> int:
     if dtype == torch.float16:
         return KIVI_F16
     raise ValueError(f"cache dtype must be bfloat16 or float16, got {dtype}")
+
+
+class _on_device:
+    """The given device current for the calls inside (a call belongs to its
+    tensors' device, whichever device the caller has current)."""
+
+    def __init__(self, device):
+        self.index = device.index
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.before != self.index:
+            torch.cuda.set_device(self.before)
 
 
 def _stream_ptr(stream) -> int:
@@ -374,3 +411,7 @@ def fake_quant_levels(x: torch.Tensor, axis: int, G: int, levels, values: bool =
                                         _stream_ptr(stream)),
            "kivi_fake_quant_levels")
     return xh, cc, err
+
+
+# The operators below use the loader and helpers above.
+from .rotary import rope, rope_frequencies  # noqa: E402

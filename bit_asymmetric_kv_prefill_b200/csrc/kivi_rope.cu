@@ -1,0 +1,291 @@
+// kivi_rope.cu -- rotary positions for queries and keys (kivi_rope) and their
+// frequency tables (kivi_rope_frequencies).
+//
+// A pair (x1, x2) of the first `rot` channels of every head of a token at
+// position t becomes m (x1 cos a - x2 sin a, x2 cos a + x1 sin a), a = t f_i.
+// The map is m times a rotation, so its transpose (the gradient) is the same
+// kernel with the angle negated.
+//
+// Angles.  t f_i is formed and reduced in fp64 turns, u = t (f_i / 2 pi),
+// u - rint(u), and only the fraction is rounded to fp32 for sincospi: the
+// error stays below 3e-7 rad up to t f = 2^31, where an fp32 product alone is
+// 2^-24 t f off (0.06 rad at a million).  fp32_angles asks for that fp32
+// product all the same, because the pre-RoPE cache rotates its keys by
+// fp32(t f_i) and its queries have to agree.
+//
+// Bound: HBM (4 bytes per element; one read, one write).  A thread owns 16
+// channels of one token (8 pairs), computes their 8 sines and cosines once
+// and applies them to `hp` heads.  hp = 1, 2, 4 or 8: the largest that still
+// gives every SM 1024 threads, since the angles cost about seven times the
+// rotation of a head and the threads in flight cover the latency.
+#include <cmath>
+#include <cstring>
+
+#include <cuda_runtime.h>
+
+#include "kivi_common.cuh"
+#include "kivi_internal.h"
+
+namespace kivi {
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopePairs = 8;   // pairs per thread
+
+struct RopeTensor {
+    const uint16_t *x;
+    uint16_t *y;
+    int heads;
+    long long xt, xh, yt, yh;   // strides in elements
+};
+
+struct RopeParams {
+    RopeTensor t[2];
+    int heads0, heads;          // heads of t[0], of both
+    long long tokens;
+    int D, rot;
+    const void *pos;
+    const float *inv_freq;
+    float scale;
+    int negate, fp32_angles, pos64;
+    int slots, hp, head_lanes;  // 16-channel slots, heads per thread, threads per (token, slot)
+};
+
+template <int DT>
+__device__ __forceinline__ float to_f(uint16_t b)
+{
+    if constexpr (DT == KIVI_BF16) return __uint_as_float((uint32_t)b << 16);
+    else return __half2float(__ushort_as_half(b));
+}
+// Two results rounded once to the tensor's type.
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    uint32_t r;
+    if constexpr (DT == KIVI_BF16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        memcpy(&r, &v, 4);
+    } else {
+        const __half2 v = __floats2half2_rn(a, b);
+        memcpy(&r, &v, 4);
+    }
+    return r;
+}
+
+__device__ __forceinline__ long long position(const RopeParams &p, long long tok)
+{
+    return p.pos64 ? ((const long long *)p.pos)[tok] : (long long)((const int *)p.pos)[tok];
+}
+
+// m cos and m sin of the angle of frequency i at position t.
+__device__ __forceinline__ float2 turn(const RopeParams &p, long long t, int i)
+{
+    constexpr double kInv2Pi = 0.15915494309189533577;
+    const float f = __ldg(p.inv_freq + i);
+    const double u = p.fp32_angles ? (double)__fmul_rn((float)t, f) * kInv2Pi : (double)t * ((double)f * kInv2Pi);
+    const float frac = (float)(u - rint(u));
+    float s, c;
+    sincospif(2.0f * frac, &s, &c);
+    if (p.negate) s = -s;
+    return make_float2(c * p.scale, s * p.scale);
+}
+
+// 16-byte loads and stores: every pointer and stride a multiple of 8
+// elements, rot a multiple of 16, D too.
+template <int DT, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p)
+{
+    const long long id = (long long)blockIdx.x * kRopeThreads + threadIdx.x;
+    const int slot = (int)(id % p.slots);
+    const long long rest = id / p.slots;
+    const int hl = (int)(rest % p.head_lanes);
+    const long long tok = rest / p.head_lanes;
+    if (tok >= p.tokens) return;
+    const bool turns = slot < p.rot / 16;
+    // First channels of the two 8-channel chunks.
+    const int c0 = INTER || !turns ? 16 * slot : 8 * slot;
+    const int c1 = INTER || !turns ? c0 + 8 : c0 + p.rot / 2;
+    float2 cs[kRopePairs];
+    if (turns) {
+        const long long t = position(p, tok);
+#pragma unroll
+        for (int i = 0; i < kRopePairs; ++i) cs[i] = turn(p, t, 8 * slot + i);
+    }
+#pragma unroll 4
+    for (int e = 0; e < p.hp; ++e) {
+        const int h = hl + e * p.head_lanes;
+        if (h >= p.heads) break;
+        const bool second = h >= p.heads0;
+        const RopeTensor &T = p.t[second ? 1 : 0];
+        const int hh = second ? h - p.heads0 : h;
+        const uint16_t *x = T.x + tok * T.xt + hh * T.xh;
+        uint16_t *y = T.y + tok * T.yt + hh * T.yh;
+        if (!turns && x == y) continue;
+        uint32_t a[4], b[4];
+        *(uint4 *)a = *(const uint4 *)(x + c0);
+        *(uint4 *)b = *(const uint4 *)(x + c1);
+        if (turns) {
+            if constexpr (INTER) {
+                // Word i of a holds pair i, of b pair 4 + i.
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float u = to_f<DT>((uint16_t)a[i]), v = to_f<DT>((uint16_t)(a[i] >> 16));
+                    const float w = to_f<DT>((uint16_t)b[i]), z = to_f<DT>((uint16_t)(b[i] >> 16));
+                    const float2 m = cs[i], n = cs[4 + i];
+                    a[i] = pack2<DT>(u * m.x - v * m.y, v * m.x + u * m.y);
+                    b[i] = pack2<DT>(w * n.x - z * n.y, z * n.x + w * n.y);
+                }
+            } else {
+                // Halves 2i, 2i + 1 of a pair with those of b.
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float u0 = to_f<DT>((uint16_t)a[i]), u1 = to_f<DT>((uint16_t)(a[i] >> 16));
+                    const float v0 = to_f<DT>((uint16_t)b[i]), v1 = to_f<DT>((uint16_t)(b[i] >> 16));
+                    const float2 m = cs[2 * i], n = cs[2 * i + 1];
+                    a[i] = pack2<DT>(u0 * m.x - v0 * m.y, u1 * n.x - v1 * n.y);
+                    b[i] = pack2<DT>(v0 * m.x + u0 * m.y, v1 * n.x + u1 * n.y);
+                }
+            }
+        }
+        *(uint4 *)(y + c0) = *(const uint4 *)a;
+        *(uint4 *)(y + c1) = *(const uint4 *)b;
+    }
+}
+
+// Any alignment and any even rot: one pair (or one untouched channel) of one
+// head per thread.
+template <int DT, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads) rope_any_kernel(const __grid_constant__ RopeParams p)
+{
+    const long long id = (long long)blockIdx.x * kRopeThreads + threadIdx.x;
+    const int per_head = p.D - p.rot / 2;   // rot/2 pairs, D - rot single channels
+    const int e = (int)(id % per_head);
+    const long long rest = id / per_head;
+    const int h = (int)(rest % p.heads);
+    const long long tok = rest / p.heads;
+    if (tok >= p.tokens) return;
+    const bool second = h >= p.heads0;
+    const RopeTensor &T = p.t[second ? 1 : 0];
+    const int hh = second ? h - p.heads0 : h;
+    const uint16_t *x = T.x + tok * T.xt + hh * T.xh;
+    uint16_t *y = T.y + tok * T.yt + hh * T.yh;
+    if (e >= p.rot / 2) {
+        const int c = e + p.rot / 2;
+        if (x != y) y[c] = x[c];
+        return;
+    }
+    const int c0 = INTER ? 2 * e : e, c1 = INTER ? 2 * e + 1 : e + p.rot / 2;
+    const float2 m = turn(p, position(p, tok), e);
+    const float u = to_f<DT>(x[c0]), v = to_f<DT>(x[c1]);
+    const uint32_t w = pack2<DT>(u * m.x - v * m.y, v * m.x + u * m.y);
+    y[c0] = (uint16_t)w;
+    y[c1] = (uint16_t)(w >> 16);
+}
+
+template <int DT, bool INTER>
+cudaError_t launch_rope(RopeParams &p, bool vec, cudaStream_t st)
+{
+    if (vec) {
+        p.slots = p.D / 16;
+        const long long want = (long long)num_sms() * 1024;
+        p.hp = 8;
+        while (p.hp > 1 && p.tokens * p.slots * ((p.heads + p.hp - 1) / p.hp) < want) p.hp /= 2;
+        p.head_lanes = (p.heads + p.hp - 1) / p.hp;
+        const long long n = p.tokens * p.slots * p.head_lanes;
+        rope_kernel<DT, INTER><<<(unsigned)((n + kRopeThreads - 1) / kRopeThreads), kRopeThreads, 0, st>>>(p);
+    } else {
+        const long long n = p.tokens * p.heads * (p.D - p.rot / 2);
+        rope_any_kernel<DT, INTER><<<(unsigned)((n + kRopeThreads - 1) / kRopeThreads), kRopeThreads, 0, st>>>(p);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace kivi
+
+using namespace kivi;
+
+extern "C" kivi_status kivi_rope(const kivi_rope_tensor *tensors, int n_tensors, kivi_dtype dtype, long long tokens,
+                                 int D, const void *positions, int positions_64, const float *inv_freq, int rot,
+                                 int interleaved, float scale, int inverse, int fp32_angles, void *stream)
+{
+    if (!tensors || n_tensors < 1 || n_tensors > 2 || tokens < 0 || D < 1 || rot < 2 || rot > D || rot % 2 != 0)
+        return KIVI_ERR_ARG;
+    if (dtype != KIVI_F16 && dtype != KIVI_BF16) return KIVI_ERR_ARG;
+    if (!std::isfinite(scale)) return KIVI_ERR_ARG;
+    if (D > 1024) return KIVI_ERR_UNSUPPORTED;
+    if (!inv_freq || ((uintptr_t)inv_freq & 3u) != 0) return KIVI_ERR_ARG;
+    if (tokens > 0 && (!positions || ((uintptr_t)positions & (positions_64 ? 7u : 3u)) != 0)) return KIVI_ERR_ARG;
+    RopeParams p;
+    std::memset(&p, 0, sizeof p);
+    bool vec = D % 16 == 0 && rot % 16 == 0;
+    for (int i = 0; i < n_tensors; ++i) {
+        const kivi_rope_tensor &t = tensors[i];
+        if (t.heads < 1) return KIVI_ERR_ARG;
+        if (tokens > 0 && (!t.x || !t.y || (((uintptr_t)t.x | (uintptr_t)t.y) & 1u) != 0)) return KIVI_ERR_ARG;
+        // In place means the same elements at the same places.
+        if (t.x == t.y && (t.x_token != t.y_token || t.x_head != t.y_head)) return KIVI_ERR_ARG;
+        // Two heads or two tokens must not share the elements they write.
+        const long long ah = t.y_head < 0 ? -t.y_head : t.y_head, at = t.y_token < 0 ? -t.y_token : t.y_token;
+        if ((t.heads > 1 && ah < D) || (tokens > 1 && at < D)) return KIVI_ERR_ARG;
+        if (t.heads > 1 && tokens > 1 && at < (t.heads - 1) * ah + D && ah < (tokens - 1) * at + D) return KIVI_ERR_ARG;
+        p.t[i] = RopeTensor{(const uint16_t *)t.x, (uint16_t *)t.y, t.heads, t.x_token, t.x_head, t.y_token, t.y_head};
+        p.heads += t.heads;
+        vec = vec && (((uintptr_t)t.x | (uintptr_t)t.y) & 15u) == 0
+              && ((t.x_token | t.x_head | t.y_token | t.y_head) & 7) == 0;
+    }
+    if (tokens == 0) return KIVI_OK;
+    if ((double)tokens * p.heads * D > 5e11) return KIVI_ERR_UNSUPPORTED;   // keeps the grid below 2^31 blocks
+    p.heads0 = tensors[0].heads;
+    p.tokens = tokens;
+    p.D = D;
+    p.rot = rot;
+    p.pos = positions;
+    p.pos64 = positions_64 != 0;
+    p.inv_freq = inv_freq;
+    p.scale = scale;
+    p.negate = inverse != 0;
+    p.fp32_angles = fp32_angles != 0;
+    const cudaStream_t st = (cudaStream_t)stream;
+    cudaError_t e;
+    if (dtype == KIVI_BF16)
+        e = interleaved ? launch_rope<KIVI_BF16, true>(p, vec, st) : launch_rope<KIVI_BF16, false>(p, vec, st);
+    else
+        e = interleaved ? launch_rope<KIVI_F16, true>(p, vec, st) : launch_rope<KIVI_F16, false>(p, vec, st);
+    return cuda_status(e);
+}
+
+extern "C" kivi_status kivi_rope_frequencies(int rot, double theta, const kivi_rope_scaling *s, float *inv_freq,
+                                             float *scale)
+{
+    if (rot < 2 || rot % 2 != 0 || !(theta > 1.0) || !std::isfinite(theta) || !inv_freq || !scale) return KIVI_ERR_ARG;
+    const int kind = s ? s->kind : KIVI_ROPE_PLAIN;
+    if (kind < KIVI_ROPE_PLAIN || kind > KIVI_ROPE_BANDS) return KIVI_ERR_ARG;
+    if (kind != KIVI_ROPE_PLAIN && (!(s->factor >= 1.0) || !std::isfinite(s->factor))) return KIVI_ERR_ARG;
+    if (kind == KIVI_ROPE_YARN || kind == KIVI_ROPE_BANDS)
+        if (!(s->original > 0.0) || !std::isfinite(s->original) || !(s->low > 0.0) || !(s->high > s->low)
+            || !std::isfinite(s->high))
+            return KIVI_ERR_ARG;
+    if (kind == KIVI_ROPE_BASE && rot < 4) return KIVI_ERR_ARG;
+    constexpr double k2Pi = 6.283185307179586477;
+    const double base = kind == KIVI_ROPE_BASE ? theta * std::pow(s->factor, (double)rot / (rot - 2)) : theta;
+    *scale = kind == KIVI_ROPE_YARN ? (float)(0.1 * std::log(s->factor) + 1.0) : 1.0f;
+    for (int i = 0; i < rot / 2; ++i) {
+        double f = std::pow(base, -2.0 * i / rot);
+        if (kind == KIVI_ROPE_LINEAR) {
+            f /= s->factor;
+        } else if (kind == KIVI_ROPE_YARN || kind == KIVI_ROPE_BANDS) {
+            // Turns over the original context: a frequency with at least
+            // `high` of them stays, one with at most `low` is divided by the
+            // factor, between the two is a blend: linear in the logarithm of
+            // the turns (i.e. in i) for YARN, in the turns for BANDS.
+            const double turns = s->original * f / k2Pi;
+            double keep = kind == KIVI_ROPE_YARN ? std::log(turns / s->low) / std::log(s->high / s->low)
+                                                 : (turns - s->low) / (s->high - s->low);
+            keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+            f = f * keep + f / s->factor * (1.0 - keep);
+        }
+        inv_freq[i] = (float)f;
+    }
+    return KIVI_OK;
+}

@@ -329,6 +329,68 @@ KIVI_API kivi_status kivi_fake_quant_levels(const void *x, kivi_dtype dtype, lon
                                             int D, int axis, int G, int nlev, const double *levels,
                                             float *xhat, uint8_t *codes, double *sq_err, void *stream);
 
+/*
+ * Rotary positions for queries and keys, the step before kivi_prefill,
+ * kivi_append, kivi_decode_attn and the pool calls (whose queries arrive
+ * rotated).  The first `rot` channels of every head are taken as rot/2 pairs:
+ * channels (i, i + rot/2), or (2i, 2i + 1) with interleaved != 0.  The pair of
+ * frequency i of a token at position t becomes
+ *   scale * (x1 cos a - x2 sin a, x2 cos a + x1 sin a),   a = t * inv_freq[i],
+ * (inverse != 0: a = -t * inv_freq[i], which is also the gradient of the
+ * rotation: dL/dx = kivi_rope(dL/dy, inverse)), computed in fp32 and rounded
+ * once; the other D - rot channels are copied.
+ *   tensors    HOST array of 1 or 2 tensors of `dtype` (queries and keys in
+ *              one launch), each DEVICE x and y [tokens, heads, D] with
+ *              strides in elements and contiguous channels.  y may be x (in
+ *              place; then with the same strides); otherwise they must not
+ *              overlap.  y's strides are at least D.
+ *   positions  DEVICE [tokens], int64 if positions_64 != 0, else int32; any
+ *              order, repeats and negative values allowed.
+ *   inv_freq   DEVICE [rot/2] fp32 (see kivi_rope_frequencies).
+ *   fp32_angles = 0: the angle is exact (formed and reduced in fp64).  != 0:
+ *              the angle is the fp32 product t * inv_freq[i], the convention
+ *              of a pre-RoPE cache's keys; rotate the queries of such a cache
+ *              this way.
+ * Tensors and strides that allow 16-byte accesses (addresses of 16 bytes,
+ * strides of 8 elements, D and rot multiples of 16) take the fast path.
+ * D <= 1024.  tokens = 0 launches nothing.  Asynchronous on `stream`.
+ */
+typedef struct {
+    const void *x;
+    void *y;
+    int heads;
+    long long x_token, x_head, y_token, y_head; /* strides in elements */
+} kivi_rope_tensor;
+
+KIVI_API kivi_status kivi_rope(const kivi_rope_tensor *tensors, int n_tensors, kivi_dtype dtype,
+                               long long tokens, int D, const void *positions, int positions_64,
+                               const float *inv_freq, int rot, int interleaved, float scale,
+                               int inverse, int fp32_angles, void *stream);
+
+/*
+ * Frequencies of rotary positions: inv_freq[i] = theta^(-2i/rot), i < rot/2,
+ * to a HOST array, computed in fp64 and rounded once, and the factor `scale`
+ * for kivi_rope (1 unless stated).  scaling (NULL: plain) stretches them for
+ * contexts `factor` >= 1 times longer:
+ *   LINEAR  every frequency divided by factor;
+ *   BASE    theta raised to theta * factor^(rot/(rot - 2));
+ *   YARN    by the turns n_i = original * inv_freq[i] / 2 pi of the original
+ *           context: n_i >= high keeps the frequency, n_i <= low divides it by
+ *           factor, between them a blend linear in log n_i;
+ *           scale = 0.1 ln(factor) + 1;
+ *   BANDS   the same with a blend linear in n_i, scale = 1.
+ */
+typedef enum {
+    KIVI_ROPE_PLAIN = 0, KIVI_ROPE_LINEAR = 1, KIVI_ROPE_BASE = 2, KIVI_ROPE_YARN = 3, KIVI_ROPE_BANDS = 4
+} kivi_rope_kind;
+typedef struct {
+    int kind; /* kivi_rope_kind */
+    double factor, original, low, high;
+} kivi_rope_scaling;
+
+KIVI_API kivi_status kivi_rope_frequencies(int rot, double theta, const kivi_rope_scaling *scaling,
+                                           float *inv_freq, float *scale);
+
 #ifdef __cplusplus
 }
 #endif

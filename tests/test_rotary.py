@@ -1,0 +1,250 @@
+"""Rotary positions: frequency tables and refusals on the CPU, the rotation on
+the GPU against the formula in 64 bits."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import bit_asymmetric_kv_prefill_b200 as kivi
+from bit_asymmetric_kv_prefill_b200 import build as kbuild
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    kbuild.build()
+
+
+# ---- frequencies (CPU) ------------------------------------------------------------
+def _freq(rot, **kw):
+    return kivi.rope_frequencies(rot, device="cpu", **kw)
+
+
+@pytest.mark.parametrize("rot,theta", [(2, 10000.0), (64, 10000.0), (128, 500000.0), (96, 1e6)])
+def test_plain_frequencies(rot, theta):
+    f, m = _freq(rot, theta=theta)
+    want = torch.tensor([theta ** (-2 * i / rot) for i in range(rot // 2)], dtype=torch.float64)
+    assert m == 1.0 and f.dtype == torch.float32
+    # One rounding to fp32 (half a step, 2^-24) of a value good to 1e-15.
+    assert ((f.double() - want).abs() <= want * (2 ** -24 + 1e-14)).all()
+
+
+def test_scaled_frequencies():
+    rot, theta, factor, L = 64, 10000.0, 8.0, 4096.0
+    plain = torch.tensor([theta ** (-2 * i / rot) for i in range(rot // 2)], dtype=torch.float64)
+    step = 2 ** -24 + 1e-13
+    f, m = _freq(rot, scaling="linear", factor=factor)
+    assert m == 1.0 and ((f.double() - plain / factor).abs() <= plain / factor * step).all()
+    f, m = _freq(rot, scaling="base", factor=factor)
+    base = theta * factor ** (rot / (rot - 2))
+    want = torch.tensor([base ** (-2 * i / rot) for i in range(rot // 2)], dtype=torch.float64)
+    assert m == 1.0 and ((f.double() - want).abs() <= want * step).all()
+    # The slowest frequency is divided by the factor, the fastest stays.
+    assert math.isclose(float(f[-1]), float(plain[-1]) / factor, rel_tol=1e-6) and float(f[0]) == 1.0
+    for kind in ("yarn", "bands"):
+        f, m = _freq(rot, scaling=kind, factor=factor, original=L, low=1.0, high=32.0)
+        assert math.isclose(m, 0.1 * math.log(factor) + 1.0 if kind == "yarn" else 1.0, rel_tol=1e-7)
+        turns = L * plain / (2 * math.pi)
+        for i in range(rot // 2):
+            n = float(turns[i])
+            x = math.log(n) / math.log(32.0) if kind == "yarn" else (n - 1.0) / 31.0
+            x = min(1.0, max(0.0, x))
+            want = float(plain[i]) * (x + (1 - x) / factor)
+            assert abs(float(f[i]) - want) <= want * step, (kind, i)
+        assert (turns < 1).any() and (turns > 32).any()   # all three ranges occur
+
+
+@pytest.mark.parametrize("kw", [
+    dict(rot=0), dict(rot=3), dict(theta=1.0), dict(theta=float("nan")), dict(scaling="linear", factor=0.5),
+    dict(scaling="linear", factor=float("inf")), dict(scaling="yarn", factor=2.0, original=0.0),
+    dict(scaling="bands", factor=2.0, original=4096.0, low=4.0, high=4.0), dict(rot=2, scaling="base", factor=2.0),
+])
+def test_bad_frequency_arguments(kw):
+    kw = dict(kw)
+    with pytest.raises(kivi.KiviError) as e:
+        _freq(kw.pop("rot", 64), **kw)
+    assert e.value.code == 1
+
+
+def test_unknown_scaling():
+    with pytest.raises(ValueError):
+        _freq(64, scaling="other")
+
+
+# ---- refusals (CPU: every case fails its argument check before any launch) -----------
+_T = dict(x=256, y=512, heads=4, x_token=512, x_head=128, y_token=512, y_head=128)
+_A = dict(n=1, dtype=kivi.KIVI_BF16, tokens=8, D=128, pos=256, pos64=0, inv=512, rot=128, scale=1.0)
+
+
+@pytest.mark.parametrize("t,a,code", [
+    (dict(x=None), {}, 1), (dict(y=None), {}, 1), (dict(x=257), {}, 1), (dict(heads=0), {}, 1),
+    (dict(y=256, y_token=1024), {}, 1),            # in place with other strides
+    (dict(y_head=64), {}, 1), (dict(y_token=64), {}, 1),   # outputs that overlap
+    (dict(y_token=256, y_head=128), {}, 1),        # tokens overlap heads
+    ({}, dict(n=0), 1), ({}, dict(n=3), 1), ({}, dict(dtype=2), 1), ({}, dict(tokens=-1), 1),
+    ({}, dict(D=0), 1), ({}, dict(rot=0), 1), ({}, dict(rot=129), 1), ({}, dict(rot=130), 1), ({}, dict(rot=63), 1),
+    ({}, dict(pos=None), 1), ({}, dict(pos=258), 1), ({}, dict(pos=260, pos64=1), 1), ({}, dict(inv=None), 1),
+    ({}, dict(inv=514), 1), ({}, dict(scale=float("nan")), 1),
+    (dict(x_head=2048, y_head=2048, x_token=8192, y_token=8192), dict(D=1026), 2),
+])
+def test_rope_rejects_bad_arguments(t, a, code):
+    t, a = dict(_T, **t), dict(_A, **a)
+    arr = (kivi.RopeTensor * 3)(*[kivi.RopeTensor(*[t[f] for f, _ in kivi.RopeTensor._fields_])] * 3)
+    assert kivi.lib().kivi_rope(arr, a["n"], a["dtype"], a["tokens"], a["D"], a["pos"], a["pos64"], a["inv"],
+                                a["rot"], 0, a["scale"], 0, 0, None) == code
+
+
+def test_rope_of_no_tokens_launches_nothing():
+    arr = (kivi.RopeTensor * 1)(kivi.RopeTensor(None, None, 4, 512, 128, 512, 128))
+    assert kivi.lib().kivi_rope(arr, 1, kivi.KIVI_F16, 0, 128, None, 0, 512, 128, 0, 1.0, 0, 0, None) == 0
+    assert kivi.lib().kivi_rope(None, 1, kivi.KIVI_F16, 0, 128, None, 0, 512, 128, 0, 1.0, 0, 0, None) == 1
+
+
+# ---- the rotation (GPU) -----------------------------------------------------------------
+def _want(x, pos, f, m, rot, inter, sign, fp32_angles=False):
+    """The formula in 64 bits (angles as documented)."""
+    if fp32_angles:
+        a = (pos.float()[:, None] * f).double()
+    else:
+        a = pos.double()[:, None] * f.double()
+    c, s = (torch.cos(a) * m)[:, None], (torch.sin(a) * (m * sign))[:, None]
+    y = x.double().clone()
+    i = torch.arange(rot // 2, device=x.device)
+    i0, i1 = (2 * i, 2 * i + 1) if inter else (i, i + rot // 2)
+    u, v = x.double()[..., i0], x.double()[..., i1]
+    y[..., i0] = u * c - v * s
+    y[..., i1] = v * c + u * s
+    size = torch.zeros_like(y)
+    size[..., i0] = size[..., i1] = (u.abs() + v.abs()) * abs(m)
+    return y, size
+
+
+def _check(got, want, size):
+    """fp32 arithmetic, then one rounding.  Per product: the sine or cosine within 2.4e-7 (two fp32 steps) plus the
+    angle's own rounding 2 pi 2^-26 = 1e-7, times m (2^-24); two products and a sum 3 x 2^-24: below 7e-7 of
+    m(|u| + |v|).  The rounding is half a step: eps/2 of the result (2^-25 below fp16's normal range)."""
+    eps = torch.finfo(got.dtype).eps / 2
+    slack = 7e-7 * size
+    bound = slack + (want.abs() + slack) * eps + (2.0 ** -25 if got.dtype == torch.float16 else 0.0)
+    assert ((got.double() - want).abs() <= bound).all(), ((got.double() - want).abs() - bound).max()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,H,Hk,D,rot,inter,dtype,pos64", [
+    (1, 1, 1, 64, 64, False, torch.bfloat16, False),
+    (5, 8, 2, 128, 128, False, torch.float16, True),
+    (33, 32, 8, 128, 64, True, torch.bfloat16, False),
+    (700, 12, 4, 128, 96, False, torch.float16, False),
+    (257, 6, 3, 80, 48, True, torch.float16, True),
+    (19, 3, 1, 72, 20, False, torch.bfloat16, False),     # no 16-byte path
+    (19, 3, 1, 7, 6, True, torch.bfloat16, True),         # odd head size
+    (4100, 40, 40, 128, 128, True, torch.bfloat16, False),
+])
+def test_rotation_against_the_formula(N, H, Hk, D, rot, inter, dtype, pos64):
+    torch.manual_seed(N)
+    q = torch.randn(N, H, D, device="cuda").to(dtype)
+    k = torch.randn(N, Hk, D, device="cuda").to(dtype)
+    pos = torch.randint(-5, 1_000_000, (N,), device="cuda", dtype=torch.int64 if pos64 else torch.int32)
+    f, m = kivi.rope_frequencies(rot, scaling="yarn", factor=16.0, original=4096.0)
+    for sign in (1.0, -1.0):
+        a, b = kivi.rope(q, k, pos, f, rotary_dim=rot, interleaved=inter, scale=m, inverse=sign < 0)
+        for x, y in ((q, a), (k, b)):
+            want, size = _want(x, pos, f, m, rot, inter, sign)
+            _check(y, want, size)
+            assert torch.equal(y[..., rot:], x[..., rot:])
+
+
+@pytest.mark.gpu
+def test_far_positions_are_exact_and_the_cache_convention_is_kept():
+    """Positions near 2^31: the angle is reduced exactly; fp32_angles gives the fp32 product's angle."""
+    f, _ = kivi.rope_frequencies(128)
+    q = torch.randn(64, 2, 128, device="cuda", dtype=torch.float16)
+    pos = torch.arange(64, device="cuda", dtype=torch.int64) + (2 ** 31 - 70)
+    a, _ = kivi.rope(q, None, pos, f)
+    want, size = _want(q, pos, f, 1.0, 128, False, 1.0)
+    # fp64 turns of 2^28.3 are within 2^-23.7 x 2^... = 2e-7 turns x 2 pi of the angle here: 5e-7 more per product.
+    assert ((a.double() - want).abs() <= 1.3e-6 * size + want.abs() * 2 ** -11 + 2.0 ** -25).all()
+    pos = torch.arange(64, device="cuda", dtype=torch.int32) * 13000
+    a, _ = kivi.rope(q, None, pos, f, fp32_angles=True)
+    want, size = _want(q, pos, f, 1.0, 128, False, 1.0, fp32_angles=True)
+    _check(a, want, size)
+    b, _ = kivi.rope(q, None, pos, f)
+    assert not torch.equal(a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("off", [0, 8, 1])
+def test_strides_and_in_place(off):
+    """Slices of one projection's output, aligned and not, in place and not; neighbours keep their values."""
+    N, H, Hk, D, rot = 37, 8, 2, 128, 64
+    buf = torch.randn(N, (H + 2 * Hk) * D + 16, device="cuda").to(torch.bfloat16)
+    view = lambda t, h0, h: t[:, off + h0 * D:off + (h0 + h) * D].unflatten(1, (h, D))  # noqa: E731
+    pos = torch.arange(N, device="cuda", dtype=torch.int32)
+    f, _ = kivi.rope_frequencies(rot)
+    q, k = view(buf, 0, H), view(buf, H, Hk)
+    a, b = kivi.rope(q, k, pos, f, rotary_dim=rot)
+    for x, y in ((q, a), (k, b)):
+        _check(y, *_want(x, pos, f, 1.0, rot, False, 1.0))
+    before = buf.clone()
+    kivi.rope(q, k, pos, f, rotary_dim=rot, q_out=q, k_out=k)
+    assert torch.equal(q, a) and torch.equal(k, b)
+    view(before, 0, H).copy_(a)
+    view(before, H, Hk).copy_(b)
+    assert torch.equal(buf, before)
+
+
+@pytest.mark.gpu
+def test_inverse_is_the_gradient():
+    """<dy, rope(x)> moves by <rope_inverse(dy), dx>: the rotation is linear, so a difference is its derivative."""
+    N, H, D, rot = 9, 2, 64, 32
+    f, m = kivi.rope_frequencies(rot, scaling="yarn", factor=4.0, original=64.0)
+    pos = torch.arange(N, device="cuda", dtype=torch.int32) * 17
+    x, dx, dy = (torch.randn(N, H, D, device="cuda", dtype=torch.float16) for _ in range(3))
+    for inter in (False, True):
+        kw = dict(rotary_dim=rot, interleaved=inter, scale=m)
+        g, _ = kivi.rope(dy, None, pos, f, inverse=True, **kw)
+        w, size = _want(dx, pos, f, m, rot, inter, 1.0)
+        lhs, rhs = (dy.double() * w).sum(), (g.double() * dx.double()).sum()
+        # g is rounded to fp16: half a step (2^-11) of each |g dx|, plus 7e-7 of the pair's magnitudes.
+        bound = (g.double().abs() * dx.double().abs()).sum() * 2 ** -11 + 7e-7 * (size * dy.double().abs()).sum() * 2
+        assert (lhs - rhs).abs() <= bound
+
+
+@pytest.mark.gpu
+def test_other_stream_graph_and_empty():
+    f, _ = kivi.rope_frequencies(64)
+    q = torch.randn(16, 4, 64, device="cuda", dtype=torch.bfloat16)
+    pos = torch.arange(16, device="cuda", dtype=torch.int32)
+    want, _ = kivi.rope(q, None, pos, f)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out = torch.empty_like(q)
+    kivi.rope(q, None, pos, f, q_out=out, stream=s)
+    s.synchronize()
+    assert torch.equal(out, want)
+    out.zero_()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kivi.rope(q, None, pos, f, q_out=out)
+    pos += 3
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, kivi.rope(q, None, pos, f)[0])
+    e, _ = kivi.rope(q[:0], None, pos[:0], f)
+    assert e.shape == (0, 4, 64)
+
+
+@pytest.mark.gpu
+def test_python_checks():
+    f, _ = kivi.rope_frequencies(64)
+    q = torch.randn(16, 4, 64, device="cuda", dtype=torch.bfloat16)
+    pos = torch.arange(16, device="cuda", dtype=torch.int32)
+    for bad in (lambda: kivi.rope(q.float(), None, pos, f), lambda: kivi.rope(q, None, pos.float(), f),
+                lambda: kivi.rope(q, None, pos[:8], f), lambda: kivi.rope(q, None, pos, f[:8]),
+                lambda: kivi.rope(q.transpose(1, 2), None, pos, f), lambda: kivi.rope(q, q[:8], pos, f),
+                lambda: kivi.rope(q, None, pos, f, q_out=q.half()), lambda: kivi.rope(q.cpu(), None, pos, f)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(kivi.KiviError):
+        kivi.rope(q, None, pos, f[:0], rotary_dim=0)
