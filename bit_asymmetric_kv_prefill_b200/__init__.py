@@ -16,6 +16,11 @@ calls raise if the library is missing.
     inv_freq, m = rope_frequencies(D, theta=10000.0)
     q, k = rope(q, k, positions, inv_freq, scale=m)   # [tokens, heads, D]
 
+    # sequences that share the pages of one pool, chunks of any length
+    pool = KiviPool(pages, sequences, H_kv, D, T_max=8192)
+    a, b = pool.open(2)
+    out = pool.attend([a, b], q, k, v, [n_a, n_b])    # rows of a, then of b
+    pool.extend([a, b], k, v, [n_a, n_b])
 
     # quantize-dequantize under another grouping (diagnostics, no cache)
     x_hat, sq_err = fake_quant(K, AXIS_PER_TOKEN, G=32, bits=2, symmetric=True)
@@ -68,6 +73,18 @@ class RopeTensor(ctypes.Structure):
                 ("y_token", ctypes.c_longlong), ("y_head", ctypes.c_longlong)]
 
 
+class PoolConfig(ctypes.Structure):
+    """kivi_pool_config"""
+    _fields_ = [("H_kv", ctypes.c_int), ("D", ctypes.c_int), ("G", ctypes.c_int), ("R", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("pages", ctypes.c_int), ("sequences", ctypes.c_int),
+                ("T_max", ctypes.c_longlong), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class PoolRows(ctypes.Structure):
+    """kivi_rows"""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong)]
+
+
 class RopeScaling(ctypes.Structure):
     """kivi_rope_scaling"""
     _fields_ = [("kind", ctypes.c_int), ("factor", ctypes.c_double), ("original", ctypes.c_double),
@@ -111,6 +128,28 @@ def lib():
                                          vp, vp, vp, vp]
     L.kivi_rope.argtypes = [P(RopeTensor), i32, i32, i64, i32, vp, i32, vp, i32, i32, ctypes.c_float, i32, i32, vp]
     L.kivi_rope_frequencies.argtypes = [i32, ctypes.c_double, P(RopeScaling), P(ctypes.c_float), P(ctypes.c_float)]
+    pi, pr = P(i32), P(PoolRows)
+    L.kivi_pool_required_bytes.argtypes = [P(PoolConfig), P(ctypes.c_size_t)]
+    L.kivi_pool_create.argtypes = [P(PoolConfig), P(vp)]
+    L.kivi_pool_destroy.argtypes = [vp]
+    L.kivi_pool_open.argtypes = [vp, i32, pi]
+    L.kivi_pool_free.argtypes = [vp, pi, i32]
+    L.kivi_pool_extend.argtypes = [vp, pi, pi, i32, pr, pr, vp]
+    L.kivi_pool_attn.argtypes = [vp, pi, pi, i32, pr, pr, pr, i32, vp, vp]
+    L.kivi_pool_gather.argtypes = [vp, pi, i32, vp, vp, vp]
+    L.kivi_pool_fork.argtypes = [vp, pi, i32, pi, vp]
+    L.kivi_pool_copy.argtypes = [vp, pi, i32, pi, vp]
+    L.kivi_pool_compact.argtypes = [vp, pi, vp]
+    L.kivi_pool_length.argtypes = [vp, i32, P(i64), pi]
+    L.kivi_pool_pages.argtypes = [vp, i32, pi, i32, pi]
+    L.kivi_pool_usage.argtypes = [vp, pi, pi, pi]
+    L.kivi_pool_device_status.argtypes = [vp, pi]
+    L.kivi_pool_export.argtypes = [vp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]
+    for name in ("kivi_pool_required_bytes", "kivi_pool_create", "kivi_pool_destroy", "kivi_pool_open",
+                 "kivi_pool_free", "kivi_pool_extend", "kivi_pool_attn", "kivi_pool_gather", "kivi_pool_fork",
+                 "kivi_pool_copy", "kivi_pool_compact", "kivi_pool_length", "kivi_pool_pages", "kivi_pool_usage",
+                 "kivi_pool_device_status", "kivi_pool_export"):
+        getattr(L, name).restype = st
     for name in ("kivi_rope", "kivi_rope_frequencies", "kivi_cache_create", "kivi_cache_create_ex", "kivi_cache_required_bytes",
                  "kivi_prefill", "kivi_prefill_ragged", "kivi_cache_length_at", "kivi_append", "kivi_decode_attn", "kivi_decode_attn_noalloc",
                  "kivi_append_decode",
@@ -414,4 +453,5 @@ def fake_quant_levels(x: torch.Tensor, axis: int, G: int, levels, values: bool =
 
 
 # The operators below use the loader and helpers above.
+from .pool import KiviPool  # noqa: E402
 from .rotary import rope, rope_frequencies  # noqa: E402

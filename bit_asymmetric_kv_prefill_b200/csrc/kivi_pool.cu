@@ -1,0 +1,699 @@
+// kivi_pool.cu -- the pool of pages (kivi_pool_*): argument checks, device
+// memory plan, page and sequence bookkeeping on the host, launches, and the
+// test-only export.
+//
+// A page is exactly one flush (R tokens of every kv head) and is never written
+// again, so sequences share pages by count and only the residual of a fork is
+// copied.  Page lists live on the host; the device table holds them for the
+// kernels and is updated by launches on the caller's stream, in order with the
+// calls that need it.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <functional>
+#include <memory>
+#include <new>
+#include <queue>
+#include <vector>
+
+#include <cuda_runtime.h>
+
+#include "../../include/kivi.h"
+#include "kivi_pool.cuh"
+
+using namespace kivi;
+
+namespace {
+
+constexpr size_t kAlign = 256;
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+
+struct PoolPlan {
+    int max_pages;
+    size_t off_packed, off_resK, off_resV, off_table, off_part, off_err, total;
+};
+
+struct PoolSeq {
+    bool open = false;
+    int r = 0;                // residual tokens
+    std::vector<int> pages;   // n_q = R * pages.size()
+};
+
+kivi_status check_pool_config(const kivi_pool_config *c)
+{
+    if (!c) return KIVI_ERR_ARG;
+    if (c->H_kv < 1 || c->D < 1 || c->G < 1 || c->R < 1 || c->T_max < 1 || c->pages < 0 || c->sequences < 1)
+        return KIVI_ERR_ARG;
+    if (c->dtype != KIVI_F16 && c->dtype != KIVI_BF16) return KIVI_ERR_ARG;
+    if (c->R % c->G != 0 || c->D % c->G != 0) return KIVI_ERR_ARG;
+    if (c->G != kG) return KIVI_ERR_UNSUPPORTED;
+    if (c->D != 64 && c->D != 128) return KIVI_ERR_UNSUPPORTED;
+    // Token and table indices are 32-bit in the kernels' tables.
+    if (c->T_max > (1LL << 30) || c->R > (1 << 20) || c->H_kv > 4096) return KIVI_ERR_UNSUPPORTED;
+    if ((c->T_max / c->R + 1) * (long long)c->sequences > (1LL << 30)) return KIVI_ERR_UNSUPPORTED;
+    return KIVI_OK;
+}
+
+void make_pool_plan(const kivi_pool_config *c, int sms, PoolPlan *p)
+{
+    p->max_pages = (int)((c->T_max - 1) / c->R + 1);
+    const size_t page = (size_t)c->H_kv * (c->R / kG) * 24 * c->D;
+    const size_t res = (size_t)c->sequences * c->H_kv * c->R * c->D * 2;
+    size_t off = 0;
+    p->off_packed = off;
+    off = align_up(off + page * c->pages);
+    p->off_resK = off;
+    off = align_up(off + res);
+    p->off_resV = off;
+    off = align_up(off + res);
+    p->off_table = off;
+    off = align_up(off + (size_t)c->sequences * p->max_pages * sizeof(int));
+    p->off_part = off;
+    off = align_up(off + pool_rows_scratch(c->D, sms) * sizeof(float));
+    p->off_err = off;
+    off = align_up(off + sizeof(int));
+    p->total = off;
+}
+
+// Tokens that stay in the residual when a sequence holds `total`.
+long long coded_tokens(long long total, int R) { return total > 0 ? R * ((total - 1) / R) : 0; }
+
+template <typename F>
+kivi_status guarded(F &&f)
+{
+    try {
+        return f();
+    } catch (...) {   // only std::bad_alloc can come: nothing was launched or changed before an allocation
+        return KIVI_ERR_OOM;
+    }
+}
+
+}  // namespace
+
+struct kivi_pool {
+    kivi_pool_config cfg;
+    PoolPlan plan;
+    int dev, sms;
+    unsigned char *base;
+    bool owns;
+    PoolView view;
+    float *part;
+    int *err;
+    std::vector<PoolSeq> seqs;
+    std::vector<int> refs;                                                    // sequences that hold each page
+    std::priority_queue<int, std::vector<int>, std::greater<int>> free_pages; // lowest first
+    std::vector<char> mark;                                                   // per sequence, for duplicate checks
+};
+
+namespace {
+
+bool on_pool_device(const kivi_pool *p)
+{
+    int d = -1;
+    return cudaGetDevice(&d) == cudaSuccess && d == p->dev;
+}
+
+bool is_open(const kivi_pool *p, int s) { return s >= 0 && s < (int)p->seqs.size() && p->seqs[s].open; }
+
+// All open, and (unless repeats are fine) no sequence twice.
+kivi_status check_seqs(kivi_pool *p, const int *seqs, int n, bool repeats)
+{
+    if (n < 0 || (n > 0 && !seqs)) return KIVI_ERR_ARG;
+    for (int i = 0; i < n; ++i)
+        if (!is_open(p, seqs[i])) return KIVI_ERR_ARG;
+    if (!repeats) {
+        bool twice = false;
+        for (int i = 0; i < n; ++i) {
+            twice = twice || p->mark[seqs[i]];
+            p->mark[seqs[i]] = 1;
+        }
+        for (int i = 0; i < n; ++i) p->mark[seqs[i]] = 0;
+        if (twice) return KIVI_ERR_ARG;
+    }
+    return KIVI_OK;
+}
+
+bool good_rows(const kivi_rows *r)
+{
+    return r && r->data && aligned16(r->data) && r->token_stride % 8 == 0 && r->head_stride % 8 == 0;
+}
+Rows rows_of(const kivi_rows *r) { return Rows{(const uint16_t *)r->data, r->token_stride, r->head_stride}; }
+
+// n sequence slots that are not open (empty: too few).
+std::vector<int> free_slots(const kivi_pool *p, int n)
+{
+    std::vector<int> s;
+    for (int i = 0; i < (int)p->seqs.size() && (int)s.size() < n; ++i)
+        if (!p->seqs[i].open) s.push_back(i);
+    if ((int)s.size() < n) s.clear();
+    return s;
+}
+
+// Table and move launches take kPoolMaxPairs entries each.
+cudaError_t launch_pairs(const kivi_pool *p, const std::vector<int> &a, const std::vector<int> &b, bool moves,
+                         cudaStream_t st)
+{
+    auto t = std::make_unique<PairTab>();
+    for (size_t i = 0; i < a.size(); i += kPoolMaxPairs) {
+        t->n = (int)std::min(a.size() - i, (size_t)kPoolMaxPairs);
+        std::copy_n(a.begin() + i, t->n, t->a);
+        std::copy_n(b.begin() + i, t->n, t->b);
+        const cudaError_t e = moves ? launch_pool_move(p->view, *t, st) : launch_pool_table(p->view, *t, st);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+void release_page(kivi_pool *p, int page)
+{
+    if (--p->refs[page] == 0) p->free_pages.push(page);   // capacity reserved at creation
+}
+
+}  // namespace
+
+extern "C" {
+
+kivi_status kivi_pool_required_bytes(const kivi_pool_config *cfg, size_t *bytes)
+{
+    const kivi_status st = check_pool_config(cfg);
+    if (st != KIVI_OK) return st;
+    if (!bytes) return KIVI_ERR_ARG;
+    PoolPlan p;
+    make_pool_plan(cfg, num_sms(), &p);
+    *bytes = p.total;
+    return KIVI_OK;
+}
+
+kivi_status kivi_pool_create(const kivi_pool_config *cfg, kivi_pool **out)
+{
+    const kivi_status st = check_pool_config(cfg);
+    if (st != KIVI_OK) return st;
+    if (!out) return KIVI_ERR_ARG;
+    *out = nullptr;
+    return guarded([&]() -> kivi_status {
+        auto p = std::make_unique<kivi_pool>();
+        p->cfg = *cfg;
+        p->owns = false;
+        if (cudaGetDevice(&p->dev) != cudaSuccess) return KIVI_ERR_CUDA;
+        p->sms = num_sms();
+        make_pool_plan(cfg, p->sms, &p->plan);
+        p->seqs.resize(cfg->sequences);
+        for (PoolSeq &s : p->seqs) s.pages.reserve(std::min(p->plan.max_pages, 64));
+        p->refs.assign(cfg->pages, 0);
+        p->mark.assign(cfg->sequences, 0);
+        std::vector<int> ids(cfg->pages);
+        for (int i = 0; i < cfg->pages; ++i) ids[i] = i;
+        p->free_pages = decltype(p->free_pages)(std::greater<int>(), std::move(ids));
+        if (cfg->workspace) {
+            if (cfg->workspace_bytes < p->plan.total) return KIVI_ERR_OOM;
+            if ((uintptr_t)cfg->workspace % kAlign != 0) return KIVI_ERR_ARG;
+            p->base = (unsigned char *)cfg->workspace;
+        } else {
+            if (cudaMalloc(&p->base, p->plan.total) != cudaSuccess) {
+                cudaGetLastError();
+                return KIVI_ERR_OOM;
+            }
+            p->owns = true;
+        }
+        p->view.packed = p->base + p->plan.off_packed;
+        p->view.resK = (uint16_t *)(p->base + p->plan.off_resK);
+        p->view.resV = (uint16_t *)(p->base + p->plan.off_resV);
+        p->view.table = (int *)(p->base + p->plan.off_table);
+        p->view.H = cfg->H_kv;
+        p->view.R = cfg->R;
+        p->view.gpp = cfg->R / kG;
+        p->view.max_pages = p->plan.max_pages;
+        p->view.D = cfg->D;
+        p->view.dtype = cfg->dtype;
+        p->part = (float *)(p->base + p->plan.off_part);
+        p->err = (int *)(p->base + p->plan.off_err);
+        cudaError_t e = cudaMemset(p->view.table, 0, (size_t)cfg->sequences * p->plan.max_pages * sizeof(int));
+        if (e == cudaSuccess) e = cudaMemset(p->err, 0, sizeof(int));
+        if (e == cudaSuccess) e = cudaDeviceSynchronize();
+        if (e != cudaSuccess) {
+            if (p->owns) cudaFree(p->base);
+            return KIVI_ERR_CUDA;
+        }
+        *out = p.release();
+        return KIVI_OK;
+    });
+}
+
+kivi_status kivi_pool_destroy(kivi_pool *p)
+{
+    if (!p) return KIVI_ERR_ARG;
+    cudaError_t e = cudaSuccess;
+    if (p->owns) e = cudaFree(p->base);
+    delete p;
+    return cuda_status(e);
+}
+
+kivi_status kivi_pool_open(kivi_pool *p, int n, int *seqs)
+{
+    if (!p || n < 0 || (n > 0 && !seqs)) return KIVI_ERR_ARG;
+    return guarded([&]() -> kivi_status {
+        const std::vector<int> s = free_slots(p, n);
+        if ((int)s.size() != n) return KIVI_ERR_CAPACITY;
+        for (int i = 0; i < n; ++i) {
+            p->seqs[s[i]].open = true;
+            p->seqs[s[i]].r = 0;
+            p->seqs[s[i]].pages.clear();
+            seqs[i] = s[i];
+        }
+        return KIVI_OK;
+    });
+}
+
+kivi_status kivi_pool_free(kivi_pool *p, const int *seqs, int n)
+{
+    if (!p) return KIVI_ERR_ARG;
+    const kivi_status st = check_seqs(p, seqs, n, false);
+    if (st != KIVI_OK) return st;
+    for (int i = 0; i < n; ++i) {
+        PoolSeq &s = p->seqs[seqs[i]];
+        for (const int page : s.pages) release_page(p, page);
+        s.pages.clear();
+        s.r = 0;
+        s.open = false;
+    }
+    return KIVI_OK;
+}
+
+kivi_status kivi_pool_length(const kivi_pool *p, int seq, long long *n_q, int *r)
+{
+    if (!p || !n_q || !r || !is_open(p, seq)) return KIVI_ERR_ARG;
+    *n_q = (long long)p->seqs[seq].pages.size() * p->cfg.R;
+    *r = p->seqs[seq].r;
+    return KIVI_OK;
+}
+
+kivi_status kivi_pool_pages(const kivi_pool *p, int seq, int *pages, int capacity, int *n)
+{
+    if (!p || !n || capacity < 0 || !is_open(p, seq)) return KIVI_ERR_ARG;
+    const std::vector<int> &v = p->seqs[seq].pages;
+    *n = (int)v.size();
+    if (pages) {
+        if (capacity < *n) return KIVI_ERR_CAPACITY;
+        std::copy(v.begin(), v.end(), pages);
+    }
+    return KIVI_OK;
+}
+
+kivi_status kivi_pool_usage(const kivi_pool *p, int *pages_used, int *pages_end, int *sequences_open)
+{
+    if (!p || !pages_used || !pages_end || !sequences_open) return KIVI_ERR_ARG;
+    *pages_used = *pages_end = *sequences_open = 0;
+    for (int i = 0; i < (int)p->refs.size(); ++i)
+        if (p->refs[i] > 0) {
+            ++*pages_used;
+            *pages_end = i + 1;
+        }
+    for (const PoolSeq &s : p->seqs) *sequences_open += s.open;
+    return KIVI_OK;
+}
+
+kivi_status kivi_pool_extend(kivi_pool *p, const int *seqs, const int *n_new, int n, const kivi_rows *k,
+                             const kivi_rows *v, void *stream)
+{
+    if (!p || n < 0 || (n > 0 && (!seqs || !n_new))) return KIVI_ERR_ARG;
+    if (!on_pool_device(p)) return KIVI_ERR_ARG;
+    if (n > kPoolMaxBatch) return KIVI_ERR_UNSUPPORTED;
+    kivi_status st = check_seqs(p, seqs, n, false);
+    if (st != KIVI_OK) return st;
+    long long total = 0;
+    for (int i = 0; i < n; ++i) {
+        if (n_new[i] < 0) return KIVI_ERR_ARG;
+        total += n_new[i];
+    }
+    if (total > 0 && (!good_rows(k) || !good_rows(v))) return KIVI_ERR_ARG;
+    if (total > (1LL << 30)) return KIVI_ERR_UNSUPPORTED;
+    return guarded([&]() -> kivi_status {
+        const int R = p->cfg.R, H = p->cfg.H_kv;
+        auto t = std::make_unique<ExtendTab>();
+        t->nb = n;
+        t->item[0] = t->kept[0] = 0;
+        std::vector<int> fresh, at, ids;   // new pages, their table entries
+        long long need = 0, items = 0;
+        int row = 0;
+        for (int i = 0; i < n; ++i) {
+            const PoolSeq &s = p->seqs[seqs[i]];
+            const long long n_q = (long long)s.pages.size() * R, len = n_q + s.r + n_new[i];
+            if (len > p->cfg.T_max) return KIVI_ERR_CAPACITY;
+            const long long coded = std::max(n_q, coded_tokens(len, R));
+            const int grown = (int)((coded - n_q) / R);
+            t->seq[i] = seqs[i];
+            t->row0[i] = row;
+            t->r[i] = s.r;
+            t->g0[i] = (int)(n_q / kG);
+            // Kept: everything behind the coded tokens.  A flush takes the
+            // whole residual with it, so what is kept then is new rows only.
+            t->from[i] = grown ? (int)(coded - n_q - s.r) : 0;
+            t->slot0[i] = grown ? 0 : s.r;
+            items += (long long)grown * (R / kG) * H;
+            if (items > (1LL << 29)) return KIVI_ERR_UNSUPPORTED;
+            t->item[i + 1] = (int)items;
+            t->kept[i + 1] = t->kept[i] + n_new[i] - t->from[i];
+            row += n_new[i];
+            need += grown;
+            for (int j = 0; j < grown; ++j) at.push_back(seqs[i] * p->view.max_pages + (int)s.pages.size() + j);
+        }
+        if (need > (long long)p->free_pages.size()) return KIVI_ERR_CAPACITY;
+        for (int i = 0; i < n; ++i) {   // every allocation before anything changes
+            PoolSeq &s = p->seqs[seqs[i]];
+            s.pages.reserve(s.pages.size() + (t->item[i + 1] - t->item[i]) / (R / kG * H));
+        }
+        fresh.reserve(need);
+        auto tab = std::make_unique<PairTab>();
+        for (long long j = 0; j < need; ++j) {
+            fresh.push_back(p->free_pages.top());
+            p->free_pages.pop();
+        }
+        cudaError_t e = cudaSuccess;
+        const cudaStream_t cs = (cudaStream_t)stream;
+        for (size_t i = 0; i < at.size() && e == cudaSuccess; i += kPoolMaxPairs) {
+            tab->n = (int)std::min(at.size() - i, (size_t)kPoolMaxPairs);
+            std::copy_n(at.begin() + i, tab->n, tab->a);
+            std::copy_n(fresh.begin() + i, tab->n, tab->b);
+            e = launch_pool_table(p->view, *tab, cs);
+        }
+        if (total > 0 && e == cudaSuccess) e = launch_pool_quant(p->view, rows_of(k), rows_of(v), *t, cs);
+        // The residual is overwritten by a launch of its own: the quantizer's
+        // warps read it.
+        if (total > 0 && e == cudaSuccess) e = launch_pool_keep(p->view, rows_of(k), rows_of(v), *t, cs);
+        if (e != cudaSuccess) {
+            for (const int page : fresh) p->free_pages.push(page);
+            return KIVI_ERR_CUDA;
+        }
+        size_t j = 0;
+        for (int i = 0; i < n; ++i) {
+            PoolSeq &s = p->seqs[seqs[i]];
+            const int grown = (t->item[i + 1] - t->item[i]) / (R / kG * H);
+            for (int q = 0; q < grown; ++q, ++j) {
+                s.pages.push_back(fresh[j]);
+                p->refs[fresh[j]] = 1;
+            }
+            s.r = grown ? n_new[i] - t->from[i] : s.r + n_new[i];
+        }
+        return KIVI_OK;
+    });
+}
+
+kivi_status kivi_pool_attn(kivi_pool *p, const int *seqs, const int *n_new, int n, const kivi_rows *q,
+                           const kivi_rows *k, const kivi_rows *v, int H_q, void *out, void *stream)
+{
+    if (!p || n < 0 || (n > 0 && (!seqs || !n_new))) return KIVI_ERR_ARG;
+    if (!on_pool_device(p)) return KIVI_ERR_ARG;
+    if (H_q < 1 || H_q % p->cfg.H_kv != 0) return KIVI_ERR_ARG;
+    if ((k == nullptr) != (v == nullptr)) return KIVI_ERR_ARG;
+    if (n > kPoolMaxBatch || H_q > 65536) return KIVI_ERR_UNSUPPORTED;
+    const kivi_status st = check_seqs(p, seqs, n, true);
+    if (st != KIVI_OK) return st;
+    long long total = 0;
+    for (int i = 0; i < n; ++i) {
+        if (n_new[i] < 0) return KIVI_ERR_ARG;
+        total += n_new[i];
+    }
+    if (total == 0) return KIVI_OK;
+    if (total > (1LL << 30) / (H_q / p->cfg.H_kv)) return KIVI_ERR_UNSUPPORTED;
+    if (!good_rows(q) || (k && (!good_rows(k) || !good_rows(v))) || !out || !aligned16(out)) return KIVI_ERR_ARG;
+    return guarded([&]() -> kivi_status {
+        auto t = std::make_unique<AttnTab>();
+        t->nb = n;
+        int row = 0;
+        for (int i = 0; i < n; ++i) {
+            const PoolSeq &s = p->seqs[seqs[i]];
+            t->seq[i] = seqs[i];
+            t->row0[i] = row;
+            t->n[i] = n_new[i];
+            t->nk[i] = k ? n_new[i] : 0;
+            t->ng[i] = (int)(s.pages.size() * (p->cfg.R / kG));
+            t->r[i] = s.r;
+            row += n_new[i];
+        }
+        AttnCall c;
+        c.v = p->view;
+        c.q = rows_of(q);
+        c.k = k ? rows_of(k) : Rows{nullptr, 0, 0};
+        c.nv = v ? rows_of(v) : Rows{nullptr, 0, 0};
+        c.out = (uint16_t *)out;
+        c.H_q = H_q;
+        c.group = H_q / p->cfg.H_kv;
+        c.scale = (float)(1.4426950408889634 / std::sqrt((double)p->cfg.D));
+        c.part = p->part;
+        c.err = p->err;
+        return cuda_status(launch_pool_rows(c, *t, p->sms, (cudaStream_t)stream));
+    });
+}
+
+kivi_status kivi_pool_gather(kivi_pool *p, const int *seqs, int n, void *K, void *V, void *stream)
+{
+    if (!p || n < 0 || (n > 0 && !seqs)) return KIVI_ERR_ARG;
+    if (!on_pool_device(p)) return KIVI_ERR_ARG;
+    if (n > kPoolMaxBatch) return KIVI_ERR_UNSUPPORTED;
+    const kivi_status st = check_seqs(p, seqs, n, true);
+    if (st != KIVI_OK) return st;
+    return guarded([&]() -> kivi_status {
+        auto t = std::make_unique<GatherTab>();
+        t->nb = n;
+        t->item[0] = 0;
+        long long row = 0, items = 0;
+        for (int i = 0; i < n; ++i) {
+            const PoolSeq &s = p->seqs[seqs[i]];
+            t->seq[i] = seqs[i];
+            t->row0[i] = (int)row;
+            t->ng[i] = (int)(s.pages.size() * (p->cfg.R / kG));
+            t->r[i] = s.r;
+            row += (long long)s.pages.size() * p->cfg.R + s.r;
+            items += (long long)(t->ng[i] + (s.r + 31) / 32) * p->cfg.H_kv;
+            if (row > (1LL << 30) || items > (1LL << 30)) return KIVI_ERR_UNSUPPORTED;
+            t->item[i + 1] = (int)items;
+        }
+        if (row == 0) return KIVI_OK;
+        if (!K || !V || !aligned16(K) || !aligned16(V)) return KIVI_ERR_ARG;
+        return cuda_status(launch_pool_gather(p->view, *t, (uint16_t *)K, (uint16_t *)V, (cudaStream_t)stream));
+    });
+}
+
+// Fork (share pages) or copy (own pages) n sequences into new ones.
+static kivi_status branch(kivi_pool *p, const int *src, int n, int *dst, bool own, void *stream)
+{
+    if (!p || n < 0 || (n > 0 && (!src || !dst))) return KIVI_ERR_ARG;
+    if (!on_pool_device(p)) return KIVI_ERR_ARG;
+    if (n > kPoolMaxBatch) return KIVI_ERR_UNSUPPORTED;
+    const kivi_status st = check_seqs(p, src, n, true);
+    if (st != KIVI_OK) return st;
+    if (n == 0) return KIVI_OK;
+    return guarded([&]() -> kivi_status {
+        const std::vector<int> slots = free_slots(p, n);
+        if ((int)slots.size() != n) return KIVI_ERR_CAPACITY;
+        auto t = std::make_unique<ForkTab>();
+        t->n = n;
+        size_t need = 0;
+        for (int i = 0; i < n; ++i) {
+            const PoolSeq &s = p->seqs[src[i]];
+            t->src[i] = src[i];
+            t->dst[i] = slots[i];
+            t->np[i] = own ? 0 : (int)s.pages.size();
+            t->r[i] = s.r;
+            if (own) need += s.pages.size();
+            p->seqs[slots[i]].pages.reserve(s.pages.size());
+        }
+        if (need > p->free_pages.size()) return KIVI_ERR_CAPACITY;
+        std::vector<int> from, to, at;
+        from.reserve(need);
+        to.reserve(need);
+        at.reserve(need);
+        auto tab = std::make_unique<PairTab>();
+        if (own)
+            for (int i = 0; i < n; ++i) {
+                const PoolSeq &s = p->seqs[src[i]];
+                for (size_t j = 0; j < s.pages.size(); ++j) {
+                    from.push_back(s.pages[j]);
+                    to.push_back(p->free_pages.top());
+                    p->free_pages.pop();
+                    at.push_back(slots[i] * p->view.max_pages + (int)j);
+                }
+            }
+        const cudaStream_t cs = (cudaStream_t)stream;
+        cudaError_t e = launch_pool_fork(p->view, *t, cs);
+        for (size_t i = 0; i < need && e == cudaSuccess; i += kPoolMaxPairs) {
+            tab->n = (int)std::min(need - i, (size_t)kPoolMaxPairs);
+            std::copy_n(at.begin() + i, tab->n, tab->a);
+            std::copy_n(to.begin() + i, tab->n, tab->b);
+            e = launch_pool_table(p->view, *tab, cs);
+            if (e != cudaSuccess) break;
+            std::copy_n(from.begin() + i, tab->n, tab->a);
+            e = launch_pool_move(p->view, *tab, cs);
+        }
+        if (e != cudaSuccess) {
+            for (const int page : to) p->free_pages.push(page);
+            return KIVI_ERR_CUDA;
+        }
+        size_t j = 0;
+        for (int i = 0; i < n; ++i) {
+            const PoolSeq &s = p->seqs[src[i]];
+            PoolSeq &d = p->seqs[slots[i]];
+            d.open = true;
+            d.r = s.r;
+            d.pages.clear();
+            for (const int page : s.pages) {
+                const int mine = own ? to[j++] : page;
+                d.pages.push_back(mine);
+                ++p->refs[mine];
+            }
+            dst[i] = slots[i];
+        }
+        return KIVI_OK;
+    });
+}
+
+kivi_status kivi_pool_fork(kivi_pool *p, const int *src, int n, int *dst, void *stream)
+{
+    return branch(p, src, n, dst, false, stream);
+}
+
+kivi_status kivi_pool_copy(kivi_pool *p, const int *src, int n, int *dst, void *stream)
+{
+    return branch(p, src, n, dst, true, stream);
+}
+
+kivi_status kivi_pool_compact(kivi_pool *p, int *moved, void *stream)
+{
+    if (!p) return KIVI_ERR_ARG;
+    if (!on_pool_device(p)) return KIVI_ERR_ARG;
+    return guarded([&]() -> kivi_status {
+        const int P = (int)p->refs.size();
+        int live = 0;
+        for (int i = 0; i < P; ++i) live += p->refs[i] > 0;
+        // Live pages behind the first `live` go to the holes among them, in order.
+        std::vector<int> from, to, at, page, where(P, -1);
+        for (int i = live, hole = 0; i < P; ++i)
+            if (p->refs[i] > 0) {
+                while (p->refs[hole] > 0) ++hole;
+                from.push_back(i);
+                to.push_back(hole);
+                where[i] = hole++;
+            }
+        if (moved) *moved = (int)from.size();
+        if (from.empty()) return KIVI_OK;
+        for (int s = 0; s < (int)p->seqs.size(); ++s)
+            for (size_t j = 0; j < p->seqs[s].pages.size(); ++j)
+                if (where[p->seqs[s].pages[j]] >= 0) {
+                    at.push_back(s * p->view.max_pages + (int)j);
+                    page.push_back(where[p->seqs[s].pages[j]]);
+                }
+        std::vector<int> ids;
+        ids.reserve(P);
+        for (int i = live; i < P; ++i) ids.push_back(i);
+        const cudaStream_t cs = (cudaStream_t)stream;
+        cudaError_t e = launch_pairs(p, from, to, true, cs);
+        if (e == cudaSuccess) e = launch_pairs(p, at, page, false, cs);
+        if (e != cudaSuccess) return KIVI_ERR_CUDA;
+        for (size_t i = 0; i < from.size(); ++i) {
+            p->refs[to[i]] = p->refs[from[i]];
+            p->refs[from[i]] = 0;
+        }
+        for (PoolSeq &s : p->seqs)
+            for (int &x : s.pages)
+                if (where[x] >= 0) x = where[x];
+        p->free_pages = decltype(p->free_pages)(std::greater<int>(), std::move(ids));
+        return KIVI_OK;
+    });
+}
+
+kivi_status kivi_pool_device_status(kivi_pool *p, int *code)
+{
+    if (!p || !code) return KIVI_ERR_ARG;
+    if (!on_pool_device(p)) return KIVI_ERR_ARG;
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e == cudaSuccess) e = cudaMemcpy(code, p->err, sizeof(int), cudaMemcpyDeviceToHost);
+    if (e == cudaSuccess && *code != 0) {
+        e = cudaMemset(p->err, 0, sizeof(int));
+        if (e == cudaSuccess) e = cudaDeviceSynchronize();
+    }
+    return cuda_status(e);
+}
+
+}  // extern "C"
+
+namespace {
+
+template <int D>
+void unpack_page_group(const uint8_t *b, int t0, uint8_t *codesK, uint8_t *codesV, uint16_t *sK, uint16_t *zK,
+                       uint16_t *sV, uint16_t *zV)
+{
+    using L = PageLayout<D>;
+    for (int lane = 0; lane < 32; ++lane) {
+        const int tq = lane >> 2, cs = lane & 3;
+        for (int x = 0; x < L::WPL; ++x) {
+            uint32_t kw, vw;
+            std::memcpy(&kw, b + L::KC + code_word_offset(lane, x), 4);
+            std::memcpy(&vw, b + L::VC + code_word_offset(lane, x), 4);
+            const int j = x / L::KW, w = x % L::KW;
+            for (int i = 0; i < 8; ++i) {
+                const int tk = t0 + tq + 8 * j, dk = 64 * w + 32 * (i / 4) + 8 * cs + 2 * (i % 4);
+                if (codesK) {
+                    codesK[(long long)tk * D + dk] = (kw >> (2 * i)) & 3u;
+                    codesK[(long long)tk * D + dk + 1] = (kw >> (16 + 2 * i)) & 3u;
+                }
+                const int tv = t0 + 8 * j + 2 * cs, dv = 8 * (8 * w + i) + tq;
+                if (codesV) {
+                    codesV[(long long)tv * D + dv] = (vw >> (2 * i)) & 3u;
+                    codesV[(long long)(tv + 1) * D + dv] = (vw >> (16 + 2 * i)) & 3u;
+                }
+            }
+        }
+    }
+    if (sK) std::memcpy(sK + (long long)t0 / kG * D, b + L::KS, 2 * D);
+    if (zK) std::memcpy(zK + (long long)t0 / kG * D, b + L::KZ, 2 * D);
+    for (int p = 0; p < 4; ++p)
+        for (int cs = 0; cs < 4; ++cs)
+            for (int j = 0; j < L::NJ; ++j) {
+                uint16_t x[4];
+                std::memcpy(x, b + L::VM + page_vm_offset<D>(p, cs, j), 8);
+                for (int k = 0; k < 2; ++k) {
+                    const long long at = (long long)(t0 + 8 * p + 2 * cs + k) * L::NJ + j;
+                    if (sV) sV[at] = x[k];
+                    if (zV) zV[at] = x[2 + k];
+                }
+            }
+}
+
+}  // namespace
+
+extern "C" kivi_status kivi_pool_export(const kivi_pool *p, int seq, int head, uint8_t *codesK, uint8_t *codesV,
+                                        uint16_t *sK, uint16_t *zK, uint16_t *sV, uint16_t *zV, void *resK, void *resV)
+{
+    if (!p || !is_open(p, seq) || head < 0 || head >= p->cfg.H_kv) return KIVI_ERR_ARG;
+    return guarded([&]() -> kivi_status {
+        if (cudaDeviceSynchronize() != cudaSuccess) return KIVI_ERR_CUDA;
+        const PoolSeq &s = p->seqs[seq];
+        const int D = p->cfg.D, R = p->cfg.R, gpp = R / kG;
+        const size_t gb = (size_t)24 * D, part = gb * gpp;
+        std::vector<uint8_t> buf(part);
+        std::vector<int> table(s.pages.size());
+        if (!table.empty()
+            && cudaMemcpy(table.data(), p->view.table + (size_t)seq * p->view.max_pages, table.size() * sizeof(int),
+                          cudaMemcpyDeviceToHost) != cudaSuccess)
+            return KIVI_ERR_CUDA;
+        if (table != s.pages) return KIVI_ERR_STATE;   // the device table and the host's list agree
+        for (size_t i = 0; i < s.pages.size(); ++i) {
+            if (cudaMemcpy(buf.data(), p->view.packed + ((size_t)s.pages[i] * p->cfg.H_kv + head) * part, part,
+                           cudaMemcpyDeviceToHost)
+                != cudaSuccess)
+                return KIVI_ERR_CUDA;
+            for (int g = 0; g < gpp; ++g) {
+                const int t0 = (int)(i * R) + g * kG;
+                if (D == 64) unpack_page_group<64>(buf.data() + g * gb, t0, codesK, codesV, sK, zK, sV, zV);
+                else unpack_page_group<128>(buf.data() + g * gb, t0, codesK, codesV, sK, zK, sV, zV);
+            }
+        }
+        const size_t off = ((size_t)seq * p->cfg.H_kv + head) * R * D, bytes = (size_t)s.r * D * 2;
+        if (resK && bytes && cudaMemcpy(resK, p->view.resK + off, bytes, cudaMemcpyDeviceToHost) != cudaSuccess)
+            return KIVI_ERR_CUDA;
+        if (resV && bytes && cudaMemcpy(resV, p->view.resV + off, bytes, cudaMemcpyDeviceToHost) != cudaSuccess)
+            return KIVI_ERR_CUDA;
+        return KIVI_OK;
+    });
+}

@@ -1,0 +1,130 @@
+// kivi_pool.cuh -- layout of a pool's pages and the launch interface of its
+// kernels.  Internal to the library.
+//
+// A page holds R tokens of every kv head: [H_kv][R/32] group blocks of 24*D
+// bytes.  The blocks have the sizes of the contiguous cache's, but their codes
+// are ordered for the matrix instructions that read them (m16n8k16 fragments:
+// lane l = 4*tq + cs holds column tq and the k indices of cs):
+//
+//   [0,    8D)  K codes.  Lane 4*tq + cs holds tokens tq + 8j (j < 4) and the
+//               channels {32u + 8cs + 0..7}: word j*(D/64) + w covers
+//               u = 2w, 2w + 1; pair i = 4(u - 2w) + p is channels
+//               32u + 8cs + 2p and the next one.
+//   [8D,  10D)  K scales, channel order.      [10D, 12D)  K zeros.
+//   [12D, 20D)  V codes.  Lane 4*n + cs holds channels 8c + n (c < D/8) of the
+//               token pairs 8p + 2cs, 8p + 2cs + 1 (p < 4): word
+//               p*(D/64) + c/8, pair i = c % 8 (the pair's halves are the two
+//               tokens).
+//   [20D, 24D)  V scales and zeros: for token pair (p, cs) and channel group
+//               j < D/32 the scales of its two tokens, then their zeros, 8
+//               bytes at (((p*(D/64) + j/2)*4 + cs)*2 + j%2)*8.
+//
+// Words hold 8 code pairs as in the contiguous cache (pair i at bits 2i and
+// 16 + 2i) and are stored [word/4][lane][word%4].
+#pragma once
+
+#include "kivi_common.cuh"
+#include "kivi_internal.h"
+
+namespace kivi {
+
+template <int D>
+struct PageLayout {
+    static constexpr int GB = 24 * D;
+    static constexpr int KC = 0, KS = 8 * D, KZ = 10 * D, VC = 12 * D, VM = 20 * D;
+    static constexpr int WPL = D / 16;   // code words per lane (K or V)
+    static constexpr int KW = D / 64;    // K words per token, V words per token pair
+    static constexpr int NJ = D / kG;    // value groups per token
+};
+
+// Byte offset in VM of the scales (zeros: + 4) of token pair (p, cs), group j.
+template <int D>
+__host__ __device__ inline int page_vm_offset(int p, int cs, int j)
+{
+    return (((p * (D / 64) + j / 2) * 4 + cs) * 2 + j % 2) * 8;
+}
+
+constexpr int kPoolMaxBatch = 512;    // sequences per call
+constexpr int kPoolMaxPairs = 1024;   // entries of one table or copy launch
+
+// The pool's device memory, as kernels see it.
+struct PoolView {
+    uint8_t *packed;        // [pages][H][R/32][24*D]
+    uint16_t *resK, *resV;  // [sequences][H][R][D]
+    int *table;             // [sequences][max_pages]: page of tokens [i*R, i*R + R)
+    int H, R, gpp;          // gpp = R/32 groups per page
+    int max_pages;
+    int D, dtype;
+};
+
+// Rows [token][head] of 16-bit elements, D contiguous.
+struct Rows {
+    const uint16_t *p;
+    long long ts, hs;
+};
+
+// kivi_pool_extend: entry e quantizes the groups [g0, g0 + ng) of its sequence
+// (the first r of their tokens from the residual, the others new rows row0..),
+// then keeps `keep` new rows from `from` in residual slots slot0...
+struct ExtendTab {
+    int nb;
+    int seq[kPoolMaxBatch], row0[kPoolMaxBatch], r[kPoolMaxBatch], g0[kPoolMaxBatch];
+    int from[kPoolMaxBatch], slot0[kPoolMaxBatch];
+    int item[kPoolMaxBatch + 1];   // first (group, head) item of each entry
+    int kept[kPoolMaxBatch + 1];   // first kept row of each entry
+};
+
+// kivi_pool_gather: entry e reads ng groups and r residual tokens into rows
+// row0.. of the output; items are (32 tokens, head).
+struct GatherTab {
+    int nb;
+    int seq[kPoolMaxBatch], row0[kPoolMaxBatch], ng[kPoolMaxBatch], r[kPoolMaxBatch];
+    int item[kPoolMaxBatch + 1];
+};
+
+// Pairs of integers: (table index, page), (page from, page to).
+struct PairTab {
+    int n;
+    int a[kPoolMaxPairs], b[kPoolMaxPairs];
+};
+
+// kivi_pool_fork, kivi_pool_copy: np table entries and r residual tokens of
+// sequence src go to sequence dst.
+struct ForkTab {
+    int n;
+    int src[kPoolMaxBatch], dst[kPoolMaxBatch], np[kPoolMaxBatch], r[kPoolMaxBatch];
+};
+
+// kivi_pool_attn: entry e has n new rows from row0 and sees ng cached groups,
+// r residual tokens and nk of its new keys.  off: where each entry's work
+// starts in the flattened split (see kivi_pool_rows.cu).
+struct AttnTab {
+    int nb;
+    int seq[kPoolMaxBatch], row0[kPoolMaxBatch], n[kPoolMaxBatch], nk[kPoolMaxBatch], ng[kPoolMaxBatch],
+        r[kPoolMaxBatch];
+    long long off[kPoolMaxBatch + 1];
+};
+
+struct AttnCall {
+    PoolView v;
+    Rows q, k, nv;
+    uint16_t *out;        // [rows][H_q][D]
+    int H_q, group;       // group = H_q / H
+    float scale;          // log2(e) / sqrt(D)
+    float *part;          // partial results (attention scratch of the pool)
+    int *err;             // status word
+    long long warps;      // warps of the split
+};
+
+cudaError_t launch_pool_quant(const PoolView &v, const Rows &k, const Rows &nv, const ExtendTab &t, cudaStream_t st);
+cudaError_t launch_pool_keep(const PoolView &v, const Rows &k, const Rows &nv, const ExtendTab &t, cudaStream_t st);
+cudaError_t launch_pool_gather(const PoolView &v, const GatherTab &t, uint16_t *K, uint16_t *V, cudaStream_t st);
+cudaError_t launch_pool_table(const PoolView &v, const PairTab &t, cudaStream_t st);
+cudaError_t launch_pool_move(const PoolView &v, const PairTab &t, cudaStream_t st);
+cudaError_t launch_pool_fork(const PoolView &v, const ForkTab &t, cudaStream_t st);
+
+// Floats of attention scratch for a device of `sms` SMs.
+size_t pool_rows_scratch(int D, int sms);
+cudaError_t launch_pool_rows(AttnCall &c, AttnTab &t, int sms, cudaStream_t st);
+
+}  // namespace kivi

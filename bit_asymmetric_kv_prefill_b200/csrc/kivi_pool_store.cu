@@ -1,0 +1,516 @@
+// kivi_pool_store.cu -- writing, reading and moving a pool's pages.
+//
+// pool_quant quantizes 32-token tiles with the cache's 2-bit code (keys per
+// channel, values per token; see kivi_quant.cu for the thresholds) straight
+// into page blocks, one warp per key or value tile.  Its tile rows may lie in
+// the residual and in the new rows, at any strides.
+// All kernels here are HBM bound: a quantized element costs 2 bytes read and
+// 0.375 written, a gathered one 0.375 read and 2 written.
+#include <cuda_runtime.h>
+
+#include "kivi_code.cuh"
+#include "kivi_pool.cuh"
+
+namespace kivi {
+namespace {
+
+__device__ __forceinline__ void cp_async16_zfill(uint32_t smem, const void *gmem, bool real)
+{
+    const int n = real ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(n) : "memory");
+}
+
+// Last index e of off[0..n] (off[0] = 0, ascending) with off[e] <= x < off[n].
+__device__ __forceinline__ int entry_of(const int *off, int n, int x)
+{
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (off[mid] <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ uint8_t *page_block(const PoolView &v, int seq, int g, int h, int gb)
+{
+    const int page = v.table[(long long)seq * v.max_pages + g / v.gpp];
+    return v.packed + (((long long)page * v.H + h) * v.gpp + g % v.gpp) * gb;
+}
+
+// Shared-memory byte offset of 16-byte chunk c of row t: chunks are exchanged
+// within a row by the row's low bits, so that eight rows of one chunk column
+// (a matrix load) fall into different banks.
+template <int D>
+__device__ __forceinline__ int tile_at(int t, int c)
+{
+    constexpr int C = D / 8;
+    return (t * C + (c ^ (t & 7))) * 16;
+}
+
+// ---- quantize -----------------------------------------------------------------
+// Key tile.  Lane l holds the CK = D/32 channels from CK*l of all 32 tokens,
+// so the statistics are its own.  A word of the block (one token, 16 channels)
+// is shared by 4 (D = 128) or 8 lanes: they exchange codes in a transposing
+// OR-shuffle over lane bits LB, after which each lane stores whole words.
+template <int D, int DT>
+__device__ __forceinline__ void page_key_tile(const uint8_t *tile, uint8_t *blk, int lane)
+{
+    using L = PageLayout<D>;
+    using H = In<DT>;
+    constexpr int CK = D / 32, NP = CK / 2;
+    constexpr int NL = D == 128 ? 2 : 3, CH = 1 << NL;
+    constexpr int LB[3] = {0, D == 128 ? 3 : 1, 4};
+    const int c0 = CK * lane;
+    uint32_t x[32][NP];
+#pragma unroll
+    for (int t = 0; t < 32; ++t) {
+        const uint8_t *s = tile + tile_at<D>(t, c0 / 8) + (c0 % 8) * 2;
+        if constexpr (NP == 2) {
+            const uint2 v = *(const uint2 *)s;
+            x[t][0] = v.x;
+            x[t][1] = v.y;
+        } else {
+            x[t][0] = *(const uint32_t *)s;
+        }
+    }
+    uint32_t T1[NP], T2[NP], T3[NP];
+    uint64_t mn64 = 0, mx64 = 0;
+#pragma unroll
+    for (int pp = 0; pp < NP; ++pp) {
+        uint32_t mn = x[0][pp], mx = x[0][pp];
+#pragma unroll
+        for (int t = 1; t < 32; ++t) {
+            mn = H::vmin(mn, x[t][pp]);
+            mx = H::vmax(mx, x[t][pp]);
+        }
+        mn64 |= (uint64_t)mn << (32 * pp);
+        mx64 |= (uint64_t)mx << (32 * pp);
+    }
+    uint64_t t1s = 0, t2s = 0, t3s = 0, ss = 0, zs = 0;
+#pragma unroll 1
+    for (int ch = 0; ch < CK; ++ch) {
+        const CodeParams c = code_params(H::f((uint16_t)mn64), H::f((uint16_t)mx64));
+        mn64 >>= 16;
+        mx64 >>= 16;
+        const int sh = 16 * ch;
+        t1s |= (uint64_t)min_passing<DT>(c.e1, c.z) << sh;
+        t2s |= (uint64_t)min_passing<DT>(c.e2, c.z) << sh;
+        t3s |= (uint64_t)min_passing<DT>(c.e3, c.z) << sh;
+        ss |= (uint64_t)c.s_bits << sh;
+        zs |= (uint64_t)c.z_bits << sh;
+    }
+#pragma unroll
+    for (int pp = 0; pp < NP; ++pp) {
+        T1[pp] = (uint32_t)(t1s >> (32 * pp));
+        T2[pp] = (uint32_t)(t2s >> (32 * pp));
+        T3[pp] = (uint32_t)(t3s >> (32 * pp));
+        *(uint32_t *)(blk + L::KS + (c0 + 2 * pp) * 2) = (uint32_t)(ss >> (32 * pp));
+        *(uint32_t *)(blk + L::KZ + (c0 + 2 * pp) * 2) = (uint32_t)(zs >> (32 * pp));
+    }
+    // The lane's channels: u = c0/32, cs = (c0%32)/8, pairs from i0 of word w.
+    const int u = c0 / 32, cs = (c0 % 32) / 8, w = u / 2;
+    const int i0 = 4 * (u % 2) + (c0 % 8) / 2;
+    uint32_t K1[NP], K3[NP];
+#pragma unroll
+    for (int pp = 0; pp < NP; ++pp) {
+        K1[pp] = 0x00010001u << (2 * (i0 + pp));
+        K3[pp] = 0x00030003u << (2 * (i0 + pp));
+    }
+    int jt = 0;   // the token of each chunk that stays with this lane
+#pragma unroll
+    for (int r = 0; r < NL; ++r) jt |= ((lane >> LB[r]) & 1) << r;
+#pragma unroll
+    for (int m = 0; m < 32 / CH; ++m) {
+        uint32_t wd[CH];
+#pragma unroll
+        for (int q = 0; q < CH; ++q) {
+            const int t = m * CH + q;
+            uint32_t acc = 0;
+#pragma unroll
+            for (int pp = 0; pp < NP; ++pp) acc |= code_pair_at<DT>(x[t][pp], T1[pp], T2[pp], T3[pp], K1[pp], K3[pp]);
+            wd[q] = acc;
+        }
+#pragma unroll
+        for (int r = 0; r < NL; ++r) {
+            const bool b = (lane >> LB[r]) & 1;
+#pragma unroll
+            for (int e = 0; e < (CH >> (r + 1)); ++e) {
+                const uint32_t lo = wd[2 * e], hi = wd[2 * e + 1];
+                const uint32_t send = b ? lo : hi, keep = b ? hi : lo;
+                wd[e] = keep | __shfl_xor_sync(0xffffffffu, send, 1 << LB[r]);
+            }
+        }
+        const int t = m * CH + jt;   // token t = tq + 8j
+        *(uint32_t *)(blk + L::KC + code_word_offset(4 * (t & 7) + cs, (t >> 3) * L::KW + w)) = wd[0];
+    }
+}
+
+// Value tile.  A transposing matrix load leaves lane 4n + cs the token pairs
+// and channels that it owns in the block.  A token's group of 32 channels
+// spans 4 registers and the 8 lanes of one cs; those reduce (min, -max) in a
+// transposing shuffle over lane bits 2, 3, 4, compute the parameters of their
+// share and publish the thresholds (packed for the two tokens) in `thr`
+// [4 pairs][NJ][4 cs].
+template <int D, int DT>
+__device__ __forceinline__ void page_value_tile(const uint8_t *tile, uint8_t *blk, int lane, uint4 *thr)
+{
+    using L = PageLayout<D>;
+    using H = In<DT>;
+    constexpr int NC = D / 8, NJ = L::NJ, NV = 4 * NJ;   // channel tiles, groups, (pair, group) combinations
+    const int cs = lane & 3;
+    uint32_t x[4][NC];
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(tile);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+#pragma unroll
+        for (int c = 0; c < NC; c += 4) {
+            const uint32_t a = base + tile_at<D>(8 * p + (lane & 7), c + (lane >> 3));
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(x[p][c]), "=r"(x[p][c + 1]), "=r"(x[p][c + 2]), "=r"(x[p][c + 3])
+                         : "r"(a));
+        }
+    }
+    // mn, nx [combination p*NJ + j]: per token min and -max (as a min).
+    uint32_t mn[NV], nx[NV];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            uint32_t a = x[p][4 * j], b = x[p][4 * j];
+#pragma unroll
+            for (int c = 1; c < 4; ++c) {
+                a = H::vmin(a, x[p][4 * j + c]);
+                b = H::vmax(b, x[p][4 * j + c]);
+            }
+            mn[p * NJ + j] = a;
+            nx[p * NJ + j] = b ^ 0x80008000u;
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 3; ++r) {
+        const bool b = (lane >> (2 + r)) & 1;
+#pragma unroll
+        for (int e = 0; e < (NV >> (r + 1)); ++e) {
+            const uint32_t s0 = b ? mn[2 * e] : mn[2 * e + 1], k0 = b ? mn[2 * e + 1] : mn[2 * e];
+            const uint32_t s1 = b ? nx[2 * e] : nx[2 * e + 1], k1 = b ? nx[2 * e + 1] : nx[2 * e];
+            mn[e] = H::vmin(k0, __shfl_xor_sync(0xffffffffu, s0, 4 << r));
+            nx[e] = H::vmin(k1, __shfl_xor_sync(0xffffffffu, s1, 4 << r));
+        }
+    }
+    // Left: combinations e*8 + n (n = lane/4), e < NV/8.
+    __syncwarp();
+#pragma unroll 1
+    for (int e = 0; e < NV / 8; ++e) {
+        const int v = e * 8 + (lane >> 2), p = v / NJ, j = v % NJ;
+        uint32_t lo = mn[0], hi = nx[0];
+#pragma unroll
+        for (int k = 1; k < NV / 8; ++k)
+            if (e == k) {
+                lo = mn[k];
+                hi = nx[k];
+            }
+        uint32_t t1 = 0, t2 = 0, t3 = 0, ss = 0, zs = 0;
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+            const CodeParams c = code_params(H::f((uint16_t)(lo >> (16 * k))), -H::f((uint16_t)(hi >> (16 * k))));
+            t1 |= (uint32_t)min_passing<DT>(c.e1, c.z) << (16 * k);
+            t2 |= (uint32_t)min_passing<DT>(c.e2, c.z) << (16 * k);
+            t3 |= (uint32_t)min_passing<DT>(c.e3, c.z) << (16 * k);
+            ss |= (uint32_t)c.s_bits << (16 * k);
+            zs |= (uint32_t)c.z_bits << (16 * k);
+        }
+        thr[v * 4 + cs] = make_uint4(t1, t2, t3, 0u);
+        *(uint2 *)(blk + L::VM + page_vm_offset<D>(p, cs, j)) = make_uint2(ss, zs);
+    }
+    __syncwarp();
+    uint32_t wv[L::WPL];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+#pragma unroll
+        for (int jh = 0; jh < L::KW; ++jh) {
+            uint32_t word = 0;
+#pragma unroll
+            for (int jj = 0; jj < 2; ++jj) {
+                const uint4 b = thr[(p * NJ + 2 * jh + jj) * 4 + cs];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int i = 4 * jj + c;
+                    word |= code_pair_at<DT>(x[p][8 * jh + i], b.x, b.y, b.z, 0x00010001u << (2 * i), 0x00030003u << (2 * i));
+                }
+            }
+            wv[p * L::KW + jh] = word;
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < L::WPL / 4; ++c)
+        *(uint4 *)(blk + L::VC + (c * 32 + lane) * 16) = make_uint4(wv[4 * c], wv[4 * c + 1], wv[4 * c + 2], wv[4 * c + 3]);
+}
+
+constexpr int kStoreWarps = 4;
+
+template <int D>
+struct StoreSmem {
+    static constexpr int TILE = 32 * D * 2;
+    static constexpr int THR = 16 * PageLayout<D>::NJ * 16;
+    static constexpr int PER_WARP = TILE + THR;
+    static constexpr int BYTES = kStoreWarps * PER_WARP;
+};
+
+// One warp per (32-token group, head) item and kind of tile.
+template <int D, int DT>
+__global__ void __launch_bounds__(kStoreWarps * 32)
+    pool_quant_kernel(const PoolView v, const Rows k, const Rows nv, const __grid_constant__ ExtendTab t)
+{
+    extern __shared__ __align__(128) uint8_t sm[];
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    uint8_t *tile = sm + wid * StoreSmem<D>::PER_WARP;
+    const int unit = blockIdx.x * kStoreWarps + wid;
+    if (unit >= 2 * t.item[t.nb]) return;
+    const int item = unit >> 1, vhalf = unit & 1;
+    const int e = entry_of(t.item, t.nb, item);
+    const int local = item - t.item[e], g = local / v.H, h = local - g * v.H;
+    const int seq = t.seq[e], r = t.r[e];
+    const uint16_t *res = (vhalf ? v.resV : v.resK) + ((long long)seq * v.H + h) * v.R * D;
+    const Rows &src = vhalf ? nv : k;
+    constexpr int C = D / 8;
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(tile);
+#pragma unroll
+    for (int it = 0; it < C; ++it) {
+        const int q = it * 32 + lane, row = q / C, c = q % C;
+        const int tok = 32 * g + row;   // from the sequence's first unquantized token
+        const uint16_t *p = tok < r ? res + (long long)tok * D
+                                    : src.p + (long long)(t.row0[e] + tok - r) * src.ts + h * src.hs;
+        cp_async16_zfill(base + tile_at<D>(row, c), p + c * 8, true);
+    }
+    cp_async_commit();
+    uint8_t *blk = page_block(v, seq, t.g0[e] + g, h, PageLayout<D>::GB);
+    cp_async_wait_all();
+    __syncwarp();
+    if (!vhalf) page_key_tile<D, DT>(tile, blk, lane);
+    else page_value_tile<D, DT>(tile, blk, lane, (uint4 *)(tile + StoreSmem<D>::TILE));
+}
+
+// New rows that stay unquantized go to their residual slots: one 16-byte chunk
+// of K and of V per thread.
+__global__ void __launch_bounds__(256)
+    pool_keep_kernel(const PoolView v, const Rows k, const Rows nv, const __grid_constant__ ExtendTab t)
+{
+    const int C = v.D / 8;
+    const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
+    const long long rest = id / C;
+    const int c = (int)(id - rest * C);
+    const long long row = rest / v.H;
+    const int h = (int)(rest - row * v.H);
+    if (row >= t.kept[t.nb]) return;
+    const int e = entry_of(t.kept, t.nb, (int)row);
+    const int i = (int)row - t.kept[e];
+    const long long from = t.row0[e] + t.from[e] + i;
+    const long long to = (((long long)t.seq[e] * v.H + h) * v.R + t.slot0[e] + i) * v.D + c * 8;
+    const uint4 a = *(const uint4 *)(k.p + from * k.ts + h * k.hs + c * 8);
+    const uint4 b = *(const uint4 *)(nv.p + from * nv.ts + h * nv.hs + c * 8);
+    *(uint4 *)(v.resK + to) = a;
+    *(uint4 *)(v.resV + to) = b;
+}
+
+// ---- gather -------------------------------------------------------------------
+template <int DT>
+__device__ __forceinline__ uint32_t round2(float a, float b)
+{
+    uint32_t r;
+    if constexpr (DT == KIVI_BF16) {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
+        memcpy(&r, &x, 4);
+    } else {
+        const __half2 x = __floats2half2_rn(a, b);
+        memcpy(&r, &x, 4);
+    }
+    return r;
+}
+__device__ __forceinline__ float half_lo(uint32_t x) { return __half2float(__ushort_as_half((uint16_t)x)); }
+__device__ __forceinline__ float half_hi(uint32_t x) { return __half2float(__ushort_as_half((uint16_t)(x >> 16))); }
+
+// Pair i of a code word, decoded and rounded to the pool's type: s, z packed.
+template <int DT>
+__device__ __forceinline__ uint32_t decode_pair(uint32_t w, int i, uint32_t s, uint32_t z)
+{
+    const float a = (float)((w >> (2 * i)) & 3u), b = (float)((w >> (16 + 2 * i)) & 3u);
+    return round2<DT>(__fmaf_rn(a, half_lo(s), half_lo(z)), __fmaf_rn(b, half_hi(s), half_hi(z)));
+}
+
+// One warp per (32 tokens, head): decode K and V (values through shared memory,
+// since a lane holds columns of them) or copy residual rows.
+template <int D, int DT>
+__global__ void __launch_bounds__(kStoreWarps * 32)
+    pool_gather_kernel(const PoolView v, const __grid_constant__ GatherTab t, uint16_t *K, uint16_t *V)
+{
+    using L = PageLayout<D>;
+    extern __shared__ __align__(128) uint8_t sm[];
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    uint8_t *tile = sm + wid * StoreSmem<D>::TILE;
+    const int item = blockIdx.x * kStoreWarps + wid;
+    if (item >= t.item[t.nb]) return;
+    const int e = entry_of(t.item, t.nb, item);
+    const int local = item - t.item[e], g = local / v.H, h = local - g * v.H;
+    const int seq = t.seq[e], ng = t.ng[e];
+    const long long ts = (long long)v.H * D;
+    constexpr int C = D / 8;
+    uint16_t *ko = K + (long long)(t.row0[e] + 32 * g) * ts + h * D;
+    uint16_t *vo = V + (long long)(t.row0[e] + 32 * g) * ts + h * D;
+    if (g >= ng) {
+        const int s0 = 32 * (g - ng), n = min(32, t.r[e] - s0);
+        const long long from = (((long long)seq * v.H + h) * v.R + s0) * D;
+        for (int q = lane; q < n * C; q += 32) {
+            const int row = q / C, c = q % C;
+            *(uint4 *)(ko + row * ts + c * 8) = *(const uint4 *)(v.resK + from + q * 8);
+            *(uint4 *)(vo + row * ts + c * 8) = *(const uint4 *)(v.resV + from + q * 8);
+        }
+        return;
+    }
+    const uint8_t *blk = page_block(v, seq, g, h, L::GB);
+    const int tq = lane >> 2, cs = lane & 3;
+    uint32_t kw[L::WPL], vw[L::WPL];
+#pragma unroll
+    for (int c = 0; c < L::WPL / 4; ++c) {
+        *(uint4 *)(kw + 4 * c) = *(const uint4 *)(blk + L::KC + (c * 32 + lane) * 16);
+        *(uint4 *)(vw + 4 * c) = *(const uint4 *)(blk + L::VC + (c * 32 + lane) * 16);
+    }
+#pragma unroll
+    for (int u = 0; u < D / 32; ++u) {
+        uint32_t s[4], z[4];
+        *(uint4 *)s = *(const uint4 *)(blk + L::KS + u * 64 + cs * 16);
+        *(uint4 *)z = *(const uint4 *)(blk + L::KZ + u * 64 + cs * 16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t o[4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) o[p] = decode_pair<DT>(kw[j * L::KW + u / 2], 4 * (u % 2) + p, s[p], z[p]);
+            *(uint4 *)(ko + (tq + 8 * j) * ts + 32 * u + 8 * cs) = *(const uint4 *)o;
+        }
+    }
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(tile);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+#pragma unroll
+        for (int j = 0; j < L::NJ; ++j) {
+            const uint2 sz = *(const uint2 *)(blk + L::VM + page_vm_offset<D>(p, cs, j));
+            uint32_t o[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[c] = decode_pair<DT>(vw[p * L::KW + j / 2], 4 * (j % 2) + c, sz.x, sz.y);
+            const uint32_t a = base + tile_at<D>(8 * p + (lane & 7), 4 * j + (lane >> 3));
+            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(o[0]),
+                         "r"(o[1]), "r"(o[2]), "r"(o[3])
+                         : "memory");
+        }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int it = 0; it < C; ++it) {
+        const int q = it * 32 + lane, row = q / C, c = q % C;
+        *(uint4 *)(vo + row * ts + c * 8) = *(const uint4 *)(tile + tile_at<D>(row, c));
+    }
+}
+
+// ---- tables, moves, forks -------------------------------------------------------
+__global__ void pool_table_kernel(int *table, const __grid_constant__ PairTab t)
+{
+    for (int i = threadIdx.x; i < t.n; i += blockDim.x) table[t.a[i]] = t.b[i];
+}
+
+// Page a[i] to page b[i]; blocks (chunk, i).
+__global__ void __launch_bounds__(256)
+    pool_move_kernel(uint8_t *packed, long long page_bytes, const __grid_constant__ PairTab t)
+{
+    const uint4 *from = (const uint4 *)(packed + t.a[blockIdx.y] * page_bytes);
+    uint4 *to = (uint4 *)(packed + t.b[blockIdx.y] * page_bytes);
+    const long long n = page_bytes / 16, step = (long long)gridDim.x * 256;
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += step) to[i] = from[i];
+}
+
+// Blocks (head, entry): the residual rows of one head; head 0's block also the
+// table row.
+__global__ void __launch_bounds__(256) pool_fork_kernel(const PoolView v, const __grid_constant__ ForkTab t)
+{
+    const int e = blockIdx.y, h = blockIdx.x;
+    const long long a = ((long long)t.src[e] * v.H + h) * v.R * v.D, b = ((long long)t.dst[e] * v.H + h) * v.R * v.D;
+    const int n = t.r[e] * v.D / 8;
+    for (int i = threadIdx.x; i < n; i += 256) {
+        const uint4 x = ((const uint4 *)(v.resK + a))[i], y = ((const uint4 *)(v.resV + a))[i];
+        ((uint4 *)(v.resK + b))[i] = x;
+        ((uint4 *)(v.resV + b))[i] = y;
+    }
+    if (h == 0)
+        for (int i = threadIdx.x; i < t.np[e]; i += 256)
+            v.table[(long long)t.dst[e] * v.max_pages + i] = v.table[(long long)t.src[e] * v.max_pages + i];
+}
+
+template <int D, int DT>
+cudaError_t quant_t(const PoolView &v, const Rows &k, const Rows &nv, const ExtendTab &t, cudaStream_t st)
+{
+    static PerDeviceOnce once;
+    const cudaError_t e = set_smem_once(once, pool_quant_kernel<D, DT>, StoreSmem<D>::BYTES);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = (2u * t.item[t.nb] + kStoreWarps - 1) / kStoreWarps;
+    pool_quant_kernel<D, DT><<<grid, kStoreWarps * 32, StoreSmem<D>::BYTES, st>>>(v, k, nv, t);
+    return cudaGetLastError();
+}
+
+template <int D, int DT>
+cudaError_t gather_t(const PoolView &v, const GatherTab &t, uint16_t *K, uint16_t *V, cudaStream_t st)
+{
+    const unsigned grid = ((unsigned)t.item[t.nb] + kStoreWarps - 1) / kStoreWarps;
+    pool_gather_kernel<D, DT><<<grid, kStoreWarps * 32, kStoreWarps * StoreSmem<D>::TILE, st>>>(v, t, K, V);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_pool_quant(const PoolView &v, const Rows &k, const Rows &nv, const ExtendTab &t, cudaStream_t st)
+{
+    if (t.item[t.nb] == 0) return cudaSuccess;
+    if (v.D == 64) return v.dtype ? quant_t<64, 1>(v, k, nv, t, st) : quant_t<64, 0>(v, k, nv, t, st);
+    return v.dtype ? quant_t<128, 1>(v, k, nv, t, st) : quant_t<128, 0>(v, k, nv, t, st);
+}
+
+cudaError_t launch_pool_keep(const PoolView &v, const Rows &k, const Rows &nv, const ExtendTab &t, cudaStream_t st)
+{
+    const long long n = (long long)t.kept[t.nb] * v.H * (v.D / 8);
+    if (n == 0) return cudaSuccess;
+    pool_keep_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(v, k, nv, t);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_pool_gather(const PoolView &v, const GatherTab &t, uint16_t *K, uint16_t *V, cudaStream_t st)
+{
+    if (t.item[t.nb] == 0) return cudaSuccess;
+    if (v.D == 64) return v.dtype ? gather_t<64, 1>(v, t, K, V, st) : gather_t<64, 0>(v, t, K, V, st);
+    return v.dtype ? gather_t<128, 1>(v, t, K, V, st) : gather_t<128, 0>(v, t, K, V, st);
+}
+
+cudaError_t launch_pool_table(const PoolView &v, const PairTab &t, cudaStream_t st)
+{
+    if (t.n == 0) return cudaSuccess;
+    pool_table_kernel<<<1, 256, 0, st>>>(v.table, t);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_pool_move(const PoolView &v, const PairTab &t, cudaStream_t st)
+{
+    if (t.n == 0) return cudaSuccess;
+    const long long bytes = (long long)v.H * v.gpp * 24 * v.D;
+    const long long need = (bytes / 16 + 255) / 256;
+    // A few chunks per thread, and enough blocks for a short list.
+    unsigned x = (unsigned)((need + 3) / 4);
+    if (x > 64) x = 64;
+    pool_move_kernel<<<dim3(x, t.n), 256, 0, st>>>(v.packed, bytes, t);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_pool_fork(const PoolView &v, const ForkTab &t, cudaStream_t st)
+{
+    if (t.n == 0) return cudaSuccess;
+    pool_fork_kernel<<<dim3(v.H, t.n), 256, 0, st>>>(v, t);
+    return cudaGetLastError();
+}
+
+}  // namespace kivi

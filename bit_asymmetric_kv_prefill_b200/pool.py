@@ -1,0 +1,206 @@
+"""A pool of cache pages (kivi_pool): sequences of the 2-bit cache that come,
+grow, branch and go at their own pace, and attention of their new tokens."""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import PoolConfig, PoolRows, _check, _dtype_code, _on_device, _stream_ptr, lib
+
+
+def _ints(values, what):
+    try:
+        return (ctypes.c_int * len(values))(*values)
+    except TypeError:
+        raise ValueError(f"{what} must be a sequence of integers") from None
+
+
+class KiviPool:
+    """One layer's pool of pages on the current GPU (see kivi_pool in the
+    header).  A page holds ``R`` tokens of every kv head in 2-bit codes; a
+    sequence is a number from :meth:`open`, :meth:`fork` or :meth:`copy`."""
+
+    def __init__(self, pages: int, sequences: int, H_kv: int, D: int, G: int = 32, R: int = 128,
+                 dtype=torch.bfloat16, T_max: int = 4096, workspace: torch.Tensor | None = None):
+        self.pages, self.sequences, self.H_kv, self.D, self.G, self.R = pages, sequences, H_kv, D, G, R
+        self.dtype, self.T_max = dtype, T_max
+        cfg = PoolConfig(H_kv, D, G, R, _dtype_code(dtype), pages, sequences, T_max, None, 0)
+        self._workspace = workspace
+        if workspace is not None:
+            if not workspace.is_cuda:
+                raise ValueError("workspace must be a CUDA tensor")
+            cfg.workspace = workspace.data_ptr()
+            cfg.workspace_bytes = workspace.numel() * workspace.element_size()
+        self.device = torch.device("cuda", torch.cuda.current_device())
+        h = ctypes.c_void_p()
+        _check(lib().kivi_pool_create(ctypes.byref(cfg), ctypes.byref(h)), "kivi_pool_create")
+        self._h = h
+
+    @staticmethod
+    def required_bytes(pages, sequences, H_kv, D, G=32, R=128, dtype=torch.bfloat16, T_max=4096) -> int:
+        cfg = PoolConfig(H_kv, D, G, R, _dtype_code(dtype), pages, sequences, T_max, None, 0)
+        n = ctypes.c_size_t()
+        _check(lib().kivi_pool_required_bytes(ctypes.byref(cfg), ctypes.byref(n)), "kivi_pool_required_bytes")
+        return n.value
+
+    def _rows(self, t: torch.Tensor, rows: int, heads: int, name: str):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != self.device:
+            raise ValueError(f"{name} must be a CUDA tensor on {self.device}")
+        if t.dtype != self.dtype:
+            raise ValueError(f"{name} must be {self.dtype}, got {t.dtype}")
+        if t.shape != (rows, heads, self.D):
+            raise ValueError(f"{name} must have shape {(rows, heads, self.D)}, got {tuple(t.shape)}")
+        ts, hs, one = t.stride()
+        if one != 1:
+            raise ValueError(f"{name} must have contiguous channels")
+        return PoolRows(t.data_ptr(), ts, hs)
+
+    # -- sequences ----------------------------------------------------------------
+    def open(self, n: int = 1) -> list:
+        """n new empty sequences."""
+        a = (ctypes.c_int * max(n, 1))()
+        _check(lib().kivi_pool_open(self._h, n, a), "kivi_pool_open")
+        return a[:n]
+
+    def free(self, seqs) -> None:
+        """Forget sequences; pages that no other sequence holds become free."""
+        _check(lib().kivi_pool_free(self._h, _ints(seqs, "seqs"), len(seqs)), "kivi_pool_free")
+
+    def fork(self, seqs, stream=None) -> list:
+        """New sequences with the contents of ``seqs`` (repeats allowed) that
+        share their pages."""
+        return self._branch(lib().kivi_pool_fork, "kivi_pool_fork", seqs, stream)
+
+    def copy(self, seqs, stream=None) -> list:
+        """New sequences with the contents of ``seqs`` in pages of their own."""
+        return self._branch(lib().kivi_pool_copy, "kivi_pool_copy", seqs, stream)
+
+    def _branch(self, call, what, seqs, stream):
+        n = len(seqs)
+        a = (ctypes.c_int * max(n, 1))()
+        with _on_device(self.device):
+            _check(call(self._h, _ints(seqs, "seqs"), n, a, _stream_ptr(stream)), what)
+        return a[:n]
+
+    def compact(self, stream=None) -> int:
+        """Move pages to the front of the pool; returns how many moved."""
+        n = ctypes.c_int()
+        with _on_device(self.device):
+            _check(lib().kivi_pool_compact(self._h, ctypes.byref(n), _stream_ptr(stream)), "kivi_pool_compact")
+        return n.value
+
+    # -- tokens -------------------------------------------------------------------
+    def extend(self, seqs, K: torch.Tensor, V: torch.Tensor, lengths=None, stream=None) -> None:
+        """Append ``lengths[i]`` tokens (one each unless given) to ``seqs[i]``:
+        K, V [sum(lengths), H_kv, D] hold those of seqs[0] first."""
+        n = len(seqs)
+        if lengths is None:
+            lengths = [1] * n
+        elif len(lengths) != n:
+            raise ValueError(f"lengths must hold {n} values")
+        N = sum(lengths)
+        k, v = self._rows(K, N, self.H_kv, "K"), self._rows(V, N, self.H_kv, "V")
+        with _on_device(self.device):
+            _check(lib().kivi_pool_extend(self._h, _ints(seqs, "seqs"), _ints(lengths, "lengths"), n, ctypes.byref(k),
+                                          ctypes.byref(v), _stream_ptr(stream)), "kivi_pool_extend")
+
+    def attend(self, seqs, q: torch.Tensor, K: torch.Tensor | None = None, V: torch.Tensor | None = None,
+               lengths=None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Attention of the new tokens' queries q [sum(lengths), H_q, D] over
+        the cached tokens of their sequence and, where K and V [sum(lengths),
+        H_kv, D] are given, the new tokens up to their own.  Returns
+        [sum(lengths), H_q, D] in the pool's dtype."""
+        n = len(seqs)
+        if lengths is None:
+            lengths = [1] * n
+        elif len(lengths) != n:
+            raise ValueError(f"lengths must hold {n} values")
+        N = sum(lengths)
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q must be a CUDA tensor [rows, H_q, D]")
+        H_q = q.shape[1]
+        qr = self._rows(q, N, H_q, "q")
+        kr = vr = None
+        if K is not None or V is not None:
+            if K is None or V is None:
+                raise ValueError("K and V come together")
+            kr = ctypes.byref(self._rows(K, N, self.H_kv, "K"))
+            vr = ctypes.byref(self._rows(V, N, self.H_kv, "V"))
+        if out is None:
+            out = torch.empty((N, H_q, self.D), dtype=self.dtype, device=self.device)
+        elif (out.dtype != self.dtype or out.shape != (N, H_q, self.D) or not out.is_contiguous()
+              or out.device != self.device):
+            raise ValueError(f"out must be a contiguous {self.dtype} {(N, H_q, self.D)} tensor on {self.device}")
+        with _on_device(self.device):
+            _check(lib().kivi_pool_attn(self._h, _ints(seqs, "seqs"), _ints(lengths, "lengths"), n, ctypes.byref(qr),
+                                        kr, vr, H_q, out.data_ptr(), _stream_ptr(stream)), "kivi_pool_attn")
+        return out
+
+    def gather(self, seqs, K: torch.Tensor | None = None, V: torch.Tensor | None = None, stream=None):
+        """The cached tokens of ``seqs``, one sequence after another, decoded:
+        (K, V) [tokens, H_kv, D] in the pool's dtype."""
+        N = sum(sum(self.length(s)) for s in seqs)
+        shape = (N, self.H_kv, self.D)
+        K, V = (torch.empty(shape, dtype=self.dtype, device=self.device) if t is None else t for t in (K, V))
+        for name, t in (("K", K), ("V", V)):
+            self._rows(t, N, self.H_kv, name)
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        with _on_device(self.device):
+            _check(lib().kivi_pool_gather(self._h, _ints(seqs, "seqs"), len(seqs), K.data_ptr(), V.data_ptr(),
+                                          _stream_ptr(stream)), "kivi_pool_gather")
+        return K, V
+
+    # -- inspection ---------------------------------------------------------------
+    def length(self, seq: int):
+        """(tokens in pages, tokens in the residual) of a sequence."""
+        n_q, r = ctypes.c_longlong(), ctypes.c_int()
+        _check(lib().kivi_pool_length(self._h, seq, ctypes.byref(n_q), ctypes.byref(r)), "kivi_pool_length")
+        return n_q.value, r.value
+
+    def pages_of(self, seq: int) -> list:
+        """The pages of a sequence, oldest first."""
+        n = ctypes.c_int()
+        _check(lib().kivi_pool_pages(self._h, seq, None, 0, ctypes.byref(n)), "kivi_pool_pages")
+        a = (ctypes.c_int * max(n.value, 1))()
+        _check(lib().kivi_pool_pages(self._h, seq, a, n.value, ctypes.byref(n)), "kivi_pool_pages")
+        return a[:n.value]
+
+    def usage(self) -> dict:
+        """Pages in use, one past the last of them, open sequences."""
+        a = [ctypes.c_int() for _ in range(3)]
+        _check(lib().kivi_pool_usage(self._h, *[ctypes.byref(x) for x in a]), "kivi_pool_usage")
+        return dict(zip(("pages_used", "pages_end", "sequences_open"), (x.value for x in a)))
+
+    def device_status(self) -> int:
+        code = ctypes.c_int()
+        with _on_device(self.device):
+            _check(lib().kivi_pool_device_status(self._h, ctypes.byref(code)), "kivi_pool_device_status")
+        return code.value
+
+    def export(self, seq: int, head: int) -> dict:
+        """Canonical unpacked copy (host numpy arrays) of one head of a sequence."""
+        import numpy as np
+        n_q, r = self.length(seq)
+        D, G = self.D, self.G
+        a = dict(codesK=np.zeros((n_q, D), np.uint8), codesV=np.zeros((n_q, D), np.uint8),
+                 sK=np.zeros((n_q // G, D), np.uint16), zK=np.zeros((n_q // G, D), np.uint16),
+                 sV=np.zeros((n_q, D // G), np.uint16), zV=np.zeros((n_q, D // G), np.uint16),
+                 resK=np.zeros((r, D), np.uint16), resV=np.zeros((r, D), np.uint16))
+        ptr = {k: v.ctypes.data_as(ctypes.c_void_p) for k, v in a.items()}
+        with _on_device(self.device):
+            _check(lib().kivi_pool_export(self._h, seq, head, ptr["codesK"], ptr["codesV"], ptr["sK"], ptr["zK"],
+                                          ptr["sV"], ptr["zV"], ptr["resK"], ptr["resV"]), "kivi_pool_export")
+        return a
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().kivi_pool_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass

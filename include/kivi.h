@@ -391,6 +391,122 @@ typedef struct {
 KIVI_API kivi_status kivi_rope_frequencies(int rot, double theta, const kivi_rope_scaling *scaling,
                                            float *inv_freq, float *scale);
 
+/*
+ * A pool of cache pages: the same 2-bit cache for sequences that come, grow,
+ * branch and go at their own pace (one pool per layer).  A page holds R tokens
+ * of every kv head in codes; a sequence is a list of pages and a residual of
+ * its newest 1..R tokens in full precision (n_q = R*floor((T-1)/R), as in a
+ * kivi_cache).  A page is written once, when its R tokens leave the residual,
+ * so sequences share pages by count.
+ *
+ *   - A sequence is a small non-negative number (`sequences` of them at once).
+ *   - Rows are token-major: k, v, q hold the new tokens of seqs[0], then of
+ *     seqs[1], and so on, each [token, head, D] with strides in elements that
+ *     are multiples of 8, contiguous channels and a 16-byte aligned start
+ *     (slices of one projection's output serve as they are).
+ *   - Bookkeeping is on the host and immediate; device work is asynchronous on
+ *     `stream`.  The calls on one pool share its tables and its attention
+ *     scratch: order them (one stream, or events), captured graphs included.
+ *     A captured call replays with the lengths and pages of its capture.
+ *   - On KIVI_ERR_ARG, _UNSUPPORTED, _CAPACITY and _OOM nothing was launched
+ *     and the pool is unchanged; KIVI_ERR_CUDA leaves the contents of the
+ *     sequences of the call undefined.  Calls that launch need the pool's
+ *     device current (else KIVI_ERR_ARG).
+ *   - At most 512 sequences per call (else KIVI_ERR_UNSUPPORTED); n = 0 does
+ *     nothing.  No call allocates device memory except kivi_pool_create
+ *     without a workspace.  A pool is not thread-safe.
+ *   - A value group whose zero + 3*scale passes 65504 (values near the fp16
+ *     limit) decodes to infinity in kivi_pool_attn.
+ *
+ * Supported: D in {64, 128}, G == 32, R a positive multiple of G (at most
+ * 2^20), H_kv <= 4096, T_max <= 2^30.  Keys are stored as given (rotate them
+ * first; there is no pre-RoPE form).
+ */
+typedef struct kivi_pool kivi_pool;
+
+typedef struct {
+    int H_kv, D, G, R;
+    kivi_dtype dtype;
+    int pages;        /* capacity in pages of R tokens */
+    int sequences;    /* sequences that may be open at once */
+    long long T_max;  /* tokens of the longest sequence */
+    void *workspace;  /* optional device memory, 256-byte aligned, as in kivi_config */
+    size_t workspace_bytes;
+} kivi_pool_config;
+
+typedef struct {
+    const void *data;
+    long long token_stride, head_stride; /* in elements */
+} kivi_rows;
+
+KIVI_API kivi_status kivi_pool_required_bytes(const kivi_pool_config *cfg, size_t *bytes);
+KIVI_API kivi_status kivi_pool_create(const kivi_pool_config *cfg, kivi_pool **out);
+KIVI_API kivi_status kivi_pool_destroy(kivi_pool *p);
+
+/* n new empty sequences (KIVI_ERR_CAPACITY if too few are left). */
+KIVI_API kivi_status kivi_pool_open(kivi_pool *p, int n, int *seqs);
+
+/* Forget sequences (none twice): pages that no other sequence holds are free
+ * for later calls. */
+KIVI_API kivi_status kivi_pool_free(kivi_pool *p, const int *seqs, int n);
+
+/* Append n_new[i] >= 0 tokens to seqs[i] (no sequence twice): tokens that are
+ * no longer among the newest are quantized into new pages, bit for bit as
+ * kivi_prefill and kivi_append would.  KIVI_ERR_CAPACITY past T_max or when
+ * the pages do not suffice. */
+KIVI_API kivi_status kivi_pool_extend(kivi_pool *p, const int *seqs, const int *n_new, int n,
+                                      const kivi_rows *k, const kivi_rows *v, void *stream);
+
+/*
+ * Attention of the n_new[i] >= 0 new rows of each sequence: row j of seqs[i]
+ * attends to every token cached in seqs[i] and to the new tokens 0..j of its
+ * own rows (k, v: not yet in the cache; append them afterwards with
+ * kivi_pool_extend).  With k = v = NULL the rows see the cached tokens only
+ * (decode after an append).  A row that sees nothing gives zeros.  Query head
+ * h reads kv head h / (H_q/H_kv), H_q any multiple of H_kv up to 65,536;
+ * scores are scaled by 1/sqrt(D).  A sequence may appear more than once.
+ *   q    [rows, H_q, D], k, v [rows, H_kv, D] in the pool's dtype
+ *   out  DEVICE [rows, H_q, D] contiguous, 16-byte aligned, in the pool's
+ *        dtype; must not overlap the inputs.
+ * A key or value that is not finite affects only rows that see its token.
+ */
+KIVI_API kivi_status kivi_pool_attn(kivi_pool *p, const int *seqs, const int *n_new, int n,
+                                    const kivi_rows *q, const kivi_rows *k, const kivi_rows *v,
+                                    int H_q, void *out, void *stream);
+
+/* The cached tokens of seqs[0], then seqs[1], ... as dense rows: K, V DEVICE
+ * [tokens, H_kv, D] contiguous in the pool's dtype, 16-byte aligned; coded
+ * tokens decoded (zero + scale*code in fp32, rounded once). */
+KIVI_API kivi_status kivi_pool_gather(kivi_pool *p, const int *seqs, int n, void *K, void *V,
+                                      void *stream);
+
+/* New sequences with the contents of src[i] (repeats allowed).  fork shares
+ * the pages and copies the residual; copy gives each its own pages.
+ * KIVI_ERR_CAPACITY if sequences or pages do not suffice. */
+KIVI_API kivi_status kivi_pool_fork(kivi_pool *p, const int *src, int n, int *dst, void *stream);
+KIVI_API kivi_status kivi_pool_copy(kivi_pool *p, const int *src, int n, int *dst, void *stream);
+
+/* Move pages so that the used ones are the first of the pool (sequences keep
+ * their numbers and contents); *moved (may be NULL) receives how many moved. */
+KIVI_API kivi_status kivi_pool_compact(kivi_pool *p, int *moved, void *stream);
+
+/* Tokens in pages and in the residual. */
+KIVI_API kivi_status kivi_pool_length(const kivi_pool *p, int seq, long long *n_q, int *r);
+/* The pages of a sequence (pages may be NULL: only *n). */
+KIVI_API kivi_status kivi_pool_pages(const kivi_pool *p, int seq, int *pages, int capacity, int *n);
+/* Pages in use, one past the last used page, open sequences. */
+KIVI_API kivi_status kivi_pool_usage(const kivi_pool *p, int *pages_used, int *pages_end,
+                                     int *sequences_open);
+
+/* As kivi_device_status: 0, or the code of the first failed bounded wait. */
+KIVI_API kivi_status kivi_pool_device_status(kivi_pool *p, int *code);
+
+/* One head of a sequence in the canonical layout of kivi_export (nseq = 1);
+ * testing and inspection, synchronises the device. */
+KIVI_API kivi_status kivi_pool_export(const kivi_pool *p, int seq, int head, uint8_t *codesK,
+                                      uint8_t *codesV, uint16_t *sK, uint16_t *zK, uint16_t *sV,
+                                      uint16_t *zV, void *resK, void *resV);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,84 @@
+"""Plain 64-bit forms for the pool's tests: the 2-bit code by its definition,
+attention of new tokens, and the error that the kernels' roundings allow."""
+import math
+
+import torch
+
+G = 32
+
+
+def code(x, dim):
+    """x [tokens, H, D]: codes and fp16 parameters of groups of 32 along dim (0: keys, 2: values), and the decoded
+    values in fp64.  fp32 roundings where the definition has them."""
+    x = x.double()
+    g = x.reshape(-1, G, *x.shape[1:]) if dim == 0 else x.reshape(*x.shape[:-1], -1, G)
+    a = 1 if dim == 0 else -1
+    lo, hi = g.amin(a, keepdim=True), g.amax(a, keepdim=True)
+    s = ((hi - lo).float().double() / 3).float().half()
+    z = lo.float().half()
+    sd, zd = s.double(), z.double()
+    y = ((g - zd).float().double() / torch.where(sd == 0, 1.0, sd)).float()
+    c = torch.where(sd == 0, 0.0, y.round().clamp(0, 3).double())
+    return c.reshape(x.shape).to(torch.uint8), s.squeeze(a), z.squeeze(a), (zd + sd * c).reshape(x.shape)
+
+
+def cached(K, V, R):
+    """The cache of one sequence's tokens [T, H, D] in fp64: coded, then residual; and the number coded."""
+    T = K.shape[0]
+    n_q = R * ((T - 1) // R) if T else 0
+    if n_q == 0:
+        return K.double(), V.double(), 0
+    return (torch.cat([code(K[:n_q], 0)[3], K[n_q:].double()]),
+            torch.cat([code(V[:n_q], 2)[3], V[n_q:].double()]), n_q)
+
+
+def attention(q, K, V, n_q, k=None, v=None):
+    """Rows q [n, H_q, D] of one sequence over its cached K, V [T, H, D] (fp64, n_q of them coded) and its new k, v.
+    Returns the result in fp64 and a bound on a kernel's error."""
+    n, H_q, D = q.shape
+    dt = q.dtype
+    T = K.shape[0]
+    if k is not None:
+        K, V = torch.cat([K, k.double()]), torch.cat([V, v.double()])
+    rows = torch.arange(n, device=q.device)[:, None]
+    seen = torch.arange(K.shape[0], device=q.device)[None] <= (rows + T if k is not None else T - 1 + 0 * rows)
+    out = torch.zeros((n, H_q, D), dtype=torch.float64, device=q.device)
+    bound = torch.zeros_like(out)
+    if K.shape[0] == 0:
+        return out, bound
+    g = H_q // K.shape[1]
+    half = torch.finfo(dt).eps / 2            # half a step: bf16 2^-8, fp16 2^-11
+    for h in range(H_q):
+        u = h // g
+        qd = q[:, h].double()
+        kh, vh = K[:, u], V[:, u]
+        w = (qd @ kh.T / math.sqrt(D)).masked_fill(~seen, -math.inf)
+        p = torch.softmax(w, 1).nan_to_num(0.0)    # rows that see nothing: zeros
+        o = torch.where(p[:, :, None] != 0, p[:, :, None] * vh[None], 0.0).sum(1)
+        out[:, h] = o
+        vf = vh.nan_to_num(0.0, 0.0, 0.0)
+        # Scores: exact products, fp32 sums.  A matrix instruction adds 16 of them and may cut each of its additions at
+        # 2^-23; D/16 of those, as many for the zero and scale columns, the scaling and the exponent's argument: at
+        # most (D/8 + 4) 2^-23 of the sum of magnitudes, which is at most 4 |q| max|k| (z, s, and c' s each stay
+        # below twice the group's largest magnitude).
+        size = qd.abs() @ kh.nan_to_num(0.0, 0.0, 0.0).abs().amax(0) * 4 / math.sqrt(D)
+        ds = torch.expm1(size * (D / 8 + 4) * 2.0 ** -23 + 2.0 ** -21)
+        # Probabilities: ds and the exponential's 2^-22 in numerator and sum; rounded once (coded tokens: fp16, the
+        # others: the pool's type), with 2^-24 at the least against a sum of at least 1.  Coded values: one fp16
+        # rounding.
+        coded = torch.arange(len(kh), device=q.device) < n_q
+        up = torch.where(coded, 2.0 ** -11 + 2.0 ** -11 + 2.0 ** -22, half).double()
+        pv = torch.where(p[:, :, None] != 0, p[:, :, None] * vf.abs()[None], 0.0)
+        mag = pv.sum(1)
+        err = (pv * up[None, :, None]).sum(1) + mag * (2 * ds[:, None] + 2.0 ** -20)
+        err = err + seen.sum(1)[:, None] * 2.0 ** -24 * vf.abs().amax(0)[None]
+        bound[:, h] = err + (o.abs() + err) * half + (2.0 ** -25 if dt == torch.float16 else 0.0)
+    return out, bound
+
+
+def check(got, want, bound, what=""):
+    bad = (got.double() - want).abs() > bound
+    same = (got.double() == want) | (got.isnan() & want.isnan())
+    bad = bad & ~same | (got.isnan() != want.isnan())
+    assert not bad.any(), (what, int(bad.sum()), bad.numel(), bad.nonzero()[:4].tolist(),
+                           ((got.double() - want).abs() / bound).nan_to_num(0).max().item())

@@ -1,0 +1,483 @@
+"""The pool of cache pages: refusals on the CPU; codes, forks, copies,
+compaction and attention on the GPU against 64-bit forms."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import bit_asymmetric_kv_prefill_b200 as kivi
+from bit_asymmetric_kv_prefill_b200 import build as kbuild
+from tests import pool_reference as ref
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    kbuild.build()
+
+
+# ---- refusals (CPU) ---------------------------------------------------------------
+def _cfg(**kw):
+    base = dict(H_kv=2, D=64, G=32, R=128, dtype=kivi.KIVI_F16, pages=4, sequences=2, T_max=1024, workspace=None,
+                workspace_bytes=0)
+    base.update(kw)
+    return kivi.PoolConfig(*[base[f] for f, _ in kivi.PoolConfig._fields_])
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(H_kv=0), 1), (dict(D=0), 1), (dict(G=0), 1), (dict(R=0), 1), (dict(T_max=0), 1), (dict(pages=-1), 1),
+    (dict(sequences=0), 1), (dict(dtype=2), 1), (dict(R=100), 1), (dict(D=96), 2), (dict(D=80), 1),
+    (dict(G=16, R=128), 2), (dict(T_max=(1 << 30) + 1), 2), (dict(H_kv=5000), 2),
+    (dict(sequences=1 << 20, T_max=1 << 20, R=32), 2), (dict(R=1 << 21), 2),
+])
+def test_bad_pool_configs(kw, code):
+    cfg, h, n = _cfg(**kw), ctypes.c_void_p(), ctypes.c_size_t()
+    assert kivi.lib().kivi_pool_create(ctypes.byref(cfg), ctypes.byref(h)) == code and not h.value
+    assert kivi.lib().kivi_pool_required_bytes(ctypes.byref(cfg), ctypes.byref(n)) == code
+
+
+def test_pool_bytes_follow_the_layout():
+    """Pages of H*R*D tokens at 0.75 bytes an element (K and V), residuals at 4, one table entry per page."""
+    small, more = _cfg(pages=10), _cfg(pages=42)
+    a, b = ctypes.c_size_t(), ctypes.c_size_t()
+    L = kivi.lib()
+    assert L.kivi_pool_required_bytes(ctypes.byref(small), ctypes.byref(a)) == 0
+    assert L.kivi_pool_required_bytes(ctypes.byref(more), ctypes.byref(b)) == 0
+    assert b.value - a.value == 32 * 2 * 128 * 64 * 3 // 4
+
+
+def test_null_pools_are_refused():
+    L = kivi.lib()
+    n = ctypes.c_int()
+    i64 = ctypes.c_longlong()
+    assert L.kivi_pool_create(None, None) == 1
+    assert L.kivi_pool_destroy(None) == 1
+    assert L.kivi_pool_open(None, 1, ctypes.byref(n)) == 1
+    assert L.kivi_pool_free(None, ctypes.byref(n), 1) == 1
+    assert L.kivi_pool_extend(None, ctypes.byref(n), ctypes.byref(n), 1, None, None, None) == 1
+    assert L.kivi_pool_attn(None, ctypes.byref(n), ctypes.byref(n), 1, None, None, None, 2, None, None) == 1
+    assert L.kivi_pool_gather(None, ctypes.byref(n), 1, None, None, None) == 1
+    assert L.kivi_pool_fork(None, ctypes.byref(n), 1, ctypes.byref(n), None) == 1
+    assert L.kivi_pool_copy(None, ctypes.byref(n), 1, ctypes.byref(n), None) == 1
+    assert L.kivi_pool_compact(None, None, None) == 1
+    assert L.kivi_pool_length(None, 0, ctypes.byref(i64), ctypes.byref(n)) == 1
+    assert L.kivi_pool_pages(None, 0, None, 0, ctypes.byref(n)) == 1
+    assert L.kivi_pool_usage(None, None, None, None) == 1
+    assert L.kivi_pool_device_status(None, ctypes.byref(n)) == 1
+    assert L.kivi_pool_export(None, 0, 0, *([None] * 8)) == 1
+
+
+# ---- helpers (GPU) ------------------------------------------------------------------
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+
+
+def _tokens(n, H, D, dtype, seed, outliers=True):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    K = torch.randn((n, H, D), generator=g, device="cuda")
+    if outliers:
+        K[:, :, 3] *= 100.0
+        K[:, :, D // 2 + 1] *= 20.0
+    return K.to(dtype), torch.randn((n, H, D), generator=g, device="cuda").to(dtype)
+
+
+def _pool(H, D, dtype, R=128, pages=64, sequences=16, T_max=1 << 16):
+    return kivi.KiviPool(pages=pages, sequences=sequences, H_kv=H, D=D, R=R, dtype=dtype, T_max=T_max)
+
+
+def _same_store(pool, seq, K, V):
+    """Codes, scales, zeros and residual of a sequence, bit for bit."""
+    R, H = pool.R, pool.H_kv
+    n_q = R * ((len(K) - 1) // R) if len(K) else 0
+    assert pool.length(seq) == (n_q, len(K) - n_q)
+    if n_q:
+        ck, sk, zk, _ = ref.code(K[:n_q], 0)
+        cv, sv, zv, _ = ref.code(V[:n_q], 2)
+    for h in range(H):
+        got = pool.export(seq, h)
+        bits = lambda t: t.contiguous().view(torch.int16).cpu().numpy().view(np.uint16)  # noqa: E731
+        if n_q:
+            assert np.array_equal(got["codesK"], ck[:, h].cpu().numpy())
+            assert np.array_equal(got["codesV"], cv[:, h].cpu().numpy())
+            for name, t in (("sK", sk[:, h]), ("zK", zk[:, h]), ("sV", sv[:, h]), ("zV", zv[:, h])):
+                t = torch.where(t == 0, torch.zeros_like(t), t)   # a stored zero is +0
+                assert np.array_equal(got[name], bits(t)), name
+        assert np.array_equal(got["resK"], bits(K[n_q:, h])) and np.array_equal(got["resV"], bits(V[n_q:, h]))
+
+
+# ---- the store (GPU) -----------------------------------------------------------------
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,D,dtype,R,T", [
+    (2, 64, "fp16", 128, 1), (2, 64, "fp16", 128, 128), (2, 64, "bf16", 128, 129), (3, 128, "bf16", 128, 1000),
+    (1, 128, "fp16", 32, 33), (2, 128, "bf16", 32, 200), (2, 64, "bf16", 96, 500), (5, 128, "fp16", 256, 1025),
+])
+def test_extend_codes_bit_for_bit(H, D, dtype, R, T):
+    """One chunk, and the same tokens in uneven chunks: the store of the definition."""
+    K, V = _tokens(T, H, D, DT[dtype], T)
+    pool = _pool(H, D, DT[dtype], R, pages=80)
+    a, b = pool.open(2)
+    pool.extend([a], K, V, [T])
+    _same_store(pool, a, K, V)
+    at, step = 0, 1
+    while at < T:
+        n = min(step, T - at)
+        pool.extend([b], K[at:at + n], V[at:at + n], [n])
+        at += n
+        step = (step * 7 + 3) % 190 + 1
+    _same_store(pool, b, K, V)
+
+
+@pytest.mark.gpu
+def test_extend_matches_the_contiguous_cache():
+    """The same bits as kivi_prefill and kivi_append leave (through both exports)."""
+    H, D, T = 2, 128, 500
+    K, V = _tokens(T + 40, H, D, torch.bfloat16, 5)
+    c = kivi.KiviCache(1, H, D, 32, 128, torch.bfloat16, T + 40)
+    c.prefill(K[:T].transpose(0, 1).contiguous()[None], V[:T].transpose(0, 1).contiguous()[None])
+    pool = _pool(H, D, torch.bfloat16)
+    s, = pool.open()
+    pool.extend([s], K[:T], V[:T], [T])
+    for t in range(T, T + 40):
+        c.append(K[t][None].contiguous(), V[t][None].contiguous())
+        pool.extend([s], K[t:t + 1], V[t:t + 1])
+    want = c.export()
+    for h in range(H):
+        got = pool.export(s, h)
+        for name in got:
+            assert np.array_equal(got[name], want[name][h].reshape(got[name].shape)), name
+
+
+@pytest.mark.gpu
+def test_ragged_extend_strided_rows_and_constant_groups():
+    H, D, R = 2, 128, 64
+    lens = [1, 0, 65, 300, 64, 7]
+    N = sum(lens)
+    qkv = torch.randn(N, (4 + 2 * H) * D + 8, device="cuda").to(torch.float16)
+    k, v = qkv[:, 4 * D:(4 + H) * D].unflatten(1, (H, D)), qkv[:, (4 + H) * D:(4 + 2 * H) * D].unflatten(1, (H, D))
+    k[70:140] = 0.5          # constant key and value groups: scale 0, codes 0
+    v[100:120] = -0.0
+    pool = _pool(H, D, torch.float16, R)
+    seqs = pool.open(len(lens))
+    for half in (0, 1):
+        n = [x // 2 if half == 0 else x - x // 2 for x in lens]
+        rows = []
+        for i, x in enumerate(lens):
+            a = sum(lens[:i]) + (0 if half == 0 else x // 2)
+            rows += list(range(a, a + n[i]))
+        idx = torch.tensor(rows, device="cuda")
+        wide = qkv[idx]
+        pool.extend(seqs, wide[:, 4 * D:(4 + H) * D].unflatten(1, (H, D)),
+                    wide[:, (4 + H) * D:(4 + 2 * H) * D].unflatten(1, (H, D)), n)
+    for i, s in enumerate(seqs):
+        a = sum(lens[:i])
+        _same_store(pool, s, k[a:a + lens[i]], v[a:a + lens[i]])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,dtype,R", [(64, "bf16", 32), (128, "fp16", 128), (128, "bf16", 96)])
+def test_gather_decodes(D, dtype, R):
+    H, lens = 3, [0, 5, R, R + 1, 700]
+    pool = _pool(H, D, DT[dtype], R, pages=80)
+    seqs = pool.open(len(lens))
+    K, V = _tokens(sum(lens), H, D, DT[dtype], 3)
+    pool.extend(seqs, K, V, lens)
+    order = [4, 1, 0, 3, 4, 2]
+    gk, gv = pool.gather([seqs[i] for i in order])
+    at = 0
+    for i in order:
+        a = sum(lens[:i])
+        wk, wv, _ = ref.cached(K[a:a + lens[i]], V[a:a + lens[i]], R)
+        # zero + scale*code in fp32, then one rounding: equal to rounding the fp64 value through fp32.
+        assert torch.equal(gk[at:at + lens[i]], wk.float().to(DT[dtype]))
+        assert torch.equal(gv[at:at + lens[i]], wv.float().to(DT[dtype]))
+        at += lens[i]
+
+
+@pytest.mark.gpu
+def test_fork_copy_free_compact():
+    H, D, R = 2, 64, 32
+    pool = _pool(H, D, torch.bfloat16, R, pages=40, sequences=8)
+    K, V = _tokens(400, H, D, torch.bfloat16, 9)
+    a, b = pool.open(2)
+    pool.extend([a, b], K[:300], V[:300], [100, 200])       # 3 and 6 pages
+    assert pool.usage() == dict(pages_used=9, pages_end=9, sequences_open=2)
+    f1, f2, g = pool.fork([a, a, b])
+    assert pool.usage()["pages_used"] == 9 and pool.pages_of(f1) == pool.pages_of(a)
+    pool.extend([f1, f2, a], K[300:400], V[300:400], [40, 50, 10])   # branches go their own way
+    tail = {a: (390, 400), f1: (300, 340), f2: (340, 390)}
+    hist = {s: (torch.cat([K[:100], K[x:y]]), torch.cat([V[:100], V[x:y]])) for s, (x, y) in tail.items()}
+    hist[b] = hist[g] = (K[100:300], V[100:300])
+    for s, (k, v) in hist.items():
+        _same_store(pool, s, k, v)
+    c, = pool.copy([f2])
+    hist[c] = hist[f2]
+    assert not set(pool.pages_of(c)) & set(pool.pages_of(f2))
+    pool.free([f1, a])
+    del hist[f1], hist[a]
+    used = pool.usage()["pages_used"]
+    assert pool.compact() > 0
+    assert pool.usage()["pages_used"] == pool.usage()["pages_end"] == used
+    assert pool.compact() == 0
+    for s, (k, v) in hist.items():
+        _same_store(pool, s, k, v)
+    d, = pool.open()
+    pool.extend([d], K[:200], V[:200], [200])                # freed pages serve again
+    _same_store(pool, d, K[:200], V[:200])
+    for s, (k, v) in hist.items():
+        _same_store(pool, s, k, v)
+    pool.free(list(hist) + [d])
+    assert pool.usage() == dict(pages_used=0, pages_end=0, sequences_open=0)
+
+
+@pytest.mark.gpu
+def test_capacity_and_state_errors_leave_the_pool_unchanged():
+    H, D, R = 1, 64, 32
+    pool = _pool(H, D, torch.float16, R, pages=3, sequences=2, T_max=150)
+    K, V = _tokens(200, H, D, torch.float16, 1)
+    a, = pool.open()
+    pool.extend([a], K[:90], V[:90], [90])                   # 2 pages
+
+    def refused(code, call):
+        before = (pool.usage(), pool.length(a))
+        with pytest.raises(kivi.KiviError) as e:
+            call()
+        assert e.value.code == code and (pool.usage(), pool.length(a)) == before
+
+    refused(3, lambda: pool.extend([a], K[:70], V[:70], [70]))          # past T_max
+    refused(3, lambda: pool.extend([a], K[:60], V[:60], [60]))          # needs 2 more pages
+    refused(3, lambda: pool.copy([a]))
+    refused(3, lambda: pool.fork([a, a]))                               # one sequence left
+    refused(3, lambda: pool.open(2))
+    refused(1, lambda: pool.extend([a, a], K[:2], V[:2], [1, 1]))       # twice
+    refused(1, lambda: pool.extend([1], K[:1], V[:1], [1]))             # not open
+    refused(1, lambda: pool.extend([7], K[:1], V[:1], [1]))
+    refused(1, lambda: pool.free([a, a]))
+    refused(1, lambda: pool.fork([-1]))
+    L, one = kivi.lib(), lambda x: (ctypes.c_int * 1)(x)  # noqa: E731
+    good = kivi.PoolRows(K.data_ptr(), 64, 64)
+
+    def raw_extend(n, rows):
+        kivi.pool._check(L.kivi_pool_extend(pool._h, one(a), one(n), 1, rows, rows, None), "")
+
+    def raw_attend(n, q, k, v, H_q, out):
+        kivi.pool._check(L.kivi_pool_attn(pool._h, one(a), one(n), 1, q, k, v, H_q, out, None), "")
+
+    refused(1, lambda: raw_extend(-1, ctypes.byref(good)))
+    refused(1, lambda: raw_extend(1, None))
+    refused(1, lambda: raw_extend(1, ctypes.byref(kivi.PoolRows(K.data_ptr() + 2, 64, 64))))
+    refused(1, lambda: raw_extend(1, ctypes.byref(kivi.PoolRows(K.data_ptr(), 68, 64))))
+    g, out = ctypes.byref(good), V.data_ptr()
+    refused(1, lambda: raw_attend(-1, g, g, g, 1, out))
+    refused(1, lambda: raw_attend(1, None, g, g, 1, out))
+    refused(1, lambda: raw_attend(1, g, g, None, 1, out))
+    refused(1, lambda: raw_attend(1, g, g, g, 0, out))
+    refused(1, lambda: raw_attend(1, g, g, g, 1, None))
+    refused(1, lambda: raw_attend(1, g, g, g, 1, out + 4))
+    refused(2, lambda: raw_attend(1, g, g, g, 65537, out))
+    with pytest.raises(ValueError):
+        pool.extend([a], K[:1].float(), V[:1].float(), [1])
+    with pytest.raises(ValueError):
+        pool.extend([a], K[:2], V[:2], [1])
+    with pytest.raises(ValueError):
+        pool.attend([a], K[:1], K[:1], None, [1])
+    pool.extend([a], K[90:100], V[90:100], [10])
+    _same_store(pool, a, K[:100], V[:100])
+
+
+@pytest.mark.gpu
+def test_a_workspace_holds_everything():
+    H, D = 2, 64
+    n = kivi.KiviPool.required_bytes(8, 2, H, D, dtype=torch.float16, T_max=1024)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    pool = kivi.KiviPool(8, 2, H, D, dtype=torch.float16, T_max=1024, workspace=ws)
+    K, V = _tokens(300, H, D, torch.float16, 2)
+    s, = pool.open()
+    pool.extend([s], K, V, [300])
+    _same_store(pool, s, K, V)
+    with pytest.raises(kivi.KiviError) as e:
+        kivi.KiviPool(8, 2, H, D, dtype=torch.float16, T_max=1024, workspace=ws[:n - 1])
+    assert e.value.code == 5
+    with pytest.raises(kivi.KiviError) as e:
+        kivi.KiviPool(8, 2, H, D, dtype=torch.float16, T_max=1024, workspace=torch.cat([ws, ws])[16:])
+    assert e.value.code == 1
+
+
+# ---- attention (GPU) ------------------------------------------------------------------
+def _case(H, g, D, dtype, R, T, n, seed, with_new=True, pages=None):
+    """A pool with sequences of T[i] tokens, and n[i] new rows each, checked against the 64-bit form."""
+    dt = DT[dtype]
+    pool = _pool(H, D, dt, R, pages=pages or sum(t // R + 1 for t in T) + 2, sequences=len(T) + 1)
+    seqs = pool.open(len(T))
+    K, V = _tokens(sum(T), H, D, dt, seed)
+    if sum(T):
+        pool.extend(seqs, K, V, T)
+    N = sum(n)
+    k, v = _tokens(N, H, D, dt, seed + 1)
+    q = torch.randn((N, H * g, D), generator=torch.Generator(device="cuda").manual_seed(seed + 2), device="cuda").to(dt)
+    q = q * 0.3 if seed % 2 else q
+    return pool, seqs, K, V, q, k, v
+
+
+def _verify(pool, out, T, n, K, V, q, k, v, R):
+    for i in range(len(T)):
+        a, b = sum(T[:i]), sum(n[:i])
+        Kc, Vc, n_q = ref.cached(K[a:a + T[i]], V[a:a + T[i]], R)
+        rows = slice(b, b + n[i])
+        want, bound = ref.attention(q[rows], Kc, Vc, n_q, *((k[rows], v[rows]) if k is not None else ()))
+        ref.check(out[rows], want, bound, f"sequence {i}")
+    assert pool.device_status() == 0
+
+
+ATTN = [
+    # H, group, D, dtype, R, cached, new
+    (1, 1, 64, "fp16", 128, [0], [1]),
+    (2, 1, 64, "fp16", 128, [256], [1]),
+    (2, 1, 128, "bf16", 128, [1], [1]),
+    (2, 4, 128, "bf16", 128, [129, 1000], [1, 1]),
+    (3, 2, 64, "bf16", 32, [500, 0, 33], [1, 2, 3]),
+    (2, 8, 128, "fp16", 64, [700, 64, 65], [5, 1, 4]),
+    (1, 3, 128, "bf16", 128, [300], [17]),
+    (2, 5, 64, "fp16", 96, [1000, 10], [7, 40]),
+    (1, 1, 128, "fp16", 128, [4000], [33]),
+    (2, 4, 128, "bf16", 128, [640, 0], [100, 150]),
+    (1, 12, 64, "bf16", 32, [95], [50]),
+    (1, 4, 128, "fp16", 128, [0], [300]),
+    (8, 4, 128, "bf16", 128, [9000], [1]),
+    (2, 2, 64, "bf16", 128, [1500, 700, 128, 1], [0, 129, 64, 257]),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,g,D,dtype,R,T,n", ATTN)
+def test_attention_of_new_tokens(H, g, D, dtype, R, T, n):
+    pool, seqs, K, V, q, k, v = _case(H, g, D, dtype, R, T, n, seed=sum(T) + sum(n))
+    out = pool.attend(seqs, q, k, v, n)
+    _verify(pool, out, T, n, K, V, q, k, v, R)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,g,D,dtype,R,T,n", [
+    (2, 4, 128, "bf16", 128, [1000, 0, 5], [1, 2, 1]),
+    (2, 1, 64, "fp16", 32, [96, 97], [1, 1]),
+    (1, 2, 128, "fp16", 64, [300, 0], [70, 90]),
+])
+def test_attention_over_the_cache_alone(H, g, D, dtype, R, T, n):
+    """Without new keys every row sees what is cached; a row that sees nothing is zero."""
+    pool, seqs, K, V, q, _, _ = _case(H, g, D, dtype, R, T, n, seed=7)
+    out = pool.attend(seqs, q, None, None, n)
+    _verify(pool, out, T, n, K, V, q, None, None, R)
+    for i, t in enumerate(T):
+        if t == 0:
+            assert (out[sum(n[:i]):sum(n[:i + 1])] == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [3, 150])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_values_that_are_not_finite_stay_with_the_rows_that_see_them(n, dtype):
+    H, g, D, R, T = 1, 4, 128, 128, 200
+    pool, seqs, K, V, q, k, v = _case(H, g, D, dtype, R, [T], [n], seed=12)
+    late = n - 2
+    v[late, 0, 5] = float("nan")
+    v[late + 1, 0, 9] = float("inf")
+    k[n - 1, 0, 2] = float("nan")
+    out = pool.attend(seqs, q, k, v, [n])
+    Kc, Vc, n_q = ref.cached(K, V, R)
+    want, bound = ref.attention(q[:late], Kc, Vc, n_q, k[:late], v[:late])
+    ref.check(out[:late], want, bound)
+    assert out[late, :, 5].isnan().all() and out[late, :, 6].isfinite().all()
+    assert out[late + 1].isnan().all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [2, 140])
+def test_strided_rows_repeats_and_rows_left_alone(n):
+    H, g, D, R = 2, 2, 64, 32
+    pool, seqs, K, V, q, k, v = _case(H, g, D, "fp16", R, [150, 70], [n, n], seed=21)
+    buf = torch.zeros(2 * n, (H * g + 2 * H + 1) * D, device="cuda", dtype=torch.float16)
+    view = lambda h0, h: buf[:, h0 * D:(h0 + h) * D].unflatten(1, (h, D))  # noqa: E731
+    view(0, H * g).copy_(q), view(H * g, H).copy_(k), view(H * g + H, H).copy_(v)
+    out = torch.full((2 * n + 3, H * g, D), 7.0, device="cuda", dtype=torch.float16)
+    pool.attend(seqs, view(0, H * g), view(H * g, H), view(H * g + H, H), [n, n], out=out[:2 * n])
+    assert torch.equal(out[:2 * n], pool.attend(seqs, q, k, v, [n, n]))
+    assert (out[2 * n:] == 7.0).all()
+    # The same sequence twice: the same rows twice (the split of the work, and so the last bits, may differ).
+    both = pool.attend([seqs[0], seqs[0]], torch.cat([q[:n], q[:n]]), torch.cat([k[:n], k[:n]]),
+                       torch.cat([v[:n], v[:n]]), [n, n])
+    _verify(pool, both[:n], [150], [n], K[:150], V[:150], q[:n], k[:n], v[:n], R)
+    _verify(pool, both[n:], [150], [n], K[:150], V[:150], q[:n], k[:n], v[:n], R)
+
+
+@pytest.mark.gpu
+def test_attention_on_streams_and_in_graphs():
+    """Repeats are bit-equal; a captured call replays on new inputs; two graphs that share the scratch, replayed one
+    after the other, keep their results."""
+    H, g, D, R = 2, 4, 128, 128
+    pool, seqs, K, V, q, k, v = _case(H, g, D, "bf16", R, [2000, 900], [1, 130], seed=4)
+    args = (q, k, v)
+    want = pool.attend(seqs, *args, [1, 130])
+    assert torch.equal(want, pool.attend(seqs, *args, [1, 130]))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out = torch.empty_like(want)
+    pool.attend(seqs, *args, [1, 130], out=out, stream=s)
+    s.synchronize()
+    assert torch.equal(out, want)
+    o1, o2 = torch.zeros_like(want), torch.zeros_like(want[:1])
+    torch.cuda.synchronize()
+    g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g1):
+        pool.attend(seqs, *args, [1, 130], out=o1)
+    with torch.cuda.graph(g2):
+        pool.attend(seqs[:1], q[:1], k[:1], v[:1], [1], out=o2)
+    one = pool.attend(seqs[:1], q[:1], k[:1], v[:1], [1])
+    for _ in range(3):
+        g1.replay()
+        g2.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o1, want) and torch.equal(o2, one)
+    q.mul_(0.5)
+    g1.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o1, pool.attend(seqs, *args, [1, 130]))
+
+
+@pytest.mark.gpu
+def test_a_serving_run():
+    """Rotate, attend, extend and branch as a serving loop does: every step against the 64-bit form."""
+    H, g, D, R, dt = 2, 2, 64, 32, torch.bfloat16
+    pool = _pool(H, D, dt, R, pages=64, sequences=8)
+    f, m = kivi.rope_frequencies(D)
+    hist = {}
+
+    def step(seqs, n, seed):
+        N = sum(n)
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        qkv = torch.randn((N, (H * g + 2 * H), D), generator=gen, device="cuda").to(dt)
+        pos = torch.cat([torch.arange(x) + len(hist[s][0]) for s, x in zip(seqs, n)]).to("cuda", torch.int32)
+        q, k = kivi.rope(qkv[:, :H * g], qkv[:, H * g:H * g + H], pos, f, scale=m)
+        v = qkv[:, H * g + H:]
+        out = pool.attend(seqs, q, k, v, n)
+        pool.extend(seqs, k, v, n)
+        at = 0
+        for s, x in zip(seqs, n):
+            Kh, Vh = hist[s]
+            Kc, Vc, n_q = ref.cached(Kh, Vh, R)
+            rows = slice(at, at + x)
+            ref.check(out[rows], *ref.attention(q[rows], Kc, Vc, n_q, k[rows], v[rows]))
+            hist[s] = (torch.cat([Kh, k[rows]]), torch.cat([Vh, v[rows]]))
+            at += x
+
+    empty = torch.zeros((0, H, D), device="cuda", dtype=dt)
+    seqs = pool.open(3)
+    hist.update({s: (empty, empty) for s in seqs})
+    step(seqs, [40, 70, 1], 1)
+    for i in range(4):
+        step(seqs, [1, 1, 1], 10 + i)
+    a, b = pool.fork([seqs[1], seqs[1]])
+    hist[a] = hist[b] = hist[seqs[1]]
+    step([a, b, seqs[0]], [5, 33, 2], 20)
+    pool.free([seqs[1]])
+    pool.compact()
+    step([seqs[0], a, seqs[2], b], [1, 1, 64, 1], 30)
+    for s in (seqs[0], seqs[2], a, b):
+        _same_store(pool, s, *hist[s])
