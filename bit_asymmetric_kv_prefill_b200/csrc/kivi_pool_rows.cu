@@ -1,24 +1,37 @@
-// kivi_pool_rows.cu -- attention of new tokens over a pool's pages, 16 rows
-// (token, head of one kv head) at a time, split over the cache's length.
+// kivi_pool_rows.cu -- attention of new tokens over a pool's pages, 8 to 24
+// rows (token, head of one kv head) at a time, split over the cache's length.
+//
+// Products are transposed, scores [32 tokens x 8 rows] and outputs
+// [channels x 8 rows]: the decoded codes are the 16-row operand A of
+// m16n8k16 and the few query rows the 8-column operand B, so that one query
+// head wastes 7 of 8 columns and not 15 of 16 rows, and a decoded fragment
+// serves every 8 rows of the tile.
 //
 // Scores.  A key group (32 tokens of one channel d) decodes to z_d + s_d c,
 // c in 0..3.  With c' = c - 1 in {-1, 0, 1, 2}, s_d c' is exact in fp16, so
 //   q . x^ = sum_d q_d (s_d c'_d) + sum_d q_d (z_d + s_d)
-// takes exact products only: the first sum on the matrix units over the 32
-// tokens, the second once per group (z and s are two more columns), as the
-// first one's initial accumulator.  Outlier key channels (100 times the
-// others) would otherwise cost the scores their accuracy.  Queries are fp16
-// there, bf16 ones scaled by a power of two per row (exact).
-// Values decode to fp16(z + s c), one rounding; probabilities are fp16
-// (relative 2^-11, absolute 2^-25 against a maximum of at least 2^-8), sums
-// and outputs fp32.  Tokens not yet coded take the same products in their own
-// type, straight from their rows.
+// takes exact products only: the first sum over the 32 tokens, the second
+// once per group (rows of z and of s against the queries), as the first
+// one's initial accumulator.  Outlier key channels (100 times the others)
+// would otherwise cost the scores their accuracy.  Queries are fp16 there,
+// bf16 ones scaled by a power of two per row (exact).
 //
-// A warp owns 16 rows and a range of the work: the (sequence, row tile, kv
+// Values.  sum_t p_t (z_t + s_t c_t) = sum_t (p_t s_t) c_t + sum_t p_t z_t:
+// the codes enter as they are (a masked word is a pair of fp16 subnormals
+// c 4^k 2^-24, exact, the power taken out at the end), the probabilities are
+// multiplied by the four groups' scales and rounded once to fp16, and the z of
+// the 32-channel groups are four rows of one more product.  p is kept
+// multiplied by 2^-E with E following the largest s seen, so that p s neither
+// overflows nor loses bits below 2^-24.
+//
+// Tokens not yet coded take the same products in their own type, straight
+// from their rows.
+//
+// A warp owns a row tile and a range of the work: the (sequence, row tile, kv
 // head) segments lie one after another, 1 per key group and kRawWeight per 32
 // uncoded tokens, and the total is cut into equal ranges (so no sequence
 // length leaves a warp idle).  A segment inside one range is finished by its
-// warp; the others leave partial (max, sum, output) rows, at most two per
+// warp; the others leave partial (max, sum, output) fragments, at most two per
 // warp, which pool_join_kernel adds in a fixed order.
 // The 24*D-byte group blocks come through a per-warp ring of cp.async stages;
 // fragments are decoded in registers: the codes of the block are ordered so
@@ -32,10 +45,12 @@ namespace kivi {
 namespace {
 
 constexpr int kRowWarps = 4;        // warps per CTA
-constexpr int kRowCtas = 3;         // CTAs per SM (168 registers a thread)
 constexpr int kRowStages = 4;       // group blocks in flight per warp
 constexpr int kRawWeight = 2;       // cost of 32 uncoded tokens, in groups
-constexpr float kLazy = 8.0f;       // the running maximum follows when exceeded by 2^8
+constexpr float kLazy = 3.0f;       // the running maximum follows when exceeded by 2^kLazy
+constexpr int kMaxTiles = 3;        // 8-row tiles per warp
+// CTAs per SM of a kernel with NT tiles (128, 168, 255 registers a thread).
+constexpr int row_ctas(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
 
 // ---- fragments ------------------------------------------------------------------
 template <int DT>
@@ -52,6 +67,15 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
                      "{%0,%1,%2,%3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The transpose of an 8 x 8 tile of 16-bit elements: lane 4i + c holds
+// elements (i, 2c), (i, 2c + 1) before, (2c, i), (2c + 1, i) after.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
 }
 
 __device__ __forceinline__ __half2 as_h2(uint32_t u)
@@ -85,23 +109,28 @@ __device__ __forceinline__ float ex2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+// 2^k for -126 <= k <= 127.
+__device__ __forceinline__ float pow2(int k) { return __uint_as_float((uint32_t)(127 + k) << 23); }
 
-// The two codes of pair i of word w plus 2^(10 - 2k), as fp16 pairs (k = i % 5:
-// a code at mantissa bits 2k, 2k + 1 of a number with exponent 10 - 2k counts
-// ones).  Pairs 5 to 7 are read from the word shifted right by 10.
-__device__ __forceinline__ uint32_t code_bits(uint32_t w, uint32_t w10, int i)
+// Place k of pair i in a word (pairs 5 to 7 are read from the word shifted
+// right by 10): its codes sit at mantissa bits 2k, 2k + 1 of a half.
+__host__ __device__ constexpr int code_place(int i) { return i < 5 ? i : i - 5; }
+
+// c - 1 of pair i, as fp16: the codes on top of 2^(10 - 2k), where they count
+// ones, minus that and 1 (exact).
+__device__ __forceinline__ __half2 code_less_one(uint32_t w, uint32_t w10, int i)
 {
-    const int k = i < 5 ? i : i - 5;
-    const uint32_t mask = 0x00030003u << (2 * k);
-    const uint32_t one = (uint32_t)((25 - 2 * k) << 10) * 0x10001u;
-    return ((i < 5 ? w : w10) & mask) | one;
+    const int k = code_place(i);
+    uint32_t x;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;"
+        : "=r"(x)
+        : "r"(i < 5 ? w : w10), "r"(0x00030003u << (2 * k)), "r"((uint32_t)((25 - 2 * k) << 10) * 0x10001u));
+    return __hadd2(as_h2(x), __half2half2(__float2half_rn(-(float)((1 << (10 - 2 * k)) + 1))));
 }
-// Minus that offset, plus `less`, as an fp16 pair (exact).
-__device__ __forceinline__ __half2 code_offset(int i, int less)
+// c 4^k 2^-24 of pair i (fp16 subnormals).
+__device__ __forceinline__ uint32_t code_tiny(uint32_t w, uint32_t w10, int i)
 {
-    const int k = i < 5 ? i : i - 5;
-    const __half h = __float2half_rn(-(float)((1 << (10 - 2 * k)) + less));
-    return __half2half2(h);
+    return (i < 5 ? w : w10) & (0x00030003u << (2 * code_place(i)));
 }
 
 struct Seg {
@@ -129,9 +158,10 @@ __device__ __forceinline__ Seg find_segment(const AttnTab &t, const AttnCall &c,
     return s;
 }
 
+// w * tot < 2^63, see launch_pool_rows.
 __device__ __forceinline__ long long range_at(long long w, long long tot, long long warps)
 {
-    return (long long)((unsigned long long)(w * tot) / (unsigned long long)warps);   // w * tot < 2^63, see launch_pool_rows
+    return (long long)((unsigned long long)(w * tot) / (unsigned long long)warps);
 }
 
 template <int D>
@@ -143,9 +173,10 @@ struct RowsSmem {
     static_assert(32 * D * 2 <= RING, "value rows are staged in the ring");
 };
 
-// Partial result of a segment: 16 rows of D floats, then 16 (max, sum) pairs.
-template <int D>
-constexpr int kPartFloats = 16 * D + 32;
+// Partial result of a segment: per 8-row tile the D/16 output fragments
+// [fragment][4][lane], then per row (maximum, sum).
+template <int D, int NT>
+constexpr int kPartFloats = NT * (8 * D + 16);
 
 template <int D>
 __device__ __forceinline__ int chunk_at(int t, int c)
@@ -153,244 +184,348 @@ __device__ __forceinline__ int chunk_at(int t, int c)
     return (t * (D / 8) + (c ^ (t & 7))) * 16;
 }
 
-// Running softmax of the lane's two rows (lane/4 and lane/4 + 8) and their
-// output columns 8c + 2cs, + 1.
-template <int D>
+// Running softmax of the lane's rows 8a + 2cs, + 1 of every tile a, and their
+// outputs: fragment f holds channels 16f + tq (elements 0, 1) and + 8 (2, 3).
+// m is the reference of p: p = 2^(score - m).  l is the lane's own sum.
+template <int D, int NT>
 struct State {
-    float o[D / 8][4];
-    float m[2], l[2];
+    float o[NT][D / 16][4];
+    float m[NT][2], l[NT][2];
 };
 
-// Scores S (4 tiles of 8 tokens; already in units of log2) to probabilities in
-// place, moving the running maximum when a row exceeds it by 2^kLazy.
-template <int D>
-__device__ __forceinline__ void softmax_step(State<D> &st, float (&S)[4][4])
+// Moves the reference of row x of tile a to m (-inf: nothing seen yet).
+template <int D, int NT>
+__device__ __forceinline__ void rescale(State<D, NT> &st, float (*oz)[4], int a, int x, float m)
 {
-    float mx[2] = {fmaxf(S[0][0], S[0][1]), fmaxf(S[0][2], S[0][3])};
+    const float f = st.m[a][x] == -INFINITY ? 0.0f : ex2(st.m[a][x] - m);
+    st.m[a][x] = m;
+    st.l[a][x] *= f;
 #pragma unroll
-    for (int j = 1; j < 4; ++j) {
-        mx[0] = fmaxf(mx[0], fmaxf(S[j][0], S[j][1]));
-        mx[1] = fmaxf(mx[1], fmaxf(S[j][2], S[j][3]));
+    for (int k = 0; k < D / 16; ++k) {
+        st.o[a][k][x] *= f;
+        st.o[a][k][2 + x] *= f;
     }
-    const bool grow = mx[0] > st.m[0] + kLazy || mx[1] > st.m[1] + kLazy;
+    if (oz) {
+        oz[a][x] *= f;
+        oz[a][2 + x] *= f;
+    }
+}
+
+// Scores S (two 16-token fragments per tile, times sc in units of log2) to
+// probabilities in place.  The reference is e above a past maximum; it moves
+// when a score passes that maximum by kLazy.
+template <int D, int NT>
+__device__ __forceinline__ void softmax_step(State<D, NT> &st, float (*oz)[4], float (&S)[NT][2][4],
+                                             const float (&sc)[NT][2], float e)
+{
+    bool grow = false;
+    float mx[NT][2];
+#pragma unroll
+    for (int a = 0; a < NT; ++a)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            mx[a][x] = fmaxf(fmaxf(S[a][0][x], S[a][0][2 + x]), fmaxf(S[a][1][x], S[a][1][2 + x])) * sc[a][x];
+            grow = grow || mx[a][x] > st.m[a][x] + (kLazy - e);
+        }
     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-            const float m = fmaxf(st.m[r], mx[r]);
-            // A row that has seen nothing keeps a scale of 0 (its sums are 0).
-            const float f = st.m[r] == -INFINITY ? 0.0f : ex2(st.m[r] - m);
-            st.m[r] = m;
-            st.l[r] *= f;
+        for (int a = 0; a < NT; ++a)
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-                st.o[c][2 * r] *= f;
-                st.o[c][2 * r + 1] *= f;
+            for (int x = 0; x < 2; ++x) {
+                float v = mx[a][x];
+#pragma unroll
+                for (int b = 4; b < 32; b *= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, b));
+                v += e;
+                if (v > st.m[a][x]) rescale<D, NT>(st, oz, a, x, v);
+            }
+    }
+#pragma unroll
+    for (int a = 0; a < NT; ++a)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const float m = st.m[a][x] == -INFINITY ? 0.0f : st.m[a][x];
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                S[a][f][x] = ex2(fmaf(S[a][f][x], sc[a][x], -m));
+                S[a][f][2 + x] = ex2(fmaf(S[a][f][2 + x], sc[a][x], -m));
+                st.l[a][x] += S[a][f][x] + S[a][f][2 + x];
             }
         }
-    }
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const float m = st.m[r] == -INFINITY ? 0.0f : st.m[r];
-        float sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            S[j][2 * r] = ex2(S[j][2 * r] - m);
-            S[j][2 * r + 1] = ex2(S[j][2 * r + 1] - m);
-            sum += S[j][2 * r] + S[j][2 * r + 1];
-        }
-        st.l[r] += sum;
-    }
 }
 
 // One segment's items [i0, i1): groups below ng, then blocks of 32 residual
 // tokens, then blocks of 32 new tokens.
-template <int D, int DT>
+template <int D, int DT, int NT>
 __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, const Seg &sg, int i0, int i1,
-                                          uint8_t *sm, State<D> &st)
+                                          uint8_t *sm, State<D, NT> &st)
 {
     using L = PageLayout<D>;
-    constexpr int KU = D / 32, NC = D / 8, KW = L::KW;
+    constexpr int KU = D / 32, NF = D / 16, KW = L::KW, NJ = L::NJ;
     const int lane = threadIdx.x & 31, tq = lane >> 2, cs = lane & 3;
     const int e = sg.e, n = t.n[e], ng = t.ng[e], r_res = t.r[e], nk = t.nk[e], seq = t.seq[e];
     const PoolView &v = c.v;
+    const int row0 = 8 * NT * sg.rt;
 #pragma unroll
-    for (int k = 0; k < NC; ++k) st.o[k][0] = st.o[k][1] = st.o[k][2] = st.o[k][3] = 0.0f;
-    st.m[0] = st.m[1] = -INFINITY;
-    st.l[0] = st.l[1] = 0.0f;
+    for (int a = 0; a < NT; ++a) {
+#pragma unroll
+        for (int k = 0; k < NF; ++k) st.o[a][k][0] = st.o[a][k][1] = st.o[a][k][2] = st.o[a][k][3] = 0.0f;
+        st.m[a][0] = st.m[a][1] = -INFINITY;
+        st.l[a][0] = st.l[a][1] = 0.0f;
+    }
     int *first = (int *)(sm + RowsSmem<D>::FIRST);
     for (int d = lane; d < D; d += 32) first[d] = 0x7fffffff;
 
-    // The lane's rows: new token tok[k] and its head.
-    int tok[2];
-    const uint16_t *qp[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int row = 16 * sg.rt + tq + 8 * k;
-        tok[k] = row / c.group;
-        const bool real = tok[k] < n;
-        const int hq = sg.h * c.group + row - tok[k] * c.group;
-        qp[k] = real ? c.q.p + (long long)(t.row0[e] + tok[k]) * c.q.ts + hq * c.q.hs : nullptr;
-        if (!real) tok[k] = -1;
-    }
-    uint32_t qa[KU][4], qb[KU][4];
+    // Query fragments: row 8a + tq, channels 32u + 8cs + 0..7 in four words.
+    uint32_t qf[NT][KU][4];
     auto load_q = [&]() {
 #pragma unroll
-        for (int u = 0; u < KU; ++u) {
-            const uint4 z = make_uint4(0, 0, 0, 0);
-            *(uint4 *)qa[u] = qp[0] ? *(const uint4 *)(qp[0] + 32 * u + 8 * cs) : z;
-            *(uint4 *)qb[u] = qp[1] ? *(const uint4 *)(qp[1] + 32 * u + 8 * cs) : z;
+        for (int a = 0; a < NT; ++a) {
+            const int row = row0 + 8 * a + tq, tok = row / c.group;
+            const uint16_t *p = c.q.p + (long long)(t.row0[e] + tok) * c.q.ts
+                                + (long long)(sg.h * c.group + row - tok * c.group) * c.q.hs;
+#pragma unroll
+            for (int u = 0; u < KU; ++u)
+                *(uint4 *)qf[a][u] = tok < n ? *(const uint4 *)(p + 32 * u + 8 * cs) : make_uint4(0, 0, 0, 0);
         }
     };
+    int E = -12;   // p is kept times 2^-E
 
     // ---- coded groups ----
     const int g1 = min(i1, ng);
     if (i0 < g1) {
         load_q();
-        float sc[2] = {c.scale, c.scale};
+        float sc[NT][2];
+#pragma unroll
+        for (int a = 0; a < NT; ++a) sc[a][0] = sc[a][1] = c.scale;
         if constexpr (DT == KIVI_BF16) {
             // fp16 queries: each row times 2^k with its largest magnitude
             // brought to [2^13, 2^14).
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                uint32_t(&q)[KU][4] = r ? qb : qa;
+            for (int a = 0; a < NT; ++a) {
                 float mx = 0.0f;
 #pragma unroll
                 for (int u = 0; u < KU; ++u)
 #pragma unroll
                     for (int w = 0; w < 4; ++w)
-                        mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(q[u][w] << 16)),
-                                             fabsf(__uint_as_float(q[u][w] & 0xffff0000u))));
+                        mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(qf[a][u][w] << 16)),
+                                             fabsf(__uint_as_float(qf[a][u][w] & 0xffff0000u))));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                 int k = 13 - ((int)(__float_as_uint(mx) >> 23) - 127);
                 k = mx > 0.0f && mx < INFINITY ? max(-110, min(110, k)) : 0;
-                const float f = __uint_as_float((uint32_t)(127 + k) << 23);
-                sc[r] = c.scale * __uint_as_float((uint32_t)(127 - k) << 23);
+                const float f = pow2(k);
 #pragma unroll
                 for (int u = 0; u < KU; ++u)
 #pragma unroll
                     for (int w = 0; w < 4; ++w)
-                        q[u][w] = pack2<KIVI_F16>(__uint_as_float(q[u][w] << 16) * f,
-                                                  __uint_as_float(q[u][w] & 0xffff0000u) * f);
+                        qf[a][u][w] = pack2<KIVI_F16>(__uint_as_float(qf[a][u][w] << 16) * f,
+                                                      __uint_as_float(qf[a][u][w] & 0xffff0000u) * f);
+                // The scale of rows 2cs, 2cs + 1, from the lanes that hold them.
+#pragma unroll
+                for (int x = 0; x < 2; ++x) sc[a][x] *= pow2(-__shfl_sync(0xffffffffu, k, 4 * (2 * cs + x)));
             }
         }
+        float oz[NT][4];   // sum p z of channel group tq (tq < NJ)
+#pragma unroll
+        for (int a = 0; a < NT; ++a) oz[a][0] = oz[a][1] = oz[a][2] = oz[a][3] = 0.0f;
         const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm);
         const long long head_bytes = (long long)v.gpp * L::GB;
         const int *table = v.table + (long long)seq * v.max_pages;
-        int next_page = table[i0 / v.gpp];
-        auto issue = [&](int g) {
-            if (g < g1) {
-                const uint8_t *blk = v.packed + ((long long)next_page * v.H + sg.h) * head_bytes + (g % v.gpp) * L::GB;
-                const uint32_t to = ring + (uint32_t)((g - i0) % kRowStages) * L::GB;
+        // The next group to fetch: page by page.
+        int fetch = i0, in_page = i0 % v.gpp;
+        int page_i = i0 / v.gpp, next_page = table[page_i];
+        const uint8_t *src = nullptr;
+        auto issue = [&](int stage) {
+            if (fetch < g1) {
+                if (src == nullptr || in_page == v.gpp) {
+                    if (src != nullptr) in_page = 0;
+                    src = v.packed + ((long long)next_page * v.H + sg.h) * head_bytes + (long long)in_page * L::GB + lane * 16;
+                    ++page_i;
+                    if (page_i * v.gpp < g1) next_page = table[page_i];
+                }
+                const uint32_t to = ring + (uint32_t)stage * L::GB + lane * 16;
 #pragma unroll
                 for (int k = 0; k < L::GB / 512; ++k)
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + (k * 32 + lane) * 16),
-                                 "l"(blk + (k * 32 + lane) * 16)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + k * 512), "l"(src + k * 512)
                                  : "memory");
-                if (g + 1 < g1) next_page = table[(g + 1) / v.gpp];
+                src += L::GB;
+                ++in_page;
+                ++fetch;
             }
             cp_async_commit();
         };
-        for (int k = 0; k < kRowStages - 1; ++k) issue(i0 + k);
+        for (int k = 0; k < kRowStages - 1; ++k) issue(k);
+        int stage = 0;
 #pragma unroll 1
         for (int g = i0; g < g1; ++g) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kRowStages - 2) : "memory");
             __syncwarp();
-            issue(g + kRowStages - 1);   // into the stage that the last iteration has read
-            const uint8_t *blk = sm + ((g - i0) % kRowStages) * L::GB;
-            // Bias of the group: columns of even tq hold z, of odd tq s, so a
-            // lane's two columns add up to it.
-            float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int u = 0; u < KU; ++u) {
-                uint32_t z[4];
-                *(uint4 *)z = *(const uint4 *)(blk + ((tq & 1) ? L::KS : L::KZ) + u * 64 + cs * 16);
-                mma<KIVI_F16>(b, qa[u][0], qb[u][0], qa[u][1], qb[u][1], z[0], z[1]);
-                mma<KIVI_F16>(b, qa[u][2], qb[u][2], qa[u][3], qb[u][3], z[2], z[3]);
-            }
-            float S[4][4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                S[j][0] = S[j][1] = b[0] + b[1];
-                S[j][2] = S[j][3] = b[2] + b[3];
-            }
+            issue((stage + kRowStages - 1) % kRowStages);   // into the stage that the last iteration has read
+            const uint8_t *blk = sm + stage * L::GB;
+            stage = (stage + 1) % kRowStages;
+            float S[NT][2][4];
             {
+                // Rows 0..7 of A hold z, rows 8..15 s: elements 0, 1 and 2, 3
+                // of every lane add up to the bias of its rows.
+                float b[NT][4];
+#pragma unroll
+                for (int a = 0; a < NT; ++a) b[a][0] = b[a][1] = b[a][2] = b[a][3] = 0.0f;
                 uint32_t kw[L::WPL];
 #pragma unroll
                 for (int q = 0; q < L::WPL / 4; ++q)
                     *(uint4 *)(kw + 4 * q) = *(const uint4 *)(blk + L::KC + (q * 32 + lane) * 16);
+                uint32_t s[KU][4];
 #pragma unroll
                 for (int u = 0; u < KU; ++u) {
-                    uint32_t s[4];
-                    *(uint4 *)s = *(const uint4 *)(blk + L::KS + u * 64 + cs * 16);
+                    uint32_t z[4];
+                    *(uint4 *)s[u] = *(const uint4 *)(blk + L::KS + u * 64 + cs * 16);
+                    *(uint4 *)z = *(const uint4 *)(blk + L::KZ + u * 64 + cs * 16);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t w = kw[j * KW + u / 2], w10 = w >> 10;
-                        uint32_t f[4];
+                    for (int a = 0; a < NT; ++a) {
+                        mma<KIVI_F16>(b[a], z[0], s[u][0], z[1], s[u][1], qf[a][u][0], qf[a][u][1]);
+                        mma<KIVI_F16>(b[a], z[2], s[u][2], z[3], s[u][3], qf[a][u][2], qf[a][u][3]);
+                    }
+                }
+#pragma unroll
+                for (int a = 0; a < NT; ++a)
+#pragma unroll
+                    for (int f = 0; f < 2; ++f)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) S[a][f][x] = S[a][f][2 + x] = b[a][x] + b[a][2 + x];
+#pragma unroll
+                for (int u = 0; u < KU; ++u)
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
+                        const uint32_t w0 = kw[(2 * f) * KW + u / 2], w1 = kw[(2 * f + 1) * KW + u / 2];
+                        const uint32_t x0 = w0 >> 10, x1 = w1 >> 10;
+                        uint32_t k0[4], k1[4];
 #pragma unroll
                         for (int p = 0; p < 4; ++p) {
                             const int i = 4 * (u % 2) + p;
-                            f[p] = as_u(__hmul2(__hadd2(as_h2(code_bits(w, w10, i)), code_offset(i, 1)), as_h2(s[p])));
+                            k0[p] = as_u(__hmul2(code_less_one(w0, x0, i), as_h2(s[u][p])));
+                            k1[p] = as_u(__hmul2(code_less_one(w1, x1, i), as_h2(s[u][p])));
                         }
-                        mma<KIVI_F16>(S[j], qa[u][0], qb[u][0], qa[u][1], qb[u][1], f[0], f[1]);
-                        mma<KIVI_F16>(S[j], qa[u][2], qb[u][2], qa[u][3], qb[u][3], f[2], f[3]);
-                    }
-                }
-            }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                S[j][0] *= sc[0];
-                S[j][1] *= sc[0];
-                S[j][2] *= sc[1];
-                S[j][3] *= sc[1];
+                        for (int a = 0; a < NT; ++a) {
+                            mma<KIVI_F16>(S[a][f], k0[0], k1[0], k0[1], k1[1], qf[a][u][0], qf[a][u][1]);
+                            mma<KIVI_F16>(S[a][f], k0[2], k1[2], k0[3], k1[3], qf[a][u][2], qf[a][u][3]);
+                        }
+                    }
             }
-            softmax_step<D>(st, S);
-            uint32_t vw[L::WPL];
+            uint32_t vw[L::WPL], vs[4][NJ];
 #pragma unroll
             for (int q = 0; q < L::WPL / 4; ++q)
                 *(uint4 *)(vw + 4 * q) = *(const uint4 *)(blk + L::VC + (q * 32 + lane) * 16);
+            uint32_t big = 0;
 #pragma unroll
-            for (int mm = 0; mm < 2; ++mm) {
-                const uint32_t a0 = pack2<KIVI_F16>(S[2 * mm][0], S[2 * mm][1]);
-                const uint32_t a1 = pack2<KIVI_F16>(S[2 * mm][2], S[2 * mm][3]);
-                const uint32_t a2 = pack2<KIVI_F16>(S[2 * mm + 1][0], S[2 * mm + 1][1]);
-                const uint32_t a3 = pack2<KIVI_F16>(S[2 * mm + 1][2], S[2 * mm + 1][3]);
+            for (int p = 0; p < 4; ++p)
 #pragma unroll
                 for (int jh = 0; jh < KW; ++jh) {
-                    uint4 sz[2][2];   // [token half][group]: scales x, z of even group .. w of odd
+                    const uint4 q = *(const uint4 *)(blk + L::VM + page_vm_offset<D>(p, cs, 2 * jh));
+                    vs[p][2 * jh] = q.x;
+                    vs[p][2 * jh + 1] = q.z;
+                    big = __vimax3_s16x2(big, q.x, q.z);
+                }
+            // p s < 2^(kLazy - E) 2^(exponent + 1) has to stay below 2^15.
+            {
+                const int ex = (int)max(big >> 26, (big >> 10) & 31u) - 15;
+                if (__any_sync(0xffffffffu, ex + 1 + (int)kLazy - E > 15)) {
+                    int w = ex;
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        const uint4 q = *(const uint4 *)(blk + L::VM + page_vm_offset<D>(2 * mm + hf, cs, 2 * jh));
-                        sz[hf][0] = make_uint4(q.x, q.y, 0, 0);
-                        sz[hf][1] = make_uint4(q.z, q.w, 0, 0);
-                    }
-                    const uint32_t w0 = vw[(2 * mm) * KW + jh], w1 = vw[(2 * mm + 1) * KW + jh];
-                    const uint32_t x0 = w0 >> 10, x1 = w1 >> 10;
+                    for (int b = 1; b < 4; b *= 2) w = max(w, __shfl_xor_sync(0xffffffffu, w, b));
+                    const int up = max(0, w + 1 + (int)kLazy - 15 - E);
+                    E += up;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint4 p0 = sz[0][i / 4], p1 = sz[1][i / 4];
-                        const uint32_t f0 = as_u(__hfma2(__hadd2(as_h2(code_bits(w0, x0, i)), code_offset(i, 0)),
-                                                         as_h2(p0.x), as_h2(p0.y)));
-                        const uint32_t f1 = as_u(__hfma2(__hadd2(as_h2(code_bits(w1, x1, i)), code_offset(i, 0)),
-                                                         as_h2(p1.x), as_h2(p1.y)));
-                        mma<KIVI_F16>(st.o[8 * jh + i], a0, a1, a2, a3, f0, f1);
+                    for (int a = 0; a < NT; ++a)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            if (st.m[a][x] != -INFINITY) rescale<D, NT>(st, oz, a, x, st.m[a][x] + (float)up);
+                }
+            }
+            softmax_step<D, NT>(st, oz, S, sc, (float)E);
+            // P transposed: rows 8a + tq, token pairs 8p + 2cs.
+            uint32_t pt[NT][4];
+#pragma unroll
+            for (int a = 0; a < NT; ++a)
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    pt[a][2 * f] = transpose8(pack2<KIVI_F16>(S[a][f][0], S[a][f][1]));
+                    pt[a][2 * f + 1] = transpose8(pack2<KIVI_F16>(S[a][f][2], S[a][f][3]));
+                }
+            {
+                // Row tq of A: the zeros of channel group tq.
+                uint32_t z[4];
+#pragma unroll
+                for (int p = 0; p < 4; ++p)
+                    z[p] = tq < NJ ? *(const uint32_t *)(blk + L::VM + page_vm_offset<D>(p, cs, tq < NJ ? tq : 0) + 4) : 0u;
+#pragma unroll
+                for (int a = 0; a < NT; ++a) {
+                    mma<KIVI_F16>(oz[a], z[0], 0u, z[1], 0u, pt[a][0], pt[a][1]);
+                    mma<KIVI_F16>(oz[a], z[2], 0u, z[3], 0u, pt[a][2], pt[a][3]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                uint32_t ps[NT][4];
+#pragma unroll
+                for (int a = 0; a < NT; ++a)
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) ps[a][p] = as_u(__hmul2(as_h2(pt[a][p]), as_h2(vs[p][j])));
+                uint32_t w[4], x10[4];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    w[p] = vw[p * KW + j / 2];
+                    x10[p] = w[p] >> 10;
+                }
+#pragma unroll
+                for (int ff = 0; ff < 2; ++ff) {
+                    // Channel tiles 4j + 2ff, + 1: pairs i, i + 1 of their words.
+                    const int i = 4 * (j % 2) + 2 * ff;
+#pragma unroll
+                    for (int mm = 0; mm < 2; ++mm) {
+                        const uint32_t a0 = code_tiny(w[2 * mm], x10[2 * mm], i);
+                        const uint32_t a1 = code_tiny(w[2 * mm], x10[2 * mm], i + 1);
+                        const uint32_t a2 = code_tiny(w[2 * mm + 1], x10[2 * mm + 1], i);
+                        const uint32_t a3 = code_tiny(w[2 * mm + 1], x10[2 * mm + 1], i + 1);
+#pragma unroll
+                        for (int a = 0; a < NT; ++a)
+                            mma<KIVI_F16>(st.o[a][2 * j + ff], a0, a1, a2, a3, ps[a][2 * mm], ps[a][2 * mm + 1]);
                     }
                 }
             }
         }
         cp_async_wait_all();
         __syncwarp();
+        // Outputs in their own units: take out 4^k 2^-24, add the zeros' part.
+#pragma unroll
+        for (int a = 0; a < NT; ++a)
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int i = (2 * f + x / 2) % 8;
+                    const float z = __shfl_sync(0xffffffffu, oz[a][x & 1], 4 * (f / 2) + cs);
+                    st.o[a][f][x] = fmaf(st.o[a][f][x], (float)(1 << (24 - 2 * code_place(i))), z);
+                }
     }
 
     // ---- uncoded tokens, 32 at a time ----
     const int nres = (r_res + 31) / 32;
     if (i1 > ng) {
         load_q();
-        // The last new token that a row of the tile sees.
-        const int last_row = min(16 * sg.rt + 15, n * c.group - 1);
-        const int last_tok = min(nk - 1, last_row / c.group), first_tok = 16 * sg.rt / c.group;
+        float sc[NT][2];
+        int tok[NT][2];   // the new token of the lane's rows (-1: no such row)
+#pragma unroll
+        for (int a = 0; a < NT; ++a)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                sc[a][x] = c.scale;
+                tok[a][x] = (row0 + 8 * a + 2 * cs + x) / c.group;
+                if (tok[a][x] >= n) tok[a][x] = -1;
+            }
+        // The last new token that a row of the tile sees, the first row's token.
+        const int last_row = min(row0 + 8 * NT - 1, n * c.group - 1);
+        const int last_tok = min(nk - 1, last_row / c.group), first_tok = row0 / c.group;
 #pragma unroll 1
         for (int it = max(i0, ng); it < i1; ++it) {
             const bool is_new = it - ng >= nres;
@@ -421,30 +556,46 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
                              : "memory");
             }
             cp_async_commit();
-            float S[4][4];
+            float S[NT][2][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                S[j][0] = S[j][1] = S[j][2] = S[j][3] = 0.0f;
-                const int row = tq + 8 * j;
-                const bool real = row < cnt;
+            for (int a = 0; a < NT; ++a)
+#pragma unroll
+                for (int f = 0; f < 2; ++f) S[a][f][0] = S[a][f][1] = S[a][f][2] = S[a][f][3] = 0.0f;
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                const int ra = 16 * f + tq, rb = ra + 8;
 #pragma unroll
                 for (int u = 0; u < KU; ++u) {
-                    uint32_t f[4] = {0, 0, 0, 0};
-                    if (real) *(uint4 *)f = *(const uint4 *)(kp + row * kts + 32 * u + 8 * cs);
-                    mma<DT>(S[j], qa[u][0], qb[u][0], qa[u][1], qb[u][1], f[0], f[1]);
-                    mma<DT>(S[j], qa[u][2], qb[u][2], qa[u][3], qb[u][3], f[2], f[3]);
+                    uint32_t k0[4] = {0, 0, 0, 0}, k1[4] = {0, 0, 0, 0};
+                    if (ra < cnt) *(uint4 *)k0 = *(const uint4 *)(kp + ra * kts + 32 * u + 8 * cs);
+                    if (rb < cnt) *(uint4 *)k1 = *(const uint4 *)(kp + rb * kts + 32 * u + 8 * cs);
+#pragma unroll
+                    for (int a = 0; a < NT; ++a) {
+                        mma<DT>(S[a][f], k0[0], k1[0], k0[1], k1[1], qf[a][u][0], qf[a][u][1]);
+                        mma<DT>(S[a][f], k0[2], k1[2], k0[3], k1[3], qf[a][u][2], qf[a][u][3]);
+                    }
                 }
             }
             const bool masked = is_new && t0 + cnt - 1 > first_tok;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int a = 0; a < NT; ++a)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int col = 8 * j + 2 * cs + (k & 1);
-                    const bool seen = col < cnt && (!is_new || t0 + col <= tok[k >> 1]);
-                    S[j][k] = seen ? S[j][k] * c.scale : -INFINITY;
+                for (int f = 0; f < 2; ++f)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int col = 16 * f + tq + 8 * (x >> 1);
+                        const bool seen = col < cnt && (!is_new || t0 + col <= tok[a][x & 1]);
+                        if (!seen) S[a][f][x] = -INFINITY;
+                    }
+            softmax_step<D, NT>(st, nullptr, S, sc, (float)E);
+            uint32_t pt[NT][4];
+#pragma unroll
+            for (int a = 0; a < NT; ++a)
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    pt[a][2 * f] = transpose8(pack2<DT>(S[a][f][0], S[a][f][1]));
+                    pt[a][2 * f + 1] = transpose8(pack2<DT>(S[a][f][2], S[a][f][3]));
                 }
-            softmax_step<D>(st, S);
             cp_async_wait_all();
             __syncwarp();
             if (masked) {
@@ -473,43 +624,58 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
                 __syncwarp();
             }
 #pragma unroll
-            for (int mm = 0; mm < 2; ++mm) {
-                const uint32_t a0 = pack2<DT>(S[2 * mm][0], S[2 * mm][1]);
-                const uint32_t a1 = pack2<DT>(S[2 * mm][2], S[2 * mm][3]);
-                const uint32_t a2 = pack2<DT>(S[2 * mm + 1][0], S[2 * mm + 1][1]);
-                const uint32_t a3 = pack2<DT>(S[2 * mm + 1][2], S[2 * mm + 1][3]);
+            for (int f = 0; f < NF; ++f)
 #pragma unroll
-                for (int k = 0; k < NC; k += 2) {
-                    // Matrices: token halves of channel tiles k and k + 1.
-                    const int row = 16 * mm + (lane & 15), ch = k + (lane >> 4);
-                    uint32_t f[4];
+                for (int mm = 0; mm < 2; ++mm) {
+                    // Tiles (tokens 16mm + 0..7 and + 8..15) x (channels 16f + 0..7 and + 8..15).
+                    const int row = 16 * mm + (lane & 7) + 8 * (lane >> 4), ch = 2 * f + ((lane >> 3) & 1);
+                    uint32_t x[4];
                     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                                 : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
+                                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
                                  : "r"((uint32_t)__cvta_generic_to_shared(sm) + chunk_at<D>(row, ch))
                                  : "memory");
-                    mma<DT>(st.o[k], a0, a1, a2, a3, f[0], f[1]);
-                    mma<DT>(st.o[k + 1], a0, a1, a2, a3, f[2], f[3]);
+#pragma unroll
+                    for (int a = 0; a < NT; ++a)
+                        mma<DT>(st.o[a][f], x[0], x[1], x[2], x[3], pt[a][2 * mm], pt[a][2 * mm + 1]);
                 }
-            }
             __syncwarp();   // the staged values have been read
         }
+        __syncwarp();
+#pragma unroll
+        for (int a = 0; a < NT; ++a)
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    if (tok[a][x & 1] >= first[16 * f + tq + 8 * (x >> 1)]) st.o[a][f][x] = NAN;
     }
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        st.l[r] += __shfl_xor_sync(0xffffffffu, st.l[r], 1);
-        st.l[r] += __shfl_xor_sync(0xffffffffu, st.l[r], 2);
-    }
-    __syncwarp();
+    for (int a = 0; a < NT; ++a)
 #pragma unroll
-    for (int k = 0; k < NC; ++k)
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-            if (tok[x >> 1] >= first[8 * k + 2 * cs + (x & 1)]) st.o[k][x] = NAN;
+            for (int b = 4; b < 32; b *= 2) st.l[a][x] += __shfl_xor_sync(0xffffffffu, st.l[a][x], b);
     __syncwarp();
 }
 
-template <int D, int DT>
-__global__ void __launch_bounds__(kRowWarps * 32, kRowCtas)
+// Rows of tile a from output fragment f: transposed to (row 8a + tq, channels
+// 16f + 8y + 2cs, + 1).
+template <int DT>
+__device__ __forceinline__ void store_rows(const AttnCall &c, const AttnTab &t, const Seg &sg, int row, int d,
+                                           const float (&o)[4], float f0, float f1)
+{
+    const int cs = threadIdx.x & 3;
+    const uint32_t x = transpose8(pack2<DT>(o[0] * f0, o[1] * f1)), y = transpose8(pack2<DT>(o[2] * f0, o[3] * f1));
+    const int tok = row / c.group;
+    if (tok >= t.n[sg.e]) return;
+    uint16_t *p = c.out
+                  + ((long long)(t.row0[sg.e] + tok) * c.H_q + sg.h * c.group + row - tok * c.group) * c.v.D + d + 2 * cs;
+    *(uint32_t *)p = x;
+    *(uint32_t *)(p + 8) = y;
+}
+
+template <int D, int DT, int NT>
+__global__ void __launch_bounds__(kRowWarps * 32, row_ctas(NT))
     pool_rows_kernel(const __grid_constant__ AttnCall c, const __grid_constant__ AttnTab t)
 {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -532,31 +698,31 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowCtas)
         };
         const long long rb = min(sg.C, hi - sg.base);
         const int i0 = min(items, first_item(pos - sg.base)), i1 = rb == sg.C ? items : first_item(rb);
-        State<D> st;
-        run_items<D, DT>(c, t, sg, i0, max(i0, i1), sm, st);
+        State<D, NT> st;
+        run_items<D, DT, NT>(c, t, sg, i0, max(i0, i1), sm, st);
         if (sg.base >= lo && rb == sg.C) {
-            // The whole segment: normalise and store.
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int row = 16 * sg.rt + tq + 8 * r, tok = row / c.group;
-                if (tok >= t.n[e]) continue;
-                const float inv = st.l[r] == 0.0f ? 0.0f : 1.0f / st.l[r];
-                uint16_t *o = c.out
-                              + ((long long)(t.row0[e] + tok) * c.H_q + sg.h * c.group + row - tok * c.group) * D + 2 * cs;
+            for (int a = 0; a < NT; ++a) {
+                const float f0 = st.l[a][0] == 0.0f ? 0.0f : 1.0f / st.l[a][0];
+                const float f1 = st.l[a][1] == 0.0f ? 0.0f : 1.0f / st.l[a][1];
 #pragma unroll
-                for (int k = 0; k < D / 8; ++k)
-                    *(uint32_t *)(o + 8 * k) = pack2<DT>(st.o[k][2 * r] * inv, st.o[k][2 * r + 1] * inv);
+                for (int f = 0; f < D / 16; ++f)
+                    store_rows<DT>(c, t, sg, 8 * NT * sg.rt + 8 * a + tq, 16 * f, st.o[a][f], f0, f1);
             }
         } else {
-            float *part = c.part + (2 * w + (sg.base >= lo ? 1 : 0)) * kPartFloats<D>;
+            float *part = c.part + (2 * w + (sg.base >= lo ? 1 : 0)) * kPartFloats<D, NT>;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int row = tq + 8 * r;
-                if ((16 * sg.rt + row) / c.group >= t.n[e]) continue;
+            for (int a = 0; a < NT; ++a) {
+                if ((8 * NT * sg.rt + 8 * a) / c.group >= t.n[e]) break;
+                float *pa = part + a * (8 * D + 16);
 #pragma unroll
-                for (int k = 0; k < D / 8; ++k)
-                    *(float2 *)(part + row * D + 8 * k + 2 * cs) = make_float2(st.o[k][2 * r], st.o[k][2 * r + 1]);
-                if (cs == 0) *(float2 *)(part + 16 * D + 2 * row) = make_float2(st.m[r], st.l[r]);
+                for (int f = 0; f < D / 16; ++f)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) pa[(4 * f + x) * 32 + lane] = st.o[a][f][x];
+                if (tq == 0)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        *(float2 *)(pa + 8 * D + 2 * (2 * cs + x)) = make_float2(st.m[a][x], st.l[a][x]);
             }
         }
         pos = sg.base + rb;
@@ -564,82 +730,105 @@ __global__ void __launch_bounds__(kRowWarps * 32, kRowCtas)
 }
 
 // Adds the partial results of the segment that starts in warp blockIdx.x's
-// range and ends behind it (if there is one), in the order of its warps: one
-// warp per row.
-template <int D, int DT>
-__global__ void __launch_bounds__(512) pool_join_kernel(const __grid_constant__ AttnCall c,
-                                                        const __grid_constant__ AttnTab t)
+// range and ends behind it (if there is one), in the order of its warps; warp
+// (a, f) of the block takes output fragment f of tile a.
+template <int D, int DT, int NT>
+__global__ void __launch_bounds__(NT *D / 16 * 32) pool_join_kernel(const __grid_constant__ AttnCall c,
+                                                                    const __grid_constant__ AttnTab t)
 {
     const long long w = blockIdx.x, tot = t.off[t.nb];
     const long long lo = range_at(w, tot, c.warps), hi = range_at(w + 1, tot, c.warps);
     if (hi >= tot || lo >= hi) return;
     const Seg sg = find_segment(t, c, hi - 1);
     if (sg.base < lo || sg.base + sg.C <= hi) return;
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, e = sg.e;
-    const int row = 16 * sg.rt + wid, tok = row / c.group;
-    if (tok >= t.n[e]) return;
-    constexpr int E = D / 32;
-    float m = -INFINITY, l = 0.0f, o[E];
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, tq = lane >> 2, cs = lane & 3;
+    const int a = wid / (D / 16), f = wid % (D / 16);
+    const int row = 8 * NT * sg.rt + 8 * a;
+    if (row / c.group >= t.n[sg.e]) return;
+    // The warp that holds the segment's last position.
+    const long long last = ((sg.base + sg.C) * c.warps - 1) / tot;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (long long x = w; x <= last; ++x) {
+        const float *pa = c.part + (2 * x + (x == w ? 1 : 0)) * kPartFloats<D, NT> + a * (8 * D + 16);
+        const float4 ml = *(const float4 *)(pa + 8 * D + 4 * cs);   // of rows 2cs and 2cs + 1
+        float q[4];
 #pragma unroll
-    for (int k = 0; k < E; ++k) o[k] = 0.0f;
-    for (long long x = w;; ++x) {
-        const float *part = c.part + (2 * x + (x == w ? 1 : 0)) * kPartFloats<D>;
-        const float2 ml = *(const float2 *)(part + 16 * D + 2 * wid);
-        if (ml.y != 0.0f) {   // (a NaN sum counts)
-            const float mn = fmaxf(m, ml.x);
-            const float f = m == -INFINITY ? 0.0f : ex2(m - mn), g = ex2(ml.x - mn);
-            l = l * f + ml.y * g;
+        for (int y = 0; y < 4; ++y) q[y] = pa[(4 * f + y) * 32 + lane];
 #pragma unroll
-            for (int k = 0; k < E; ++k) o[k] = o[k] * f + part[wid * D + lane * E + k] * g;
-            m = mn;
+        for (int y = 0; y < 2; ++y) {
+            const float pm = y ? ml.z : ml.x, pl = y ? ml.w : ml.y;
+            if (pl == 0.0f) continue;   // nothing seen (a NaN sum counts)
+            const float mn = fmaxf(m[y], pm);
+            const float fo = m[y] == -INFINITY ? 0.0f : ex2(m[y] - mn), fn = ex2(pm - mn);
+            l[y] = l[y] * fo + pl * fn;
+            o[y] = o[y] * fo + q[y] * fn;
+            o[2 + y] = o[2 + y] * fo + q[2 + y] * fn;
+            m[y] = mn;
         }
-        if (range_at(x + 1, tot, c.warps) >= sg.base + sg.C) break;
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    uint16_t *out = c.out + ((long long)(t.row0[e] + tok) * c.H_q + sg.h * c.group + row - tok * c.group) * D;
-#pragma unroll
-    for (int k = 0; k < E; k += 2) *(uint32_t *)(out + lane * E + k) = pack2<DT>(o[k] * inv, o[k + 1] * inv);
+    const float f0 = l[0] == 0.0f ? 0.0f : 1.0f / l[0], f1 = l[1] == 0.0f ? 0.0f : 1.0f / l[1];
+    store_rows<DT>(c, t, sg, row + tq, 16 * f, o, f0, f1);
 }
 
-template <int D, int DT>
+template <int D, int DT, int NT>
 cudaError_t rows_t(AttnCall &c, AttnTab &t, cudaStream_t st)
 {
     static PerDeviceOnce once;
-    cudaError_t e = set_smem_once(once, pool_rows_kernel<D, DT>, RowsSmem<D>::BYTES);
+    cudaError_t e = set_smem_once(once, pool_rows_kernel<D, DT, NT>, RowsSmem<D>::BYTES);
     if (e != cudaSuccess) return e;
-    pool_rows_kernel<D, DT><<<(unsigned)((c.warps + kRowWarps - 1) / kRowWarps), kRowWarps * 32, RowsSmem<D>::BYTES, st>>>(
-        c, t);
+    pool_rows_kernel<D, DT, NT>
+        <<<(unsigned)((c.warps + kRowWarps - 1) / kRowWarps), kRowWarps * 32, RowsSmem<D>::BYTES, st>>>(c, t);
     e = cudaGetLastError();
     if (e != cudaSuccess || c.warps == 1) return e;
-    pool_join_kernel<D, DT><<<(unsigned)c.warps, 512, 0, st>>>(c, t);
+    pool_join_kernel<D, DT, NT><<<(unsigned)c.warps, NT * D / 16 * 32, 0, st>>>(c, t);
     return cudaGetLastError();
 }
 
-long long split_warps(int sms) { return (long long)sms * kRowCtas * kRowWarps; }
+template <int D, int DT>
+cudaError_t rows_n(AttnCall &c, AttnTab &t, int nt, cudaStream_t st)
+{
+    if (nt == 1) return rows_t<D, DT, 1>(c, t, st);
+    if (nt == 2) return rows_t<D, DT, 2>(c, t, st);
+    return rows_t<D, DT, 3>(c, t, st);
+}
+
+long long split_warps(int sms, int nt) { return (long long)sms * row_ctas(nt) * kRowWarps; }
 
 }  // namespace
 
 size_t pool_rows_scratch(int D, int sms)
 {
-    return (size_t)(2 * split_warps(sms)) * (D == 64 ? kPartFloats<64> : kPartFloats<128>);
+    size_t most = 0;
+    for (int nt = 1; nt <= kMaxTiles; ++nt) {
+        const size_t n = (size_t)(2 * split_warps(sms, nt)) * nt * (8 * D + 16);
+        most = n > most ? n : most;
+    }
+    return most;
 }
 
 // Fills the split (t.off, c.warps) and launches.
 cudaError_t launch_pool_rows(AttnCall &c, AttnTab &t, int sms, cudaStream_t st)
 {
+    // As many tiles per warp as the most rows of an entry need: the decoded
+    // fragments serve all of them.
+    long long most = 0;
+    for (int e = 0; e < t.nb; ++e) most = most > t.n[e] ? most : t.n[e];
+    most = (most * c.group + 7) / 8;
+    const int nt = most < kMaxTiles ? (int)most : kMaxTiles;
+    if (nt == 0) return cudaSuccess;
     t.off[0] = 0;
     for (int e = 0; e < t.nb; ++e) {
         const long long C = t.ng[e] + (long long)((t.r[e] + 31) / 32 + (t.nk[e] + 31) / 32) * kRawWeight;
-        const long long tiles = ((long long)t.n[e] * c.group + 15) / 16;
+        const long long tiles = ((long long)t.n[e] * c.group + 8 * nt - 1) / (8 * nt);
         t.off[e + 1] = t.off[e] + tiles * c.v.H * (C > 0 ? C : 1);
     }
     const long long tot = t.off[t.nb];
     if (tot == 0) return cudaSuccess;
-    c.warps = split_warps(sms);
+    c.warps = split_warps(sms, nt);
     if (c.warps > tot) c.warps = tot;
     if (tot > (1LL << 62) / (c.warps + 1)) return cudaErrorInvalidValue;
-    if (c.v.D == 64) return c.v.dtype ? rows_t<64, 1>(c, t, st) : rows_t<64, 0>(c, t, st);
-    return c.v.dtype ? rows_t<128, 1>(c, t, st) : rows_t<128, 0>(c, t, st);
+    if (c.v.D == 64) return c.v.dtype ? rows_n<64, 1>(c, t, nt, st) : rows_n<64, 0>(c, t, nt, st);
+    return c.v.dtype ? rows_n<128, 1>(c, t, nt, st) : rows_n<128, 0>(c, t, nt, st);
 }
 
 }  // namespace kivi
