@@ -70,7 +70,7 @@ void make_pool_plan(const kivi_pool_config *c, int sms, PoolPlan *p)
     p->off_table = off;
     off = align_up(off + (size_t)c->sequences * p->max_pages * sizeof(int));
     p->off_part = off;
-    off = align_up(off + pool_rows_scratch(c->D, sms) * sizeof(float));
+    off = align_up(off + std::max(pool_rows_scratch(c->D, sms), pool_tiles_scratch(c->D, sms)) * sizeof(float));
     p->off_err = off;
     off = align_up(off + sizeof(int));
     p->total = off;
@@ -418,17 +418,23 @@ kivi_status kivi_pool_attn(kivi_pool *p, const int *seqs, const int *n_new, int 
     if (total > (1LL << 30) / (H_q / p->cfg.H_kv)) return KIVI_ERR_UNSUPPORTED;
     if (!good_rows(q) || (k && (!good_rows(k) || !good_rows(v))) || !out || !aligned16(out)) return KIVI_ERR_ARG;
     return guarded([&]() -> kivi_status {
-        auto t = std::make_unique<AttnTab>();
-        t->nb = n;
+        // Sequences of few rows and of many go to kernels of their own.
+        auto few = std::make_unique<AttnTab>(), many = std::make_unique<AttnTab>();
+        few->nb = many->nb = 0;
+        const int group = H_q / p->cfg.H_kv;
         int row = 0;
         for (int i = 0; i < n; ++i) {
             const PoolSeq &s = p->seqs[seqs[i]];
-            t->seq[i] = seqs[i];
-            t->row0[i] = row;
-            t->n[i] = n_new[i];
-            t->nk[i] = k ? n_new[i] : 0;
-            t->ng[i] = (int)(s.pages.size() * (p->cfg.R / kG));
-            t->r[i] = s.r;
+            if (n_new[i] == 0) continue;
+            const bool sees = k || s.r > 0;
+            AttnTab &t = sees && (long long)n_new[i] * group > kTileMinRows ? *many : *few;
+            const int e = t.nb++;
+            t.seq[e] = seqs[i];
+            t.row0[e] = row;
+            t.n[e] = n_new[i];
+            t.nk[e] = k ? n_new[i] : 0;
+            t.ng[e] = (int)(s.pages.size() * (p->cfg.R / kG));
+            t.r[e] = s.r;
             row += n_new[i];
         }
         AttnCall c;
@@ -438,11 +444,14 @@ kivi_status kivi_pool_attn(kivi_pool *p, const int *seqs, const int *n_new, int 
         c.nv = v ? rows_of(v) : Rows{nullptr, 0, 0};
         c.out = (uint16_t *)out;
         c.H_q = H_q;
-        c.group = H_q / p->cfg.H_kv;
+        c.group = group;
         c.scale = (float)(1.4426950408889634 / std::sqrt((double)p->cfg.D));
         c.part = p->part;
         c.err = p->err;
-        return cuda_status(launch_pool_rows(c, *t, p->sms, (cudaStream_t)stream));
+        // One after the other on the stream: they share the scratch.
+        cudaError_t e = many->nb ? launch_pool_tiles(c, *many, p->sms, (cudaStream_t)stream) : cudaSuccess;
+        if (e == cudaSuccess && few->nb) e = launch_pool_rows(c, *few, p->sms, (cudaStream_t)stream);
+        return cuda_status(e);
     });
 }
 

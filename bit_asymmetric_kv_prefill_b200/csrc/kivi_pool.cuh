@@ -123,8 +123,13 @@ cudaError_t launch_pool_table(const PoolView &v, const PairTab &t, cudaStream_t 
 cudaError_t launch_pool_move(const PoolView &v, const PairTab &t, cudaStream_t st);
 cudaError_t launch_pool_fork(const PoolView &v, const ForkTab &t, cudaStream_t st);
 
-// Floats of attention scratch for a device of `sms` SMs.
+// Attention of few rows (matrix fragments) and of many (tcgen05 tiles), and
+// the floats of scratch each needs on a device of `sms` SMs.
 size_t pool_rows_scratch(int D, int sms);
 cudaError_t launch_pool_rows(AttnCall &c, AttnTab &t, int sms, cudaStream_t st);
+size_t pool_tiles_scratch(int D, int sms);
+cudaError_t launch_pool_tiles(AttnCall &c, AttnTab &t, int sms, cudaStream_t st);
+// Entries with more rows per kv head than this take the tiles.
+constexpr int kTileMinRows = 32;
 
 }  // namespace kivi

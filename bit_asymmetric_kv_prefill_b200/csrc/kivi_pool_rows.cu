@@ -49,8 +49,10 @@ constexpr int kRowStages = 4;       // group blocks in flight per warp
 constexpr int kRawWeight = 2;       // cost of 32 uncoded tokens, in groups
 constexpr float kLazy = 3.0f;       // the running maximum follows when exceeded by 2^kLazy
 constexpr int kMaxTiles = 3;        // 8-row tiles per warp
-// CTAs per SM of a kernel with NT tiles (128, 168, 255 registers a thread).
-constexpr int row_ctas(int nt) { return nt == 1 ? 4 : nt == 2 ? 3 : 2; }
+// CTAs per SM of a kernel with NT tiles (168 or 255 registers a thread).  One
+// tile would fit 128 registers and 4 CTAs: 80 us against 73 with 3 (24 x 8K
+// tokens, 8 kv heads of 4 query heads).
+constexpr int row_ctas(int nt) { return nt <= 2 ? 3 : 2; }
 
 // ---- fragments ------------------------------------------------------------------
 template <int DT>
@@ -116,15 +118,12 @@ __device__ __forceinline__ float pow2(int k) { return __uint_as_float((uint32_t)
 // right by 10): its codes sit at mantissa bits 2k, 2k + 1 of a half.
 __host__ __device__ constexpr int code_place(int i) { return i < 5 ? i : i - 5; }
 
-// c - 1 of pair i, as fp16: the codes on top of 2^(10 - 2k), where they count
-// ones, minus that and 1 (exact).
-__device__ __forceinline__ __half2 code_less_one(uint32_t w, uint32_t w10, int i)
+// c - 1 of pair i, as fp16: the codes on top of one[k] = 2^(10 - 2k), where
+// they count ones, minus that and 1 (exact).
+__device__ __forceinline__ __half2 code_less_one(uint32_t w, uint32_t w10, int i, const uint32_t (&one)[5])
 {
     const int k = code_place(i);
-    uint32_t x;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;"
-        : "=r"(x)
-        : "r"(i < 5 ? w : w10), "r"(0x00030003u << (2 * k)), "r"((uint32_t)((25 - 2 * k) << 10) * 0x10001u));
+    const uint32_t x = ((i < 5 ? w : w10) & (0x00030003u << (2 * k))) | one[k];
     return __hadd2(as_h2(x), __half2half2(__float2half_rn(-(float)((1 << (10 - 2 * k)) + 1))));
 }
 // c 4^k 2^-24 of pair i (fp16 subnormals).
@@ -289,6 +288,12 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
         }
     };
     int E = -12;   // p is kept times 2^-E
+    // Kept in registers: as constants each use would load them anew, next to
+    // the mask that the logic instruction already holds.
+    uint32_t one[5];
+#pragma unroll
+    for (int k = 0; k < 5; ++k)
+        asm volatile("mov.b32 %0, %1;" : "=r"(one[k]) : "r"((uint32_t)((25 - 2 * k) << 10) * 0x10001u));
 
     // ---- coded groups ----
     const int g1 = min(i1, ng);
@@ -402,8 +407,8 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
 #pragma unroll
                         for (int p = 0; p < 4; ++p) {
                             const int i = 4 * (u % 2) + p;
-                            k0[p] = as_u(__hmul2(code_less_one(w0, x0, i), as_h2(s[u][p])));
-                            k1[p] = as_u(__hmul2(code_less_one(w1, x1, i), as_h2(s[u][p])));
+                            k0[p] = as_u(__hmul2(code_less_one(w0, x0, i, one), as_h2(s[u][p])));
+                            k1[p] = as_u(__hmul2(code_less_one(w1, x1, i, one), as_h2(s[u][p])));
                         }
 #pragma unroll
                         for (int a = 0; a < NT; ++a) {

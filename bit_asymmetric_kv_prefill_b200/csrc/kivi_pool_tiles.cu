@@ -1,0 +1,890 @@
+// kivi_pool_tiles.cu -- attention of new tokens over a pool's pages for many
+// rows: tcgen05 products over decoded tiles.
+//
+// A CTA holds 256 rows (token, head of one kv head) as two 128-row query tiles
+// and walks the keys in tiles of 96 tokens (three coded groups, or 96 uncoded
+// tokens).  Per tile and query tile
+//   S [128 x 112] = Q K^T     (operands in shared memory, result in TMEM)
+//   P = 2^(S - m)             (fp16 or the pool's type, over S in TMEM)
+//   O [128 x D] += P V        (P from TMEM, V in shared memory)
+// Keys enter as the exact fp16 products s_d (c_d - 1) (see kivi_pool_rows.cu);
+// the z and s of the three groups are six more rows of the key tile, so that
+// columns 96..101 of S are q.z and q.s of each group, which every row adds to
+// its scores.  Values enter as fp16(z + s c).  Uncoded tokens enter as they
+// are, in the pool's type; the queries are reloaded for them, since bf16 ones
+// are scaled to fp16 for the coded tiles.
+//
+// Roles (15 warps): warps 0-3 and 4-7 are the softmax of query tiles 0 and 1
+// (thread = row, no exchange between threads), warps 8-10 and 11-13 decode the
+// keys and values of one 32-token group each, warp 14 issues the products.
+// The order QK(i + 1) after PV(i) of each query tile lets one tile's softmax
+// run under the other's products; S and P share TMEM columns because products
+// of one CTA execute in order.
+//
+// The flattened work (sequence, kv head, row tile, key tile) is cut into one
+// equal range per SM; segments that cross ranges leave partial results that
+// pool_tiles_join_kernel adds in a fixed order.
+//
+// Bound: per 96 tokens and 256 rows 1728 tensor cycles (peak rate), 1536 for
+// the exponentials (16 a cycle), about 6000 issue slots of 6900 in 1728
+// cycles, and 1750 cycles of shared memory (operands 168 KB, decoded tiles 52
+// KB at 128 bytes a cycle): all four are close, none is far ahead.
+#include <cuda_runtime.h>
+
+#include "kivi_code.cuh"
+#include "kivi_pool.cuh"
+
+namespace kivi {
+namespace {
+
+constexpr int kTileTok = 96;             // tokens per key tile
+constexpr int kKeyRows = 112;            // rows of the key tile: tokens, 3 z, 3 s, unused
+constexpr int kTileRows = 256;           // query rows per CTA
+constexpr int kThreads = 15 * 32;
+constexpr int kRing = 3;                 // coded halves in flight per decoding warp
+constexpr int kFirstBufs = 4;
+constexpr float kLazy = 3.0f;            // the running maximum follows when exceeded by 2^kLazy
+constexpr float kRef = -8.0f;            // p is kept times 2^8: fp16 keeps 2^-32 of the largest
+constexpr uint64_t kWaitNs = 2000000000; // a wait gives up after two seconds
+
+template <int D>
+struct TileSmem {
+    static constexpr int KB = D / 64;                      // 64-channel blocks of 128-byte rows
+    static constexpr int QT = KB * 128 * 128;              // one query tile
+    static constexpr int KT = KB * kKeyRows * 128;         // one key tile
+    static constexpr int VT = KB * kTileTok * 128;         // one value tile
+    static constexpr int HALF = 12 * D;                    // K or V half of a group block
+    static constexpr int Q = 0;
+    static constexpr int K = Q + 2 * QT;
+    static constexpr int V = K + 2 * KT;
+    static constexpr int RING = V + 2 * VT;
+    static constexpr int FIRST = RING + 6 * kRing * HALF;  // [query tile][buffer][D] first token with a bad value
+    static constexpr int FLAG = FIRST + 2 * kFirstBufs * D * 8;
+    static constexpr int BAR = FLAG + 2 * kFirstBufs * 4;
+    static constexpr int BYTES = BAR + 24 * 8 + 16;
+};
+// Barriers.
+enum { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kQFull = 8, kSFull = 10, kPFull = 12, kOFull = 14, kBars = 16 };
+
+// ---- barriers and tensor-core instructions -----------------------------------------
+__device__ __forceinline__ uint32_t saddr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void bar_init(uint32_t b, int n)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(b), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t b)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(b) : "memory");
+}
+__device__ __forceinline__ bool bar_test(uint32_t b, uint32_t phase)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(b), "r"(phase)
+        : "memory");
+    return ok != 0;
+}
+
+struct Ctl {
+    volatile int *stop;   // shared: some wait gave up
+    int *err;             // the pool's status word
+};
+
+__device__ __forceinline__ uint64_t now_ns()
+{
+    uint64_t t;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    return t;
+}
+
+// Waits for the barrier's phase; false when this wait, or another of the CTA,
+// gave up (then the caller leaves).
+__device__ __noinline__ bool bar_wait_long(const Ctl &ctl, uint32_t b, uint32_t phase)
+{
+    const uint64_t t0 = now_ns();
+#pragma unroll 1
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (bar_test(b, phase)) return true;
+        if (*ctl.stop) return false;
+        if (now_ns() - t0 > kWaitNs) break;
+    }
+    *ctl.stop = 1;
+    atomicCAS(ctl.err, 0, KIVI_DEVICE_WAIT_TIMEOUT);
+    return false;
+}
+__device__ __forceinline__ bool bar_wait(const Ctl &ctl, uint32_t b, uint32_t phase)
+{
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i)
+        if (bar_test(b, phase)) return true;
+    return bar_wait_long(ctl, b, phase);
+}
+// The same for a whole warp: its lanes leave together.
+__device__ __forceinline__ bool warp_wait(const Ctl &ctl, uint32_t b, uint32_t phase)
+{
+    return __all_sync(0xffffffffu, bar_wait(ctl, b, phase));
+}
+
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint32_t b)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(b) : "memory");
+}
+
+// 32 (16, 8) columns of the thread's TMEM lane.
+__device__ __forceinline__ void tc_ld32(uint32_t (&r)[32], uint32_t a)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(a)
+        : "memory");
+}
+__device__ __forceinline__ void tc_ld8(uint32_t (&r)[8], uint32_t a)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ void tc_st32(uint32_t a, const uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(a),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t a, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// Shared-memory operand descriptor: 128-byte swizzled rows, 1024 bytes per 8
+// rows; lbo: bytes between 64-element blocks of the contiguous direction
+// (operands whose contiguous direction is not the summed one).
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lbo)
+{
+    return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32)
+           | (1ull << 46) | (2ull << 61);
+}
+// Instruction descriptor: fp32 result, 16-bit operands, M = 128, N = n;
+// transposed: B's contiguous direction is N.
+__device__ __forceinline__ constexpr uint32_t instruction(bool bf16, int n, bool transposed)
+{
+    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (transposed ? 1u << 16 : 0u) | ((uint32_t)(n / 8) << 17)
+           | ((128u / 16) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t inst, bool add)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(inst), "r"((uint32_t)add)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t inst, bool add)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(inst), "r"((uint32_t)add)
+                 : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    uint32_t r;
+    if constexpr (DT == KIVI_BF16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        memcpy(&r, &v, 4);
+    } else {
+        const __half2 v = __floats2half2_rn(a, b);
+        memcpy(&r, &v, 4);
+    }
+    return r;
+}
+__device__ __forceinline__ __half2 as_h2(uint32_t u)
+{
+    __half2 r;
+    memcpy(&r, &u, 4);
+    return r;
+}
+__device__ __forceinline__ uint32_t as_u(__half2 h)
+{
+    uint32_t r;
+    memcpy(&r, &h, 4);
+    return r;
+}
+__device__ __forceinline__ float pow2(int k) { return __uint_as_float((uint32_t)(127 + k) << 23); }
+
+// The codes of pair i minus `less`, as fp16 (exact; see kivi_pool_rows.cu).
+__device__ __forceinline__ __half2 code_less(uint32_t w, uint32_t w10, int i, int less, const uint32_t (&one)[5])
+{
+    const int k = i < 5 ? i : i - 5;
+    const uint32_t x = ((i < 5 ? w : w10) & (0x00030003u << (2 * k))) | one[k];
+    return __hadd2(as_h2(x), __half2half2(__float2half_rn(-(float)((1 << (10 - 2 * k)) + less))));
+}
+
+// ---- the split ------------------------------------------------------------------------
+struct TSeg {
+    int e, h, rt;
+    int nc, nr;          // coded and uncoded key tiles
+    long long base;      // where the segment starts
+};
+
+__host__ __device__ __forceinline__ int coded_tiles(int ng) { return (ng + 2) / 3; }
+// Uncoded tokens that rows of tile rt may see (residual, then new tokens).
+__host__ __device__ __forceinline__ int raw_seen(int r, int nk, int n, int group, int rt)
+{
+    const long long last = (long long)rt * kTileRows + kTileRows - 1, end = (long long)n * group - 1;
+    const int tok = (int)((last < end ? last : end) / group);
+    return r + (nk < tok + 1 ? nk : tok + 1);
+}
+
+__device__ __forceinline__ TSeg find_segment(const AttnTab &t, const AttnCall &c, long long pos)
+{
+    int lo = 0, hi = t.nb - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (t.off[mid] <= pos) lo = mid;
+        else hi = mid - 1;
+    }
+    TSeg s;
+    s.e = lo;
+    const long long per_head = (t.off[lo + 1] - t.off[lo]) / c.v.H;
+    s.h = (int)((pos - t.off[lo]) / per_head);
+    s.base = t.off[lo] + s.h * per_head;
+    s.nc = coded_tiles(t.ng[lo]);
+    for (s.rt = 0;; ++s.rt) {
+        s.nr = (raw_seen(t.r[lo], t.nk[lo], t.n[lo], c.group, s.rt) + kTileTok - 1) / kTileTok;
+        if (pos < s.base + s.nc + s.nr) return s;
+        s.base += s.nc + s.nr;
+    }
+}
+
+__device__ __forceinline__ long long range_at(long long w, long long tot, long long parts)
+{
+    return (long long)((unsigned long long)(w * tot) / (unsigned long long)parts);
+}
+
+template <int D>
+constexpr int kTilePart = kTileRows * (D + 2);   // floats of a partial result
+
+// A CTA's walk over its segments, the same for every role.
+struct Walk {
+    long long lo, hi, pos;
+    TSeg s;
+    int i0, i1;       // key tiles of the segment that are this CTA's
+    int nq;           // query tiles with rows
+    bool whole;       // the segment lies inside the range
+    __device__ __forceinline__ bool next(const AttnCall &c, const AttnTab &t)
+    {
+        if (pos >= hi) return false;
+        s = find_segment(t, c, pos);
+        const int C = s.nc + s.nr;
+        i0 = (int)(pos - s.base);
+        i1 = (int)(hi - s.base < C ? hi - s.base : C);
+        whole = i0 == 0 && i1 == C;
+        const long long rows = (long long)t.n[s.e] * c.group - (long long)s.rt * kTileRows;
+        nq = rows > 128 ? 2 : 1;
+        pos = s.base + i1;
+        return true;
+    }
+};
+
+template <int D>
+__device__ __forceinline__ uint32_t key_at(int row, int c)
+{
+    return (c / 8) * (kKeyRows * 128) + row * 128 + ((c % 8) ^ (row & 7)) * 16;
+}
+template <int D>
+__device__ __forceinline__ uint32_t value_at(int row, int c)
+{
+    return (c / 8) * (kTileTok * 128) + row * 128 + ((c % 8) ^ (row & 7)) * 16;
+}
+__device__ __forceinline__ uint32_t query_at(int row, int c)
+{
+    return (c / 8) * (128 * 128) + row * 128 + ((c % 8) ^ (row & 7)) * 16;
+}
+
+// The first token with a value that is not finite, per channel: later segments
+// of a CTA win the minimum, so the table is never cleared.  Four tables in
+// turn: the decoding warps are at most three segments ahead of the softmax.
+__device__ __forceinline__ unsigned long long bad_token(int seg, int tok)
+{
+    return ((unsigned long long)(0x7fffffff - seg) << 32) | (uint32_t)(tok + 0x40000000);
+}
+
+// ---- decoding warps: one 32-token group of keys (VAL = 0) or values ----------------------
+template <int D, int DT, int VAL>
+__device__ __forceinline__ void decode_role(const AttnCall &c, const AttnTab &t, uint8_t *sm, uint32_t bars, const Ctl &ctl,
+                                            int sub, Walk w)
+{
+    using L = PageLayout<D>;
+    using S = TileSmem<D>;
+    const int lane = threadIdx.x & 31, tq = lane >> 2, cs = lane & 3;
+    const PoolView &v = c.v;
+    uint32_t one[5];
+#pragma unroll
+    for (int k = 0; k < 5; ++k)
+        asm volatile("mov.b32 %0, %1;" : "=r"(one[k]) : "r"((uint32_t)((25 - 2 * k) << 10) * 0x10001u));
+    uint8_t *ring = sm + S::RING + (VAL * 3 + sub) * kRing * S::HALF;
+    const uint32_t ring_s = saddr(ring);
+    const uint32_t full = bars + 8 * (VAL ? kVFull : kKFull), empty = bars + 8 * (VAL ? kVEmpty : kKEmpty);
+    int it = 0, seg = 0;
+    while (w.next(c, t)) {
+        const int e = w.s.e, ng = t.ng[e], r = t.r[e], nk = t.nk[e], seq = t.seq[e];
+        const int *table = v.table + (long long)seq * v.max_pages;
+        // Coded halves through the ring, kRing - 1 tiles ahead.
+        auto fetch = [&](int i) {
+            const int g = 3 * i + sub;
+            if (i < w.i1 && i < w.s.nc && g < ng) {
+                const uint8_t *src = v.packed + ((long long)table[g / v.gpp] * v.H + w.s.h) * ((long long)v.gpp * L::GB)
+                                     + (long long)(g % v.gpp) * L::GB + (VAL ? L::VC : L::KC);
+                const uint32_t to = ring_s + (uint32_t)((i - w.i0) % kRing) * S::HALF;
+#pragma unroll
+                for (int k = 0; k < S::HALF / 512; ++k)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + (k * 32 + lane) * 16),
+                                 "l"(src + (k * 32 + lane) * 16)
+                                 : "memory");
+                if constexpr (S::HALF % 512 != 0)
+                    if (lane < S::HALF % 512 / 16)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                         to + ((S::HALF / 512) * 32 + lane) * 16),
+                                     "l"(src + ((S::HALF / 512) * 32 + lane) * 16)
+                                     : "memory");
+            }
+            cp_async_commit();
+        };
+        for (int k = 0; k < kRing - 1; ++k) fetch(w.i0 + k);
+#pragma unroll 1
+        for (int i = w.i0; i < w.i1; ++i, ++it) {
+            const int st = it & 1;
+            uint8_t *tile = sm + (VAL ? S::V + st * S::VT : S::K + st * S::KT);
+            if (!warp_wait(ctl, empty + 8 * st, ((it >> 1) & 1) ^ 1)) return;
+            if (i < w.s.nc) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+                __syncwarp();
+                fetch(i + kRing - 1);
+                const uint8_t *half = ring + ((i - w.i0) % kRing) * S::HALF;
+                const bool real = 3 * i + sub < ng;
+                if (!real) {
+                    // No such group: zeros.
+#pragma unroll
+                    for (int k = 0; k < D / 8; ++k) {
+                        const int q = k * 32 + lane, row = 32 * sub + q / (D / 8), ch = q % (D / 8);
+                        *(uint4 *)(tile + (VAL ? value_at<D>(row, ch) : key_at<D>(row, ch))) = make_uint4(0, 0, 0, 0);
+                    }
+                } else if constexpr (VAL == 0) {
+                    uint32_t kw[L::WPL];
+#pragma unroll
+                    for (int q = 0; q < L::WPL / 4; ++q)
+                        *(uint4 *)(kw + 4 * q) = *(const uint4 *)(half + (q * 32 + lane) * 16);
+#pragma unroll
+                    for (int u = 0; u < D / 32; ++u) {
+                        uint32_t s[4];
+                        *(uint4 *)s = *(const uint4 *)(half + (L::KS - L::KC) + u * 64 + cs * 16);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t x = kw[j * L::KW + u / 2], x10 = x >> 10;
+                            uint32_t o[4];
+#pragma unroll
+                            for (int p = 0; p < 4; ++p)
+                                o[p] = as_u(__hmul2(code_less(x, x10, 4 * (u % 2) + p, 1, one), as_h2(s[p])));
+                            *(uint4 *)(tile + key_at<D>(32 * sub + tq + 8 * j, 4 * u + cs)) = *(const uint4 *)o;
+                        }
+                    }
+                    // Rows 96 + sub (z) and 99 + sub (s).
+                    if (lane < D / 8) {
+                        *(uint4 *)(tile + key_at<D>(kTileTok + sub, lane)) =
+                            *(const uint4 *)(half + (L::KZ - L::KC) + lane * 16);
+                        *(uint4 *)(tile + key_at<D>(kTileTok + 3 + sub, lane)) =
+                            *(const uint4 *)(half + (L::KS - L::KC) + lane * 16);
+                    }
+                } else {
+                    uint32_t vw[L::WPL];
+#pragma unroll
+                    for (int q = 0; q < L::WPL / 4; ++q)
+                        *(uint4 *)(vw + 4 * q) = *(const uint4 *)(half + (q * 32 + lane) * 16);
+                    const uint32_t tile_s = saddr(tile);
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+#pragma unroll
+                        for (int jh = 0; jh < L::KW; ++jh) {
+                            const uint4 sz = *(const uint4 *)(half + (L::VM - L::VC) + page_vm_offset<D>(p, cs, 2 * jh));
+                            const uint32_t x = vw[p * L::KW + jh], x10 = x >> 10;
+#pragma unroll
+                            for (int jj = 0; jj < 2; ++jj) {
+                                uint32_t o[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    o[k] = as_u(__hfma2(code_less(x, x10, 4 * jj + k, 0, one), as_h2(jj ? sz.z : sz.x),
+                                                        as_h2(jj ? sz.w : sz.y)));
+                                const uint32_t a =
+                                    tile_s + value_at<D>(32 * sub + 8 * p + (lane & 7), 8 * jh + 4 * jj + (lane >> 3));
+                                asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(a),
+                                             "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                                             : "memory");
+                            }
+                        }
+                }
+            } else {
+                // 32 uncoded tokens: residual, then new ones.
+                const int seen = raw_seen(r, nk, t.n[e], c.group, w.s.rt);
+                const int t0 = (i - w.s.nc) * kTileTok + 32 * sub;
+                const uint16_t *res = (VAL ? v.resV : v.resK) + ((long long)seq * v.H + w.s.h) * v.R * D;
+                const Rows &src = VAL ? c.nv : c.k;
+                // Some row does not see the last of these tokens.
+                const bool masked = VAL && t0 + 32 > r && t0 + 31 - r > (int)((long long)w.s.rt * kTileRows / c.group);
+#pragma unroll 4
+                for (int k = 0; k < D / 8; ++k) {
+                    const int q = k * 32 + lane, row = q / (D / 8), ch = q % (D / 8), tok = t0 + row;
+                    uint32_t x[4] = {0, 0, 0, 0};
+                    if (tok < seen)
+                        *(uint4 *)x = *(const uint4 *)((tok < r ? res + (long long)tok * D
+                                                                : src.p + (long long)(t.row0[e] + tok - r) * src.ts
+                                                                      + w.s.h * src.hs)
+                                                       + ch * 8);
+                    if (masked) {
+                        // As in kivi_pool_rows.cu: values that are not finite
+                        // leave the product, rows that see them become NaN.
+                        constexpr uint32_t kExp = DT == KIVI_BF16 ? 0x7f80u : 0x7c00u;
+                        bool bad = false;
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) bad = bad || (x[z] & kExp) == kExp || ((x[z] >> 16) & kExp) == kExp;
+                        if (bad) {
+#pragma unroll
+                            for (int z = 0; z < 8; ++z)
+                                if (((x[z / 2] >> (16 * (z & 1))) & kExp) == kExp) {
+                                    for (int a = 0; a < w.nq; ++a) {
+                                        const int buf = a * kFirstBufs + seg % kFirstBufs;
+                                        atomicMin((unsigned long long *)(sm + S::FIRST) + buf * D + ch * 8 + z,
+                                                  bad_token(seg, tok - r));
+                                        ((volatile int *)(sm + S::FLAG))[buf] = seg;
+                                    }
+                                    x[z / 2] &= z & 1 ? 0x0000ffffu : 0xffff0000u;
+                                }
+                        }
+                    }
+                    *(uint4 *)(tile + (VAL ? value_at<D>(32 * sub + row, ch) : key_at<D>(32 * sub + row, ch))) =
+                        *(const uint4 *)x;
+                }
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) bar_arrive(full + 8 * st);
+        }
+        cp_async_wait_all();
+        __syncwarp();
+        ++seg;
+    }
+}
+
+// ---- the issuing thread -----------------------------------------------------------------
+template <int D, int DT>
+__device__ __forceinline__ void issue_role(const AttnCall &c, const AttnTab &t, uint8_t *sm, uint32_t bars, const Ctl &ctl,
+                                           uint32_t tmem, Walk w)
+{
+    using S = TileSmem<D>;
+    const uint32_t q_s = saddr(sm) + S::Q, k_s = saddr(sm) + S::K, v_s = saddr(sm) + S::V;
+    int it = 0;                       // key tiles so far
+    uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};   // phases of qfull, pfull
+    auto qk = [&](int a, int st, bool coded) {
+        // bf16 operands only for uncoded tokens of a bf16 pool.
+        const uint32_t inst = instruction(DT == KIVI_BF16 && !coded, kKeyRows, false);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+            mma_ss(tmem + a * 128, operand(q_s + a * S::QT + (k / 4) * (128 * 128) + (k % 4) * 32, 16),
+                   operand(k_s + st * S::KT + (k / 4) * (kKeyRows * 128) + (k % 4) * 32, 16), inst, k != 0);
+    };
+    auto pv = [&](int a, int st, bool coded, bool add) {
+        const uint32_t inst = instruction(DT == KIVI_BF16 && !coded, D, true);
+#pragma unroll
+        for (int k = 0; k < kTileTok / 16; ++k)
+            mma_ts(tmem + 256 + a * 128, tmem + a * 128 + k * 8, operand(v_s + st * S::VT + k * 2048, kTileTok * 128), inst,
+                   add || k != 0);
+    };
+    while (w.next(c, t)) {
+        for (int a = 0; a < w.nq; ++a)
+            if (!bar_wait(ctl, bars + 8 * (kQFull + a), qn[a]++ & 1)) return;
+        if (!bar_wait(ctl, bars + 8 * (kKFull + (it & 1)), (it >> 1) & 1)) return;
+        tc_after();
+        for (int a = 0; a < w.nq; ++a) {
+            qk(a, it & 1, w.i0 < w.s.nc);
+            tc_commit(bars + 8 * (kSFull + a));
+        }
+        tc_commit(bars + 8 * (kKEmpty + (it & 1)));
+#pragma unroll 1
+        for (int i = w.i0; i < w.i1; ++i, ++it) {
+            if (!bar_wait(ctl, bars + 8 * (kVFull + (it & 1)), (it >> 1) & 1)) return;
+            const bool more = i + 1 < w.i1;
+            const bool reload = DT == KIVI_BF16 && more && i + 1 == w.s.nc;
+            for (int a = 0; a < w.nq; ++a) {
+                if (!bar_wait(ctl, bars + 8 * (kPFull + a), pn[a]++ & 1)) return;
+                tc_after();
+                pv(a, it & 1, i < w.s.nc, i != w.i0);
+                if (more) {
+                    if (reload && !bar_wait(ctl, bars + 8 * (kQFull + a), qn[a]++ & 1)) return;
+                    if (a == 0 && !bar_wait(ctl, bars + 8 * (kKFull + ((it + 1) & 1)), ((it + 1) >> 1) & 1)) return;
+                    tc_after();
+                    qk(a, (it + 1) & 1, i + 1 < w.s.nc);
+                    tc_commit(bars + 8 * (kSFull + a));
+                } else {
+                    tc_commit(bars + 8 * (kOFull + a));
+                }
+            }
+            tc_commit(bars + 8 * (kVEmpty + (it & 1)));
+            if (more) tc_commit(bars + 8 * (kKEmpty + ((it + 1) & 1)));
+        }
+    }
+}
+
+// ---- softmax of one query tile: thread = row ------------------------------------------------
+template <int D, int DT>
+__device__ __forceinline__ void softmax_role(const AttnCall &c, const AttnTab &t, uint8_t *sm, uint32_t bars, const Ctl &ctl,
+                                             uint32_t tmem, int a, long long part, Walk w)
+{
+    using S = TileSmem<D>;
+    const int lane = threadIdx.x & 31, m_row = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)(m_row & ~31) << 16;   // the warp's TMEM lanes
+    const uint32_t s_t = tmem + a * 128 + lanes, o_t = tmem + 256 + a * 128 + lanes;
+    uint8_t *qs = sm + S::Q + a * S::QT;
+    uint32_t sn = 0, on = 0;   // phases of sfull, ofull
+    int seg = -1;
+    while (w.next(c, t)) {
+        ++seg;
+        if (a >= w.nq) continue;
+        const int e = w.s.e, ng = t.ng[e], r = t.r[e], nk = t.nk[e], n = t.n[e];
+        const long long row = (long long)w.s.rt * kTileRows + a * 128 + m_row;
+        const int tok = (int)(row / c.group), hq = w.s.h * c.group + (int)(row - (long long)tok * c.group);
+        const bool real = tok < n;
+        // Uncoded tokens that the row sees.
+        const int lim_raw = nk > 0 ? r + (tok + 1 < nk ? tok + 1 : nk) : r;
+        float sc = c.scale;
+        auto load_q = [&](bool coded) {
+            uint32_t x[D / 8][4];
+            const uint16_t *p = c.q.p + (long long)(t.row0[e] + tok) * c.q.ts + hq * c.q.hs;
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k) *(uint4 *)x[k] = real ? *(const uint4 *)(p + 8 * k) : make_uint4(0, 0, 0, 0);
+            sc = c.scale;
+            if constexpr (DT == KIVI_BF16) {
+                if (coded) {
+                    // fp16, times a power of two that brings the row's
+                    // largest magnitude to [2^13, 2^14).
+                    float mx = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < D / 8; ++k)
+#pragma unroll
+                        for (int z = 0; z < 4; ++z)
+                            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(x[k][z] << 16)),
+                                                 fabsf(__uint_as_float(x[k][z] & 0xffff0000u))));
+                    int k2 = 13 - ((int)(__float_as_uint(mx) >> 23) - 127);
+                    k2 = mx > 0.0f && mx < INFINITY ? max(-110, min(110, k2)) : 0;
+                    const float f = pow2(k2);
+                    sc = c.scale * pow2(-k2);
+#pragma unroll
+                    for (int k = 0; k < D / 8; ++k)
+#pragma unroll
+                        for (int z = 0; z < 4; ++z)
+                            x[k][z] = pack2<KIVI_F16>(__uint_as_float(x[k][z] << 16) * f,
+                                                      __uint_as_float(x[k][z] & 0xffff0000u) * f);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k) *(uint4 *)(qs + query_at(m_row, k)) = *(const uint4 *)x[k];
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) bar_arrive(bars + 8 * (kQFull + a));
+        };
+        load_q(w.i0 < w.s.nc);
+        float m = -INFINITY, l = 0.0f;
+#pragma unroll 1
+        for (int i = w.i0; i < w.i1; ++i) {
+            const bool coded = i < w.s.nc;
+            if (DT == KIVI_BF16 && i == w.s.nc && i > w.i0) load_q(false);
+            if (!warp_wait(ctl, bars + 8 * (kSFull + a), sn++ & 1)) return;
+            tc_after();
+            float b[3] = {0.0f, 0.0f, 0.0f};
+            // Columns that the row sees.
+            const int lim = coded ? (ng - 3 * i) * 32 : lim_raw - (i - w.s.nc) * kTileTok;
+            const bool cut = __any_sync(0xffffffffu, lim < kTileTok);
+            if (coded) {
+                uint32_t x[8];
+                tc_ld8(x, s_t + kTileTok);
+                tc_wait_ld();
+#pragma unroll
+                for (int g = 0; g < 3; ++g) b[g] = (__uint_as_float(x[g]) + __uint_as_float(x[3 + g])) * sc;
+            }
+            // The row's maximum.
+            float mx = -INFINITY;
+#pragma unroll
+            for (int g = 0; g < 3; ++g) {
+                uint32_t x[32];
+                tc_ld32(x, s_t + 32 * g);
+                tc_wait_ld();
+                float y = -INFINITY;
+                if (cut) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) y = 32 * g + k < lim ? fmaxf(y, __uint_as_float(x[k])) : y;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) y = fmaxf(y, __uint_as_float(x[k]));
+                }
+                mx = fmaxf(mx, fmaf(y, sc, b[g]));
+            }
+            const bool grow = mx > m + (kLazy - kRef);
+            if (__any_sync(0xffffffffu, grow)) {
+                const float nm = fmaxf(m, mx + kRef);
+                const float f = m == -INFINITY ? 0.0f : ex2(m - nm);
+                m = nm;
+                l *= f;
+                if (i != w.i0) {
+#pragma unroll 1
+                    for (int k = 0; k < D; k += 32) {
+                        uint32_t x[32];
+                        tc_ld32(x, o_t + k);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int z = 0; z < 32; ++z) x[z] = __float_as_uint(__uint_as_float(x[z]) * f);
+                        tc_st32(o_t + k, x);
+                    }
+                    tc_wait_st();
+                }
+            }
+            const float mm = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+            for (int g = 0; g < 3; ++g) {
+                uint32_t x[32], p[16];
+                tc_ld32(x, s_t + 32 * g);
+                tc_wait_ld();
+                const float off = b[g] - mm;
+                float sum = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) {
+                    float u = ex2(fmaf(__uint_as_float(x[k]), sc, off)), v = ex2(fmaf(__uint_as_float(x[k + 1]), sc, off));
+                    if (cut) {
+                        u = 32 * g + k < lim ? u : 0.0f;
+                        v = 32 * g + k + 1 < lim ? v : 0.0f;
+                    }
+                    sum += u + v;
+                    p[k / 2] = DT == KIVI_BF16 && !coded ? pack2<KIVI_BF16>(u, v) : pack2<KIVI_F16>(u, v);
+                }
+                l += sum;
+                tc_st16(s_t + 16 * g, p);
+            }
+            tc_wait_st();
+            tc_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(bars + 8 * (kPFull + a));
+        }
+        if (!warp_wait(ctl, bars + 8 * (kOFull + a), on++ & 1)) return;
+        tc_after();
+        // Rows that see a value that was taken out become NaN there.
+        const int buf = a * kFirstBufs + seg % kFirstBufs;
+        const unsigned long long *first = (const unsigned long long *)(sm + S::FIRST) + buf * D;
+        const bool bad = ((volatile int *)(sm + S::FLAG))[buf] == seg;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        float *po = c.part + part * 2 * kTilePart<D> + (w.s.base >= w.lo ? kTilePart<D> : 0);
+        uint16_t *out = c.out + ((long long)(t.row0[e] + tok) * c.H_q + hq) * D;
+#pragma unroll 1
+        for (int k = 0; k < D; k += 32) {
+            uint32_t x[32];
+            __syncwarp();
+            tc_ld32(x, o_t + k);
+            tc_wait_ld();
+            if (bad) {
+#pragma unroll
+                for (int z = 0; z < 32; ++z)
+                    if (bad_token(seg, tok) >= first[k + z]) x[z] = 0x7fffffffu;
+            }
+            if (real && w.whole) {
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    uint32_t y[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        y[q] = pack2<DT>(__uint_as_float(x[8 * z + 2 * q]) * inv, __uint_as_float(x[8 * z + 2 * q + 1]) * inv);
+                    *(uint4 *)(out + k + 8 * z) = *(const uint4 *)y;
+                }
+            } else if (real) {
+#pragma unroll
+                for (int z = 0; z < 8; ++z)
+                    *(uint4 *)(po + (long long)(a * 128 + m_row) * D + k + 4 * z) = *(const uint4 *)(x + 4 * z);
+            }
+        }
+        if (real && !w.whole) *(float2 *)(po + (long long)kTileRows * D + 2 * (a * 128 + m_row)) = make_float2(m, l);
+        tc_before();
+    }
+}
+
+template <int D, int DT>
+__global__ void __launch_bounds__(kThreads, 1)
+    pool_tiles_kernel(const __grid_constant__ AttnCall c, const __grid_constant__ AttnTab t)
+{
+    using S = TileSmem<D>;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t bars = saddr(sm) + S::BAR;
+    uint32_t *tmem_at = (uint32_t *)(sm + S::BAR + kBars * 8);
+    int *stop = (int *)(sm + S::BAR + kBars * 8 + 8);
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < 2; ++k) {
+            bar_init(bars + 8 * (kKFull + k), 3);
+            bar_init(bars + 8 * (kKEmpty + k), 1);
+            bar_init(bars + 8 * (kVFull + k), 3);
+            bar_init(bars + 8 * (kVEmpty + k), 1);
+            bar_init(bars + 8 * (kQFull + k), 4);
+            bar_init(bars + 8 * (kSFull + k), 1);
+            bar_init(bars + 8 * (kPFull + k), 4);
+            bar_init(bars + 8 * (kOFull + k), 1);
+        }
+        *stop = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    for (int k = threadIdx.x; k < 2 * kFirstBufs * D; k += kThreads) ((unsigned long long *)(sm + S::FIRST))[k] = ~0ull;
+    if (threadIdx.x < 2 * kFirstBufs) ((int *)(sm + S::FLAG))[threadIdx.x] = -1;
+    if (wid == 14) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(saddr(tmem_at)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = *tmem_at;
+    const Ctl ctl{stop, c.err};
+    const long long tot = t.off[t.nb];
+    Walk w;
+    w.lo = w.pos = range_at(blockIdx.x, tot, c.warps);
+    w.hi = range_at(blockIdx.x + 1, tot, c.warps);
+    if (wid < 8) softmax_role<D, DT>(c, t, sm, bars, ctl, tmem, wid >> 2, blockIdx.x, w);
+    else if (wid < 11) decode_role<D, DT, 0>(c, t, sm, bars, ctl, wid - 8, w);
+    else if (wid < 14) decode_role<D, DT, 1>(c, t, sm, bars, ctl, wid - 11, w);
+    else if (lane == 0) {
+        issue_role<D, DT>(c, t, sm, bars, ctl, tmem, w);
+        if (*ctl.stop) {
+            // Some wait gave up: let the products issued so far finish before
+            // their memory goes away (a barrier of its own, with a limit).
+            const uint32_t b = bars + 8 * kBars + 16;
+            bar_init(b, 1);
+            tc_commit(b);
+            const uint64_t t0 = now_ns();
+            while (!bar_test(b, 0) && now_ns() - t0 < kWaitNs) {
+            }
+        }
+    }
+    cp_async_wait_all();
+    tc_before();
+    __syncthreads();
+    tc_after();
+    __syncwarp();
+    if (wid == 14) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// Adds the partial results of the segment that starts in range blockIdx.x and
+// ends behind it (if there is one): a warp per row, rows by blockIdx.y.
+template <int D, int DT>
+__global__ void __launch_bounds__(256) pool_tiles_join_kernel(const __grid_constant__ AttnCall c,
+                                                              const __grid_constant__ AttnTab t)
+{
+    const long long w = blockIdx.x, tot = t.off[t.nb];
+    const long long lo = range_at(w, tot, c.warps), hi = range_at(w + 1, tot, c.warps);
+    if (hi >= tot || lo >= hi) return;
+    const TSeg s = find_segment(t, c, hi - 1);
+    const long long end = s.base + s.nc + s.nr;
+    if (s.base < lo || end <= hi) return;
+    const int lane = threadIdx.x & 31;
+    const long long last = (end * c.warps - 1) / tot;
+    constexpr int E = D / 32;
+    for (int k = threadIdx.x >> 5; k < kTileRows / 8; k += 8) {
+        const int lr = blockIdx.y * (kTileRows / 8) + k;
+        const long long row = (long long)s.rt * kTileRows + lr;
+        const int tok = (int)(row / c.group);
+        if (tok >= t.n[s.e]) return;
+        float m = -INFINITY, l = 0.0f, o[E];
+#pragma unroll
+        for (int z = 0; z < E; ++z) o[z] = 0.0f;
+        for (long long x = w; x <= last; ++x) {
+            const float *po = c.part + x * 2 * kTilePart<D> + (x == w ? kTilePart<D> : 0);
+            const float2 ml = *(const float2 *)(po + (long long)kTileRows * D + 2 * lr);
+            float y[E];
+#pragma unroll
+            for (int z = 0; z < E; ++z) y[z] = po[(long long)lr * D + lane * E + z];
+            if (ml.y == 0.0f) continue;   // nothing seen (a NaN sum counts)
+            const float mn = fmaxf(m, ml.x);
+            const float f = m == -INFINITY ? 0.0f : ex2(m - mn), g = ex2(ml.x - mn);
+            l = l * f + ml.y * g;
+#pragma unroll
+            for (int z = 0; z < E; ++z) o[z] = o[z] * f + y[z] * g;
+            m = mn;
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        uint16_t *out = c.out
+                        + ((long long)(t.row0[s.e] + tok) * c.H_q + s.h * c.group + (row - (long long)tok * c.group)) * D;
+#pragma unroll
+        for (int z = 0; z < E; z += 2) *(uint32_t *)(out + lane * E + z) = pack2<DT>(o[z] * inv, o[z + 1] * inv);
+    }
+}
+
+template <int D, int DT>
+cudaError_t tiles_t(AttnCall &c, AttnTab &t, cudaStream_t st)
+{
+    static PerDeviceOnce once;
+    cudaError_t e = set_smem_once(once, pool_tiles_kernel<D, DT>, TileSmem<D>::BYTES);
+    if (e != cudaSuccess) return e;
+    pool_tiles_kernel<D, DT><<<(unsigned)c.warps, kThreads, TileSmem<D>::BYTES, st>>>(c, t);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || c.warps == 1) return e;
+    pool_tiles_join_kernel<D, DT><<<dim3((unsigned)c.warps, 8), 256, 0, st>>>(c, t);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t pool_tiles_scratch(int D, int sms) { return (size_t)2 * sms * kTileRows * (D + 2); }
+
+// Every entry sees at least one token.
+cudaError_t launch_pool_tiles(AttnCall &c, AttnTab &t, int sms, cudaStream_t st)
+{
+    t.off[0] = 0;
+    for (int e = 0; e < t.nb; ++e) {
+        long long per_head = 0;
+        const int tiles = (int)(((long long)t.n[e] * c.group + kTileRows - 1) / kTileRows);
+        for (int rt = 0; rt < tiles; ++rt)
+            per_head += coded_tiles(t.ng[e]) + (raw_seen(t.r[e], t.nk[e], t.n[e], c.group, rt) + kTileTok - 1) / kTileTok;
+        t.off[e + 1] = t.off[e] + per_head * c.v.H;
+    }
+    const long long tot = t.off[t.nb];
+    if (tot == 0) return cudaSuccess;
+    c.warps = sms < tot ? sms : tot;
+    if (tot > (1LL << 62) / (c.warps + 1)) return cudaErrorInvalidValue;
+    if (c.v.D == 64) return c.v.dtype ? tiles_t<64, 1>(c, t, st) : tiles_t<64, 0>(c, t, st);
+    return c.v.dtype ? tiles_t<128, 1>(c, t, st) : tiles_t<128, 0>(c, t, st);
+}
+
+}  // namespace kivi
