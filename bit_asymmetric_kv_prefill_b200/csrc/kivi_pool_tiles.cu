@@ -14,9 +14,9 @@
 // are, in the pool's type; the queries are reloaded for them, since bf16 ones
 // are scaled to fp16 for the coded tiles.
 //
-// Roles (15 warps): warps 0-3 and 4-7 are the softmax of query tiles 0 and 1
-// (thread = row, no exchange between threads), warps 8-10 and 11-13 decode the
-// keys and values of one 32-token group each, warp 14 issues the products.
+// Roles (24 warps): warps 0-3 and 4-7 are the softmax of query tiles 0 and 1
+// (thread = row, no exchange between threads), warps 8-13 and 14-19 decode the
+// keys and values of 16 tokens each, warp 20 issues the products.
 // The order QK(i + 1) after PV(i) of each query tile lets one tile's softmax
 // run under the other's products; S and P share TMEM columns because products
 // of one CTA execute in order.
@@ -40,8 +40,13 @@ namespace {
 constexpr int kTileTok = 96;             // tokens per key tile
 constexpr int kKeyRows = 112;            // rows of the key tile: tokens, 3 z, 3 s, unused
 constexpr int kTileRows = 256;           // query rows per CTA
-constexpr int kThreads = 15 * 32;
-constexpr int kRing = 3;                 // coded halves in flight per decoding warp
+constexpr int kSoftWarps = 8, kDecodeWarps = 12;
+constexpr int kThreads = 24 * 32;        // three warps idle: registers move by warpgroups
+// Registers: 80 a thread at launch (61,440), then 256 x 128 + 512 x 56.
+constexpr int kSoftRegs = 128, kWorkRegs = 56;
+constexpr int kProbAt = 48;               // P's first TMEM column within S's
+constexpr int kRing = 3;                 // coded tiles in flight per decoding warp
+constexpr int kSlot = 1024;              // bytes of a ring slot: 16 tokens' codes and their scales and zeros
 constexpr int kFirstBufs = 4;
 constexpr float kLazy = 3.0f;            // the running maximum follows when exceeded by 2^kLazy
 constexpr float kRef = -8.0f;            // p is kept times 2^8: fp16 keeps 2^-32 of the largest
@@ -53,12 +58,11 @@ struct TileSmem {
     static constexpr int QT = KB * 128 * 128;              // one query tile
     static constexpr int KT = KB * kKeyRows * 128;         // one key tile
     static constexpr int VT = KB * kTileTok * 128;         // one value tile
-    static constexpr int HALF = 12 * D;                    // K or V half of a group block
     static constexpr int Q = 0;
     static constexpr int K = Q + 2 * QT;
     static constexpr int V = K + 2 * KT;
     static constexpr int RING = V + 2 * VT;
-    static constexpr int FIRST = RING + 6 * kRing * HALF;  // [query tile][buffer][D] first token with a bad value
+    static constexpr int FIRST = RING + kDecodeWarps * kRing * kSlot;  // [query tile][buffer][D] first token with a bad value
     static constexpr int FLAG = FIRST + 2 * kFirstBufs * D * 8;
     static constexpr int BAR = FLAG + 2 * kFirstBufs * 4;
     static constexpr int BYTES = BAR + 24 * 8 + 16;
@@ -102,7 +106,7 @@ __device__ __forceinline__ uint64_t now_ns()
 
 // Waits for the barrier's phase; false when this wait, or another of the CTA,
 // gave up (then the caller leaves).
-__device__ __noinline__ bool bar_wait_long(const Ctl &ctl, uint32_t b, uint32_t phase)
+__device__ __forceinline__ bool bar_wait_long(const Ctl &ctl, uint32_t b, uint32_t phase)
 {
     const uint64_t t0 = now_ns();
 #pragma unroll 1
@@ -134,6 +138,22 @@ __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.a
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Ties registers to this place: what a TMEM load fills must not be used before
+// the wait, which the compiler does not know to be their producer.
+template <int N>
+__device__ __forceinline__ void here(uint32_t (&r)[N])
+{
+#pragma unroll
+    for (int k = 0; k < N; k += 8)
+        asm volatile("" : "+r"(r[k]), "+r"(r[k + 1]), "+r"(r[k + 2]), "+r"(r[k + 3]), "+r"(r[k + 4]), "+r"(r[k + 5]),
+                          "+r"(r[k + 6]), "+r"(r[k + 7])::"memory");
+}
+template <typename... R>
+__device__ __forceinline__ void tc_wait_ld(R &...r)
+{
+    tc_wait_ld();
+    (here(r), ...);
+}
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_commit(uint32_t b)
 {
@@ -153,23 +173,21 @@ __device__ __forceinline__ void tc_ld32(uint32_t (&r)[32], uint32_t a)
         : "r"(a)
         : "memory");
 }
+__device__ __forceinline__ void tc_ld16(uint32_t (&r)[16], uint32_t a)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(a)
+        : "memory");
+}
 __device__ __forceinline__ void tc_ld8(uint32_t (&r)[8], uint32_t a)
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(a)
                  : "memory");
-}
-__device__ __forceinline__ void tc_st32(uint32_t a, const uint32_t (&r)[32])
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(a),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
 }
 __device__ __forceinline__ void tc_st16(uint32_t a, const uint32_t (&r)[16])
 {
@@ -341,45 +359,46 @@ __device__ __forceinline__ unsigned long long bad_token(int seg, int tok)
     return ((unsigned long long)(0x7fffffff - seg) << 32) | (uint32_t)(tok + 0x40000000);
 }
 
-// ---- decoding warps: one 32-token group of keys (VAL = 0) or values ----------------------
+// ---- decoding warps: 16 tokens (half hf of group sub) of keys (VAL = 0) or values --------
 template <int D, int DT, int VAL>
 __device__ __forceinline__ void decode_role(const AttnCall &c, const AttnTab &t, uint8_t *sm, uint32_t bars, const Ctl &ctl,
-                                            int sub, Walk w)
+                                            int sub, int hf, Walk w)
 {
     using L = PageLayout<D>;
     using S = TileSmem<D>;
     const int lane = threadIdx.x & 31, tq = lane >> 2, cs = lane & 3;
     const PoolView &v = c.v;
+    const int row0 = 32 * sub + 16 * hf;   // the warp's rows of the tile
     uint32_t one[5];
 #pragma unroll
     for (int k = 0; k < 5; ++k)
         asm volatile("mov.b32 %0, %1;" : "=r"(one[k]) : "r"((uint32_t)((25 - 2 * k) << 10) * 0x10001u));
-    uint8_t *ring = sm + S::RING + (VAL * 3 + sub) * kRing * S::HALF;
-    const uint32_t ring_s = saddr(ring);
+    uint8_t *ring = sm + S::RING + (VAL * 6 + sub * 2 + hf) * kRing * kSlot;
+    const uint32_t ring_s = saddr(ring) + lane * 16;
     const uint32_t full = bars + 8 * (VAL ? kVFull : kKFull), empty = bars + 8 * (VAL ? kVEmpty : kKEmpty);
     int it = 0, seg = 0;
     while (w.next(c, t)) {
         const int e = w.s.e, ng = t.ng[e], r = t.r[e], nk = t.nk[e], seq = t.seq[e];
         const int *table = v.table + (long long)seq * v.max_pages;
-        // Coded halves through the ring, kRing - 1 tiles ahead.
+        // A slot holds the lanes' code words (D = 64: of the whole group), then
+        // K: the group's scales and zeros, V: those of the 16 tokens.
+        constexpr int kMeta = VAL ? 2 * D : 4 * D;
+        int slot_in = 0, slot_out = 0;
         auto fetch = [&](int i) {
             const int g = 3 * i + sub;
             if (i < w.i1 && i < w.s.nc && g < ng) {
-                const uint8_t *src = v.packed + ((long long)table[g / v.gpp] * v.H + w.s.h) * ((long long)v.gpp * L::GB)
-                                     + (long long)(g % v.gpp) * L::GB + (VAL ? L::VC : L::KC);
-                const uint32_t to = ring_s + (uint32_t)((i - w.i0) % kRing) * S::HALF;
-#pragma unroll
-                for (int k = 0; k < S::HALF / 512; ++k)
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + (k * 32 + lane) * 16),
-                                 "l"(src + (k * 32 + lane) * 16)
+                const uint8_t *blk = v.packed + ((long long)table[g / v.gpp] * v.H + w.s.h) * ((long long)v.gpp * L::GB)
+                                     + (long long)(g % v.gpp) * L::GB;
+                const uint32_t to = ring_s + slot_in * kSlot;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to),
+                             "l"(blk + (VAL ? L::VC : L::KC) + (D == 128 ? hf * 512 : 0) + lane * 16)
+                             : "memory");
+                if (lane < kMeta / 16)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 512),
+                                 "l"(blk + (VAL ? L::VM + hf * 2 * D : L::KS) + lane * 16)
                                  : "memory");
-                if constexpr (S::HALF % 512 != 0)
-                    if (lane < S::HALF % 512 / 16)
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                         to + ((S::HALF / 512) * 32 + lane) * 16),
-                                     "l"(src + ((S::HALF / 512) * 32 + lane) * 16)
-                                     : "memory");
             }
+            slot_in = slot_in + 1 == kRing ? 0 : slot_in + 1;
             cp_async_commit();
         };
         for (int k = 0; k < kRing - 1; ++k) fetch(w.i0 + k);
@@ -392,53 +411,50 @@ __device__ __forceinline__ void decode_role(const AttnCall &c, const AttnTab &t,
                 asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
                 __syncwarp();
                 fetch(i + kRing - 1);
-                const uint8_t *half = ring + ((i - w.i0) % kRing) * S::HALF;
-                const bool real = 3 * i + sub < ng;
-                if (!real) {
+                const uint8_t *slot = ring + slot_out * kSlot;
+                slot_out = slot_out + 1 == kRing ? 0 : slot_out + 1;
+                if (3 * i + sub >= ng) {
                     // No such group: zeros.
 #pragma unroll
-                    for (int k = 0; k < D / 8; ++k) {
-                        const int q = k * 32 + lane, row = 32 * sub + q / (D / 8), ch = q % (D / 8);
+                    for (int k = 0; k < D / 16; ++k) {
+                        const int q = k * 32 + lane, row = row0 + q / (D / 8), ch = q % (D / 8);
                         *(uint4 *)(tile + (VAL ? value_at<D>(row, ch) : key_at<D>(row, ch))) = make_uint4(0, 0, 0, 0);
                     }
                 } else if constexpr (VAL == 0) {
-                    uint32_t kw[L::WPL];
-#pragma unroll
-                    for (int q = 0; q < L::WPL / 4; ++q)
-                        *(uint4 *)(kw + 4 * q) = *(const uint4 *)(half + (q * 32 + lane) * 16);
+                    // Words of tokens tq + 8(2hf + jj).
+                    uint32_t kw[4];
+                    *(uint4 *)kw = *(const uint4 *)(slot + lane * 16);
 #pragma unroll
                     for (int u = 0; u < D / 32; ++u) {
                         uint32_t s[4];
-                        *(uint4 *)s = *(const uint4 *)(half + (L::KS - L::KC) + u * 64 + cs * 16);
+                        *(uint4 *)s = *(const uint4 *)(slot + 512 + u * 64 + cs * 16);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t x = kw[j * L::KW + u / 2], x10 = x >> 10;
+                        for (int jj = 0; jj < 2; ++jj) {
+                            const uint32_t x = D == 128 ? kw[jj * 2 + u / 2] : hf ? kw[2 + jj] : kw[jj];
+                            const uint32_t x10 = x >> 10;
                             uint32_t o[4];
 #pragma unroll
                             for (int p = 0; p < 4; ++p)
                                 o[p] = as_u(__hmul2(code_less(x, x10, 4 * (u % 2) + p, 1, one), as_h2(s[p])));
-                            *(uint4 *)(tile + key_at<D>(32 * sub + tq + 8 * j, 4 * u + cs)) = *(const uint4 *)o;
+                            *(uint4 *)(tile + key_at<D>(row0 + tq + 8 * jj, 4 * u + cs)) = *(const uint4 *)o;
                         }
                     }
-                    // Rows 96 + sub (z) and 99 + sub (s).
-                    if (lane < D / 8) {
-                        *(uint4 *)(tile + key_at<D>(kTileTok + sub, lane)) =
-                            *(const uint4 *)(half + (L::KZ - L::KC) + lane * 16);
-                        *(uint4 *)(tile + key_at<D>(kTileTok + 3 + sub, lane)) =
-                            *(const uint4 *)(half + (L::KS - L::KC) + lane * 16);
-                    }
+                    // Row 96 + sub holds the group's z, row 99 + sub its s.
+                    if (lane < D / 8)
+                        *(uint4 *)(tile + key_at<D>(kTileTok + (hf ? 3 : 0) + sub, lane)) =
+                            *(const uint4 *)(slot + 512 + (hf ? 0 : 2 * D) + lane * 16);
                 } else {
-                    uint32_t vw[L::WPL];
-#pragma unroll
-                    for (int q = 0; q < L::WPL / 4; ++q)
-                        *(uint4 *)(vw + 4 * q) = *(const uint4 *)(half + (q * 32 + lane) * 16);
+                    // Words of token pairs 8(2hf + pp) + 2cs.
+                    uint32_t vw[4];
+                    *(uint4 *)vw = *(const uint4 *)(slot + lane * 16);
                     const uint32_t tile_s = saddr(tile);
 #pragma unroll
-                    for (int p = 0; p < 4; ++p)
+                    for (int pp = 0; pp < 2; ++pp)
 #pragma unroll
                         for (int jh = 0; jh < L::KW; ++jh) {
-                            const uint4 sz = *(const uint4 *)(half + (L::VM - L::VC) + page_vm_offset<D>(p, cs, 2 * jh));
-                            const uint32_t x = vw[p * L::KW + jh], x10 = x >> 10;
+                            const uint4 sz = *(const uint4 *)(slot + 512 + page_vm_offset<D>(pp, cs, 2 * jh));
+                            const uint32_t x = D == 128 ? vw[pp * 2 + jh] : hf ? vw[2 + pp] : vw[pp];
+                            const uint32_t x10 = x >> 10;
 #pragma unroll
                             for (int jj = 0; jj < 2; ++jj) {
                                 uint32_t o[4];
@@ -447,7 +463,7 @@ __device__ __forceinline__ void decode_role(const AttnCall &c, const AttnTab &t,
                                     o[k] = as_u(__hfma2(code_less(x, x10, 4 * jj + k, 0, one), as_h2(jj ? sz.z : sz.x),
                                                         as_h2(jj ? sz.w : sz.y)));
                                 const uint32_t a =
-                                    tile_s + value_at<D>(32 * sub + 8 * p + (lane & 7), 8 * jh + 4 * jj + (lane >> 3));
+                                    tile_s + value_at<D>(row0 + 8 * pp + (lane & 7), 8 * jh + 4 * jj + (lane >> 3));
                                 asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(a),
                                              "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
                                              : "memory");
@@ -455,45 +471,53 @@ __device__ __forceinline__ void decode_role(const AttnCall &c, const AttnTab &t,
                         }
                 }
             } else {
-                // 32 uncoded tokens: residual, then new ones.
+                // 16 uncoded tokens: residual, then new ones.
                 const int seen = raw_seen(r, nk, t.n[e], c.group, w.s.rt);
-                const int t0 = (i - w.s.nc) * kTileTok + 32 * sub;
+                const int t0 = (i - w.s.nc) * kTileTok + row0;
                 const uint16_t *res = (VAL ? v.resV : v.resK) + ((long long)seq * v.H + w.s.h) * v.R * D;
                 const Rows &src = VAL ? c.nv : c.k;
                 // Some row does not see the last of these tokens.
-                const bool masked = VAL && t0 + 32 > r && t0 + 31 - r > (int)((long long)w.s.rt * kTileRows / c.group);
+                const bool masked = VAL && t0 + 16 > r && t0 + 15 - r > (int)((long long)w.s.rt * kTileRows / c.group);
+                const uint32_t tile_s = saddr(tile);
 #pragma unroll 4
-                for (int k = 0; k < D / 8; ++k) {
+                for (int k = 0; k < D / 16; ++k) {
                     const int q = k * 32 + lane, row = q / (D / 8), ch = q % (D / 8), tok = t0 + row;
-                    uint32_t x[4] = {0, 0, 0, 0};
-                    if (tok < seen)
-                        *(uint4 *)x = *(const uint4 *)((tok < r ? res + (long long)tok * D
-                                                                : src.p + (long long)(t.row0[e] + tok - r) * src.ts
-                                                                      + w.s.h * src.hs)
-                                                       + ch * 8);
-                    if (masked) {
-                        // As in kivi_pool_rows.cu: values that are not finite
-                        // leave the product, rows that see them become NaN.
-                        constexpr uint32_t kExp = DT == KIVI_BF16 ? 0x7f80u : 0x7c00u;
+                    const uint16_t *p = tok < r ? res + (long long)tok * D
+                                                : src.p + (long long)(t.row0[e] + tok - r) * src.ts + w.s.h * src.hs;
+                    const int bytes = tok < seen ? 16 : 0;   // past the end: zeros
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                     tile_s + (VAL ? value_at<D>(row0 + row, ch) : key_at<D>(row0 + row, ch))),
+                                 "l"((tok < seen ? p : res) + ch * 8), "r"(bytes)
+                                 : "memory");
+                }
+                cp_async_commit();
+                cp_async_wait_all();
+                if (masked) {
+                    // As in kivi_pool_rows.cu: values that are not finite
+                    // leave the product, rows that see them become NaN.
+                    constexpr uint32_t kExp = DT == KIVI_BF16 ? 0x7f80u : 0x7c00u;
+#pragma unroll 1
+                    for (int k = 0; k < D / 16; ++k) {   // (the lane's own copies)
+                        const int q = k * 32 + lane, row = q / (D / 8), ch = q % (D / 8), tok = t0 + row;
+                        uint16_t *p = (uint16_t *)(tile + value_at<D>(row0 + row, ch));
+                        uint32_t x[4];
+                        *(uint4 *)x = *(const uint4 *)p;
                         bool bad = false;
 #pragma unroll
                         for (int z = 0; z < 4; ++z) bad = bad || (x[z] & kExp) == kExp || ((x[z] >> 16) & kExp) == kExp;
-                        if (bad) {
-#pragma unroll
+                        if (bad)
+#pragma unroll 1
                             for (int z = 0; z < 8; ++z)
-                                if (((x[z / 2] >> (16 * (z & 1))) & kExp) == kExp) {
+                                if ((p[z] & kExp) == kExp) {
                                     for (int a = 0; a < w.nq; ++a) {
                                         const int buf = a * kFirstBufs + seg % kFirstBufs;
                                         atomicMin((unsigned long long *)(sm + S::FIRST) + buf * D + ch * 8 + z,
                                                   bad_token(seg, tok - r));
                                         ((volatile int *)(sm + S::FLAG))[buf] = seg;
                                     }
-                                    x[z / 2] &= z & 1 ? 0x0000ffffu : 0xffff0000u;
+                                    p[z] = 0;
                                 }
-                        }
                     }
-                    *(uint4 *)(tile + (VAL ? value_at<D>(32 * sub + row, ch) : key_at<D>(32 * sub + row, ch))) =
-                        *(const uint4 *)x;
                 }
             }
             fence_async_smem();
@@ -506,74 +530,218 @@ __device__ __forceinline__ void decode_role(const AttnCall &c, const AttnTab &t,
     }
 }
 
-// ---- the issuing thread -----------------------------------------------------------------
+// ---- the issuing warp -------------------------------------------------------------------
+// All lanes walk together, so that addresses and descriptors stay uniform
+// registers, which the instructions want; one elected lane issues.  (With one
+// lane walking alone each product cost about 25 instructions to move its
+// operands, 135 cycles: as long as two products take.)
+__device__ __forceinline__ bool elected()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 template <int D, int DT>
 __device__ __forceinline__ void issue_role(const AttnCall &c, const AttnTab &t, uint8_t *sm, uint32_t bars, const Ctl &ctl,
-                                           uint32_t tmem, Walk w)
+                                           Walk w)
 {
     using S = TileSmem<D>;
-    const uint32_t q_s = saddr(sm) + S::Q, k_s = saddr(sm) + S::K, v_s = saddr(sm) + S::V;
-    int it = 0;                       // key tiles so far
+    const uint32_t base = saddr(sm);
+    int it = 0;                            // key tiles so far
     uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};   // phases of qfull, pfull
     auto qk = [&](int a, int st, bool coded) {
         // bf16 operands only for uncoded tokens of a bf16 pool.
         const uint32_t inst = instruction(DT == KIVI_BF16 && !coded, kKeyRows, false);
+        const uint64_t q0 = operand(base + S::Q + a * S::QT, 16), k0 = operand(base + S::K + st * S::KT, 16);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-            mma_ss(tmem + a * 128, operand(q_s + a * S::QT + (k / 4) * (128 * 128) + (k % 4) * 32, 16),
-                   operand(k_s + st * S::KT + (k / 4) * (kKeyRows * 128) + (k % 4) * 32, 16), inst, k != 0);
+            mma_ss(a * 128, q0 + ((k / 4) * (128 * 128) + (k % 4) * 32) / 16,
+                   k0 + ((k / 4) * (kKeyRows * 128) + (k % 4) * 32) / 16, inst, k != 0);
     };
     auto pv = [&](int a, int st, bool coded, bool add) {
         const uint32_t inst = instruction(DT == KIVI_BF16 && !coded, D, true);
+        const uint64_t v0 = operand(base + S::V + st * S::VT, kTileTok * 128);
 #pragma unroll
         for (int k = 0; k < kTileTok / 16; ++k)
-            mma_ts(tmem + 256 + a * 128, tmem + a * 128 + k * 8, operand(v_s + st * S::VT + k * 2048, kTileTok * 128), inst,
-                   add || k != 0);
+            mma_ts(256 + a * 128, a * 128 + kProbAt + k * 8, v0 + k * 2048 / 16, inst, add || k != 0);
     };
     while (w.next(c, t)) {
         for (int a = 0; a < w.nq; ++a)
-            if (!bar_wait(ctl, bars + 8 * (kQFull + a), qn[a]++ & 1)) return;
-        if (!bar_wait(ctl, bars + 8 * (kKFull + (it & 1)), (it >> 1) & 1)) return;
+            if (!warp_wait(ctl, bars + 8 * (kQFull + a), qn[a]++ & 1)) return;
+        if (!warp_wait(ctl, bars + 8 * (kKFull + (it & 1)), (it >> 1) & 1)) return;
         tc_after();
-        for (int a = 0; a < w.nq; ++a) {
-            qk(a, it & 1, w.i0 < w.s.nc);
-            tc_commit(bars + 8 * (kSFull + a));
+        if (elected()) {
+            for (int a = 0; a < w.nq; ++a) {
+                qk(a, it & 1, w.i0 < w.s.nc);
+                tc_commit(bars + 8 * (kSFull + a));
+            }
+            tc_commit(bars + 8 * (kKEmpty + (it & 1)));
         }
-        tc_commit(bars + 8 * (kKEmpty + (it & 1)));
+        __syncwarp();
 #pragma unroll 1
         for (int i = w.i0; i < w.i1; ++i, ++it) {
-            if (!bar_wait(ctl, bars + 8 * (kVFull + (it & 1)), (it >> 1) & 1)) return;
+            if (!warp_wait(ctl, bars + 8 * (kVFull + (it & 1)), (it >> 1) & 1)) return;
             const bool more = i + 1 < w.i1;
             const bool reload = DT == KIVI_BF16 && more && i + 1 == w.s.nc;
-            for (int a = 0; a < w.nq; ++a) {
-                if (!bar_wait(ctl, bars + 8 * (kPFull + a), pn[a]++ & 1)) return;
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+                if (a >= w.nq) break;
+                if (!warp_wait(ctl, bars + 8 * (kPFull + a), pn[a]++ & 1)) return;
                 tc_after();
-                pv(a, it & 1, i < w.s.nc, i != w.i0);
+                if (elected()) {
+                    pv(a, it & 1, i < w.s.nc, i != w.i0);
+                    if (!more) tc_commit(bars + 8 * (kOFull + a));
+                }
+                __syncwarp();
                 if (more) {
-                    if (reload && !bar_wait(ctl, bars + 8 * (kQFull + a), qn[a]++ & 1)) return;
-                    if (a == 0 && !bar_wait(ctl, bars + 8 * (kKFull + ((it + 1) & 1)), ((it + 1) >> 1) & 1)) return;
+                    if (reload && !warp_wait(ctl, bars + 8 * (kQFull + a), qn[a]++ & 1)) return;
+                    if (a == 0 && !warp_wait(ctl, bars + 8 * (kKFull + ((it + 1) & 1)), ((it + 1) >> 1) & 1)) return;
                     tc_after();
-                    qk(a, (it + 1) & 1, i + 1 < w.s.nc);
-                    tc_commit(bars + 8 * (kSFull + a));
-                } else {
-                    tc_commit(bars + 8 * (kOFull + a));
+                    if (elected()) {
+                        qk(a, (it + 1) & 1, i + 1 < w.s.nc);
+                        tc_commit(bars + 8 * (kSFull + a));
+                    }
+                    __syncwarp();
                 }
             }
-            tc_commit(bars + 8 * (kVEmpty + (it & 1)));
-            if (more) tc_commit(bars + 8 * (kKEmpty + ((it + 1) & 1)));
+            if (elected()) {
+                tc_commit(bars + 8 * (kVEmpty + (it & 1)));
+                if (more) tc_commit(bars + 8 * (kKEmpty + ((it + 1) & 1)));
+            }
+            __syncwarp();
         }
     }
+}
+
+// ---- two fp32 at once ------------------------------------------------------------------
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float &a, float &b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// The largest of 32 scores; CUT: those from column lim - c0 on become -inf.
+template <bool CUT>
+__device__ __forceinline__ float row_max(uint32_t (&x)[32], int c0, int lim)
+{
+    float y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+        if (CUT && c0 + k >= lim) x[k] = 0xff800000u;
+        y[k & 3] = fmaxf(y[k & 3], __uint_as_float(x[k]));
+    }
+    return fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+}
+
+// 2^(x sc + off) of 32 scores to 16 columns at p, packed; their sum to sum.
+template <bool CUT, bool BF16>
+__device__ __forceinline__ void row_exp(const uint32_t (&x)[32], uint32_t p_t, uint64_t sc, float off1, int c0, int lim,
+                                        uint64_t &sum)
+{
+    const uint64_t off = pair(off1, off1);
+    uint32_t p[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        float u, v;
+        unpair(fma2(pair(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), sc, off), u, v);
+        u = ex2(u);
+        v = ex2(v);
+        if (CUT) {
+            u = c0 + 2 * k < lim ? u : 0.0f;
+            v = c0 + 2 * k + 1 < lim ? v : 0.0f;
+        }
+        sum = add2(sum, pair(u, v));
+        p[k] = pack2<BF16 ? KIVI_BF16 : KIVI_F16>(u, v);
+    }
+    tc_st16(p_t, p);
+}
+
+// One key tile of a row: scores from TMEM (times sc in units of log2),
+// probabilities back over them.  CUT: columns from lim on are not seen.  The
+// scores are read twice, 32 at a time (96 would not fit the registers beside
+// them); the probabilities of the third, second, first 32 go to columns 80,
+// 64, 48, where scores that are no longer needed stood.
+template <int D, bool CODED, bool CUT, bool BF16>
+__device__ __forceinline__ void softmax_step(uint32_t s_t, uint32_t o_t, float sc, int lim, bool first, float &m, float &l)
+{
+    uint32_t x[32], y[32];
+    float b[3] = {0.0f, 0.0f, 0.0f};
+    tc_ld32(x, s_t);
+    tc_ld32(y, s_t + 32);
+    if constexpr (CODED) {
+        uint32_t z[8];
+        tc_ld8(z, s_t + kTileTok);
+        tc_wait_ld(x, y, z);
+#pragma unroll
+        for (int g = 0; g < 3; ++g)   // (a group that is not there has no zeros)
+            if (!CUT || 32 * g < lim) b[g] = (__uint_as_float(z[g]) + __uint_as_float(z[3 + g])) * sc;
+    } else {
+        tc_wait_ld(x, y);
+    }
+    float mx = fmaf(row_max<CUT>(x, 0, lim), sc, b[0]);
+    tc_ld32(x, s_t + 64);
+    mx = fmaxf(mx, fmaf(row_max<CUT>(y, 32, lim), sc, b[1]));
+    tc_wait_ld(x);
+    tc_ld32(y, s_t + 32);
+    mx = fmaxf(mx, fmaf(row_max<CUT>(x, 64, lim), sc, b[2]));
+    if (__any_sync(0xffffffffu, mx > m + (kLazy - kRef))) {
+        const float nm = fmaxf(m, mx + kRef);
+        const float f = m == -INFINITY ? 0.0f : ex2(m - nm);
+        m = nm;
+        l *= f;
+        if (!first) {
+#pragma unroll 1
+            for (int k = 0; k < D; k += 16) {
+                uint32_t o[16];
+                tc_ld16(o, o_t + k);
+                tc_wait_ld(o);
+#pragma unroll
+                for (int z = 0; z < 16; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) * f);
+                tc_st16(o_t + k, o);
+            }
+        }
+    }
+    const float mm = m == -INFINITY ? 0.0f : m;
+    const uint64_t sc2 = pair(sc, sc);
+    uint64_t sum = 0;
+    row_exp<CUT, BF16>(x, s_t + kProbAt + 32, sc2, b[2] - mm, 64, lim, sum);
+    tc_wait_ld(y);
+    tc_ld32(x, s_t);
+    row_exp<CUT, BF16>(y, s_t + kProbAt + 16, sc2, b[1] - mm, 32, lim, sum);
+    tc_wait_ld(x);
+    row_exp<CUT, BF16>(x, s_t + kProbAt, sc2, b[0] - mm, 0, lim, sum);
+    float u, v;
+    unpair(sum, u, v);
+    l += u + v;
 }
 
 // ---- softmax of one query tile: thread = row ------------------------------------------------
 template <int D, int DT>
 __device__ __forceinline__ void softmax_role(const AttnCall &c, const AttnTab &t, uint8_t *sm, uint32_t bars, const Ctl &ctl,
-                                             uint32_t tmem, int a, long long part, Walk w)
+                                             int a, long long part, Walk w)
 {
     using S = TileSmem<D>;
     const int lane = threadIdx.x & 31, m_row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(m_row & ~31) << 16;   // the warp's TMEM lanes
-    const uint32_t s_t = tmem + a * 128 + lanes, o_t = tmem + 256 + a * 128 + lanes;
+    const uint32_t s_t = a * 128 + lanes, o_t = 256 + a * 128 + lanes;
     uint8_t *qs = sm + S::Q + a * S::QT;
     uint32_t sn = 0, on = 0;   // phases of sfull, ofull
     int seg = -1;
@@ -630,74 +798,12 @@ __device__ __forceinline__ void softmax_role(const AttnCall &c, const AttnTab &t
             if (DT == KIVI_BF16 && i == w.s.nc && i > w.i0) load_q(false);
             if (!warp_wait(ctl, bars + 8 * (kSFull + a), sn++ & 1)) return;
             tc_after();
-            float b[3] = {0.0f, 0.0f, 0.0f};
             // Columns that the row sees.
             const int lim = coded ? (ng - 3 * i) * 32 : lim_raw - (i - w.s.nc) * kTileTok;
-            const bool cut = __any_sync(0xffffffffu, lim < kTileTok);
-            if (coded) {
-                uint32_t x[8];
-                tc_ld8(x, s_t + kTileTok);
-                tc_wait_ld();
-#pragma unroll
-                for (int g = 0; g < 3; ++g) b[g] = (__uint_as_float(x[g]) + __uint_as_float(x[3 + g])) * sc;
-            }
-            // The row's maximum.
-            float mx = -INFINITY;
-#pragma unroll
-            for (int g = 0; g < 3; ++g) {
-                uint32_t x[32];
-                tc_ld32(x, s_t + 32 * g);
-                tc_wait_ld();
-                float y = -INFINITY;
-                if (cut) {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) y = 32 * g + k < lim ? fmaxf(y, __uint_as_float(x[k])) : y;
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) y = fmaxf(y, __uint_as_float(x[k]));
-                }
-                mx = fmaxf(mx, fmaf(y, sc, b[g]));
-            }
-            const bool grow = mx > m + (kLazy - kRef);
-            if (__any_sync(0xffffffffu, grow)) {
-                const float nm = fmaxf(m, mx + kRef);
-                const float f = m == -INFINITY ? 0.0f : ex2(m - nm);
-                m = nm;
-                l *= f;
-                if (i != w.i0) {
-#pragma unroll 1
-                    for (int k = 0; k < D; k += 32) {
-                        uint32_t x[32];
-                        tc_ld32(x, o_t + k);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int z = 0; z < 32; ++z) x[z] = __float_as_uint(__uint_as_float(x[z]) * f);
-                        tc_st32(o_t + k, x);
-                    }
-                    tc_wait_st();
-                }
-            }
-            const float mm = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-            for (int g = 0; g < 3; ++g) {
-                uint32_t x[32], p[16];
-                tc_ld32(x, s_t + 32 * g);
-                tc_wait_ld();
-                const float off = b[g] - mm;
-                float sum = 0.0f;
-#pragma unroll
-                for (int k = 0; k < 32; k += 2) {
-                    float u = ex2(fmaf(__uint_as_float(x[k]), sc, off)), v = ex2(fmaf(__uint_as_float(x[k + 1]), sc, off));
-                    if (cut) {
-                        u = 32 * g + k < lim ? u : 0.0f;
-                        v = 32 * g + k + 1 < lim ? v : 0.0f;
-                    }
-                    sum += u + v;
-                    p[k / 2] = DT == KIVI_BF16 && !coded ? pack2<KIVI_BF16>(u, v) : pack2<KIVI_F16>(u, v);
-                }
-                l += sum;
-                tc_st16(s_t + 16 * g, p);
-            }
+            const bool cut = __any_sync(0xffffffffu, lim < kTileTok), first = i == w.i0;
+            if (coded && !cut) softmax_step<D, true, false, false>(s_t, o_t, sc, lim, first, m, l);
+            else if (coded) softmax_step<D, true, true, false>(s_t, o_t, sc, lim, first, m, l);
+            else softmax_step<D, false, true, DT == KIVI_BF16>(s_t, o_t, sc, lim, first, m, l);
             tc_wait_st();
             tc_before();
             __syncwarp();
@@ -717,7 +823,7 @@ __device__ __forceinline__ void softmax_role(const AttnCall &c, const AttnTab &t
             uint32_t x[32];
             __syncwarp();
             tc_ld32(x, o_t + k);
-            tc_wait_ld();
+            tc_wait_ld(x);
             if (bad) {
 #pragma unroll
                 for (int z = 0; z < 32; ++z)
@@ -755,9 +861,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     int *stop = (int *)(sm + S::BAR + kBars * 8 + 8);
     if (threadIdx.x == 0) {
         for (int k = 0; k < 2; ++k) {
-            bar_init(bars + 8 * (kKFull + k), 3);
+            bar_init(bars + 8 * (kKFull + k), kDecodeWarps / 2);
             bar_init(bars + 8 * (kKEmpty + k), 1);
-            bar_init(bars + 8 * (kVFull + k), 3);
+            bar_init(bars + 8 * (kVFull + k), kDecodeWarps / 2);
             bar_init(bars + 8 * (kVEmpty + k), 1);
             bar_init(bars + 8 * (kQFull + k), 4);
             bar_init(bars + 8 * (kSFull + k), 1);
@@ -769,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int k = threadIdx.x; k < 2 * kFirstBufs * D; k += kThreads) ((unsigned long long *)(sm + S::FIRST))[k] = ~0ull;
     if (threadIdx.x < 2 * kFirstBufs) ((int *)(sm + S::FLAG))[threadIdx.x] = -1;
-    if (wid == 14) {
+    if (wid == kSoftWarps + kDecodeWarps) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(saddr(tmem_at)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -782,19 +888,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     Walk w;
     w.lo = w.pos = range_at(blockIdx.x, tot, c.warps);
     w.hi = range_at(blockIdx.x + 1, tot, c.warps);
-    if (wid < 8) softmax_role<D, DT>(c, t, sm, bars, ctl, tmem, wid >> 2, blockIdx.x, w);
-    else if (wid < 11) decode_role<D, DT, 0>(c, t, sm, bars, ctl, wid - 8, w);
-    else if (wid < 14) decode_role<D, DT, 1>(c, t, sm, bars, ctl, wid - 11, w);
-    else if (lane == 0) {
-        issue_role<D, DT>(c, t, sm, bars, ctl, tmem, w);
-        if (*ctl.stop) {
-            // Some wait gave up: let the products issued so far finish before
-            // their memory goes away (a barrier of its own, with a limit).
-            const uint32_t b = bars + 8 * kBars + 16;
-            bar_init(b, 1);
-            tc_commit(b);
-            const uint64_t t0 = now_ns();
-            while (!bar_test(b, 0) && now_ns() - t0 < kWaitNs) {
+    if (wid < kSoftWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        softmax_role<D, DT>(c, t, sm, bars, ctl, wid >> 2, blockIdx.x, w);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWorkRegs));
+        const int d = wid - kSoftWarps;
+        if (d < kDecodeWarps / 2) decode_role<D, DT, 0>(c, t, sm, bars, ctl, d >> 1, d & 1, w);
+        else if (d < kDecodeWarps) decode_role<D, DT, 1>(c, t, sm, bars, ctl, (d - kDecodeWarps / 2) >> 1, d & 1, w);
+        else if (d == kDecodeWarps) {
+            // (All 512 columns are this CTA's: they start at 0.)
+            if (tmem == 0) issue_role<D, DT>(c, t, sm, bars, ctl, w);
+            else *stop = 1;
+            __syncwarp();
+            if (*ctl.stop && lane == 0) {
+                // Some wait gave up: let the products issued so far finish
+                // before their memory goes away (a barrier of its own, with a
+                // limit).
+                const uint32_t b = bars + 8 * kBars + 16;
+                bar_init(b, 1);
+                tc_commit(b);
+                const uint64_t t0 = now_ns();
+                while (!bar_test(b, 0) && now_ns() - t0 < kWaitNs) {
+                }
             }
         }
     }
@@ -803,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_after();
     __syncwarp();
-    if (wid == 14) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    if (wid == kSoftWarps + kDecodeWarps) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
 // Adds the partial results of the segment that starts in range blockIdx.x and
