@@ -44,13 +44,15 @@ constexpr int kSoftWarps = 8, kDecodeWarps = 12;
 constexpr int kThreads = 24 * 32;        // three warps idle: registers move by warpgroups
 // Registers: 80 a thread at launch (61,440), then 256 x 128 + 512 x 56.
 constexpr int kSoftRegs = 128, kWorkRegs = 56;
-constexpr int kProbAt = 48;               // P's first TMEM column within S's
+// TMEM columns of P's g-th 32 tokens within S's: over scores that are no
+// longer needed when they are written (the third, second, first 32 in turn).
+__host__ __device__ constexpr int prob_at(int g) { return 48 + 16 * g; }
 constexpr int kRing = 3;                 // coded tiles in flight per decoding warp
 constexpr int kSlot = 1024;              // bytes of a ring slot: 16 tokens' codes and their scales and zeros
 constexpr int kFirstBufs = 4;
 constexpr float kLazy = 3.0f;            // the running maximum follows when exceeded by 2^kLazy
 constexpr float kRef = -8.0f;            // p is kept times 2^8: fp16 keeps 2^-32 of the largest
-constexpr uint64_t kWaitNs = 2000000000; // a wait gives up after two seconds
+constexpr int kMaxPolls = 1 << 23;       // a wait gives up after that many polls (each some 100 cycles)
 
 template <int D>
 struct TileSmem {
@@ -97,36 +99,21 @@ struct Ctl {
     int *err;             // the pool's status word
 };
 
-__device__ __forceinline__ uint64_t now_ns()
-{
-    uint64_t t;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-    return t;
-}
-
 // Waits for the barrier's phase; false when this wait, or another of the CTA,
-// gave up (then the caller leaves).
-__device__ __forceinline__ bool bar_wait_long(const Ctl &ctl, uint32_t b, uint32_t phase)
-{
-    const uint64_t t0 = now_ns();
-#pragma unroll 1
-    for (;;) {
-#pragma unroll 1
-        for (int i = 0; i < 32; ++i)
-            if (bar_test(b, phase)) return true;
-        if (*ctl.stop) return false;
-        if (now_ns() - t0 > kWaitNs) break;
-    }
-    *ctl.stop = 1;
-    atomicCAS(ctl.err, 0, KIVI_DEVICE_WAIT_TIMEOUT);
-    return false;
-}
+// gave up (then the caller leaves).  Small on purpose: it is inlined at every
+// wait, and the roles' code has to share the instruction cache.
 __device__ __forceinline__ bool bar_wait(const Ctl &ctl, uint32_t b, uint32_t phase)
 {
+    int polls = 0;
 #pragma unroll 1
-    for (int i = 0; i < 8; ++i)
-        if (bar_test(b, phase)) return true;
-    return bar_wait_long(ctl, b, phase);
+    while (!bar_test(b, phase)) {
+        if (++polls > kMaxPolls || *ctl.stop) {
+            *ctl.stop = 1;
+            atomicCAS(ctl.err, 0, KIVI_DEVICE_WAIT_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
 }
 // The same for a whole warp: its lanes leave together.
 __device__ __forceinline__ bool warp_wait(const Ctl &ctl, uint32_t b, uint32_t phase)
@@ -359,6 +346,11 @@ __device__ __forceinline__ unsigned long long bad_token(int seg, int tok)
     return ((unsigned long long)(0x7fffffff - seg) << 32) | (uint32_t)(tok + 0x40000000);
 }
 
+// Row of token o (0..7) of a coded octet: with the lanes of two neighbouring
+// tokens four rows apart, the eight lanes of a store phase fall into
+// different banks (one row apart the swizzle gives both the same four).
+__device__ __forceinline__ constexpr int octet_row(int o) { return (o & 1) * 4 + (o >> 1); }
+
 // ---- decoding warps: 16 tokens (half hf of group sub) of keys (VAL = 0) or values --------
 template <int D, int DT, int VAL>
 __device__ __forceinline__ void decode_role(const AttnCall &c, const AttnTab &t, uint8_t *sm, uint32_t bars, const Ctl &ctl,
@@ -421,22 +413,21 @@ __device__ __forceinline__ void decode_role(const AttnCall &c, const AttnTab &t,
                         *(uint4 *)(tile + (VAL ? value_at<D>(row, ch) : key_at<D>(row, ch))) = make_uint4(0, 0, 0, 0);
                     }
                 } else if constexpr (VAL == 0) {
-                    // Words of tokens tq + 8(2hf + jj).
-                    uint32_t kw[4];
-                    *(uint4 *)kw = *(const uint4 *)(slot + lane * 16);
+                    // Words of tokens tq + 8(2hf + jj), 64 channels each.
+                    const uint32_t *kw = (const uint32_t *)(slot + lane * 16) + (D == 128 ? 0 : 2 * hf);
+#pragma unroll 1
+                    for (int k = 0; k < 2 * L::KW; ++k) {
+                        const int jj = k / L::KW, wd = k % L::KW;
+                        const uint32_t x = kw[k], x10 = x >> 10;
 #pragma unroll
-                    for (int u = 0; u < D / 32; ++u) {
-                        uint32_t s[4];
-                        *(uint4 *)s = *(const uint4 *)(slot + 512 + u * 64 + cs * 16);
-#pragma unroll
-                        for (int jj = 0; jj < 2; ++jj) {
-                            const uint32_t x = D == 128 ? kw[jj * 2 + u / 2] : hf ? kw[2 + jj] : kw[jj];
-                            const uint32_t x10 = x >> 10;
-                            uint32_t o[4];
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t s[4], o[4];
+                            *(uint4 *)s = *(const uint4 *)(slot + 512 + (2 * wd + h) * 64 + cs * 16);
 #pragma unroll
                             for (int p = 0; p < 4; ++p)
-                                o[p] = as_u(__hmul2(code_less(x, x10, 4 * (u % 2) + p, 1, one), as_h2(s[p])));
-                            *(uint4 *)(tile + key_at<D>(row0 + tq + 8 * jj, 4 * u + cs)) = *(const uint4 *)o;
+                                o[p] = as_u(__hmul2(code_less(x, x10, 4 * h + p, 1, one), as_h2(s[p])));
+                            *(uint4 *)(tile + key_at<D>(row0 + octet_row(tq) + 8 * jj, 8 * wd + 4 * h + cs)) =
+                                *(const uint4 *)o;
                         }
                     }
                     // Row 96 + sub holds the group's z, row 99 + sub its s.
@@ -444,31 +435,29 @@ __device__ __forceinline__ void decode_role(const AttnCall &c, const AttnTab &t,
                         *(uint4 *)(tile + key_at<D>(kTileTok + (hf ? 3 : 0) + sub, lane)) =
                             *(const uint4 *)(slot + 512 + (hf ? 0 : 2 * D) + lane * 16);
                 } else {
-                    // Words of token pairs 8(2hf + pp) + 2cs.
-                    uint32_t vw[4];
-                    *(uint4 *)vw = *(const uint4 *)(slot + lane * 16);
+                    // Words of token pairs 8(2hf + pp) + 2cs, 64 channels each.
+                    const uint32_t *vw = (const uint32_t *)(slot + lane * 16) + (D == 128 ? 0 : 2 * hf);
                     const uint32_t tile_s = saddr(tile);
+#pragma unroll 1
+                    for (int k = 0; k < 2 * L::KW; ++k) {
+                        const int pp = k / L::KW, jh = k % L::KW;
+                        const uint4 sz = *(const uint4 *)(slot + 512 + page_vm_offset<D>(pp, cs, 2 * jh));
+                        const uint32_t x = vw[k], x10 = x >> 10;
+                        const uint32_t a = tile_s + value_at<D>(row0 + 8 * pp + octet_row(lane & 7), 8 * jh + (lane >> 3));
 #pragma unroll
-                    for (int pp = 0; pp < 2; ++pp)
+                        for (int jj = 0; jj < 2; ++jj) {
+                            uint32_t o[4];
 #pragma unroll
-                        for (int jh = 0; jh < L::KW; ++jh) {
-                            const uint4 sz = *(const uint4 *)(slot + 512 + page_vm_offset<D>(pp, cs, 2 * jh));
-                            const uint32_t x = D == 128 ? vw[pp * 2 + jh] : hf ? vw[2 + pp] : vw[pp];
-                            const uint32_t x10 = x >> 10;
-#pragma unroll
-                            for (int jj = 0; jj < 2; ++jj) {
-                                uint32_t o[4];
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    o[k] = as_u(__hfma2(code_less(x, x10, 4 * jj + k, 0, one), as_h2(jj ? sz.z : sz.x),
-                                                        as_h2(jj ? sz.w : sz.y)));
-                                const uint32_t a =
-                                    tile_s + value_at<D>(row0 + 8 * pp + (lane & 7), 8 * jh + 4 * jj + (lane >> 3));
-                                asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(a),
-                                             "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
-                                             : "memory");
-                            }
+                            for (int z = 0; z < 4; ++z)
+                                o[z] = as_u(__hfma2(code_less(x, x10, 4 * jj + z, 0, one), as_h2(jj ? sz.z : sz.x),
+                                                    as_h2(jj ? sz.w : sz.y)));
+                            // (chunks 4 apart: the swizzle's bit 2)
+                            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(
+                                             a ^ (jj * 64)),
+                                         "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                                         : "memory");
                         }
+                    }
                 }
             } else {
                 // 16 uncoded tokens: residual, then new ones.
@@ -553,18 +542,29 @@ __device__ __forceinline__ void issue_role(const AttnCall &c, const AttnTab &t, 
     auto qk = [&](int a, int st, bool coded) {
         // bf16 operands only for uncoded tokens of a bf16 pool.
         const uint32_t inst = instruction(DT == KIVI_BF16 && !coded, kKeyRows, false);
-        const uint64_t q0 = operand(base + S::Q + a * S::QT, 16), k0 = operand(base + S::K + st * S::KT, 16);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-            mma_ss(a * 128, q0 + ((k / 4) * (128 * 128) + (k % 4) * 32) / 16,
-                   k0 + ((k / 4) * (kKeyRows * 128) + (k % 4) * 32) / 16, inst, k != 0);
+        uint64_t q = operand(base + S::Q + a * S::QT, 16), k = operand(base + S::K + st * S::KT, 16);
+        bool add = false;
+#pragma unroll 1
+        for (int kb = 0; kb < S::KB; ++kb) {
+#pragma unroll 1
+            for (int x = 0; x < 4; ++x) {
+                mma_ss(a * 128, q + 2 * x, k + 2 * x, inst, add);
+                add = true;
+            }
+            q += 128 * 128 / 16;
+            k += kKeyRows * 128 / 16;
+        }
     };
     auto pv = [&](int a, int st, bool coded, bool add) {
         const uint32_t inst = instruction(DT == KIVI_BF16 && !coded, D, true);
-        const uint64_t v0 = operand(base + S::V + st * S::VT, kTileTok * 128);
-#pragma unroll
-        for (int k = 0; k < kTileTok / 16; ++k)
-            mma_ts(256 + a * 128, a * 128 + kProbAt + k * 8, v0 + k * 2048 / 16, inst, add || k != 0);
+        uint64_t v = operand(base + S::V + st * S::VT, kTileTok * 128);
+#pragma unroll 1
+        for (int g = 0; g < 3; ++g) {
+            mma_ts(256 + a * 128, a * 128 + prob_at(g), v, inst, add);
+            mma_ts(256 + a * 128, a * 128 + prob_at(g) + 8, v + 2048 / 16, inst, true);
+            v += 2 * 2048 / 16;
+            add = true;
+        }
     };
     while (w.next(c, t)) {
         for (int a = 0; a < w.nq; ++a)
@@ -584,9 +584,8 @@ __device__ __forceinline__ void issue_role(const AttnCall &c, const AttnTab &t, 
             if (!warp_wait(ctl, bars + 8 * (kVFull + (it & 1)), (it >> 1) & 1)) return;
             const bool more = i + 1 < w.i1;
             const bool reload = DT == KIVI_BF16 && more && i + 1 == w.s.nc;
-#pragma unroll
-            for (int a = 0; a < 2; ++a) {
-                if (a >= w.nq) break;
+#pragma unroll 1
+            for (int a = 0; a < w.nq; ++a) {
                 if (!warp_wait(ctl, bars + 8 * (kPFull + a), pn[a]++ & 1)) return;
                 tc_after();
                 if (elected()) {
@@ -722,12 +721,12 @@ __device__ __forceinline__ void softmax_step(uint32_t s_t, uint32_t o_t, float s
     const float mm = m == -INFINITY ? 0.0f : m;
     const uint64_t sc2 = pair(sc, sc);
     uint64_t sum = 0;
-    row_exp<CUT, BF16>(x, s_t + kProbAt + 32, sc2, b[2] - mm, 64, lim, sum);
+    row_exp<CUT, BF16>(x, s_t + prob_at(2), sc2, b[2] - mm, 64, lim, sum);
     tc_wait_ld(y);
     tc_ld32(x, s_t);
-    row_exp<CUT, BF16>(y, s_t + kProbAt + 16, sc2, b[1] - mm, 32, lim, sum);
+    row_exp<CUT, BF16>(y, s_t + prob_at(1), sc2, b[1] - mm, 32, lim, sum);
     tc_wait_ld(x);
-    row_exp<CUT, BF16>(x, s_t + kProbAt, sc2, b[0] - mm, 0, lim, sum);
+    row_exp<CUT, BF16>(x, s_t + prob_at(0), sc2, b[0] - mm, 0, lim, sum);
     float u, v;
     unpair(sum, u, v);
     l += u + v;
@@ -908,8 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t b = bars + 8 * kBars + 16;
                 bar_init(b, 1);
                 tc_commit(b);
-                const uint64_t t0 = now_ns();
-                while (!bar_test(b, 0) && now_ns() - t0 < kWaitNs) {
+                for (int k = 0; k < kMaxPolls && !bar_test(b, 0); ++k) {
                 }
             }
         }
