@@ -23,6 +23,8 @@
 // 16 + 2i) and are stored [word/4][lane][word%4].
 #pragma once
 
+#include <utility>
+
 #include "kivi_common.cuh"
 #include "kivi_internal.h"
 
@@ -103,6 +105,35 @@ struct AttnTab {
     int seq[kPoolMaxBatch], row0[kPoolMaxBatch], n[kPoolMaxBatch], nk[kPoolMaxBatch], ng[kPoolMaxBatch],
         r[kPoolMaxBatch];
     long long off[kPoolMaxBatch + 1];
+    // The split: part w of `parts` is positions [at(w), at(w + 1)), at(w) =
+    // floor(w * total / parts) with total = quo * parts + rem.
+    long long quo;
+    int rem, parts;
+    __device__ __forceinline__ long long at(int w) const
+    {
+        return w * quo + (unsigned)w * (unsigned)rem / (unsigned)parts;   // w, rem <= parts < 2^16
+    }
+    // The part that holds position pos.
+    __device__ __forceinline__ int part_of(long long pos) const
+    {
+        int w = (int)min((long long)parts - 1, quo > 0 ? quotient(pos, quo) : (long long)parts);
+        while (at(w) > pos) --w;
+        while (at(w + 1) <= pos) ++w;
+        return w;
+    }
+    // a / b for a >= 0, b > 0: short where 32 bits hold both.
+    __device__ static __forceinline__ long long quotient(long long a, long long b)
+    {
+        if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+        return a / b;
+    }
+    __host__ void split(long long most)
+    {
+        const long long total = off[nb];
+        parts = (int)(most < total ? most : total);
+        quo = parts > 0 ? total / parts : 0;
+        rem = parts > 0 ? (int)(total % parts) : 0;
+    }
 };
 
 struct AttnCall {
@@ -112,9 +143,30 @@ struct AttnCall {
     int H_q, group;       // group = H_q / H
     float scale;          // log2(e) / sqrt(D)
     float *part;          // partial results (attention scratch of the pool)
+    int4 *joins;          // per part: the segment that starts there and ends behind it (kivi_pool_rows.cu)
     int *err;             // status word
-    long long warps;      // warps of the split
 };
+
+// Launch as a programmatic dependent of the launch before it on the stream: the
+// kernel may start while that one finishes and waits for it (griddep_wait)
+// before it touches memory.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int block, int smem, cudaStream_t st, Args &&...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 cudaError_t launch_pool_quant(const PoolView &v, const Rows &k, const Rows &nv, const ExtendTab &t, cudaStream_t st);
 cudaError_t launch_pool_keep(const PoolView &v, const Rows &k, const Rows &nv, const ExtendTab &t, cudaStream_t st);
@@ -126,6 +178,7 @@ cudaError_t launch_pool_fork(const PoolView &v, const ForkTab &t, cudaStream_t s
 // Attention of few rows (matrix fragments) and of many (tcgen05 tiles), and
 // the floats of scratch each needs on a device of `sms` SMs.
 size_t pool_rows_scratch(int D, int sms);
+constexpr int kJoinsPerSm = 16;   // entries of AttnCall::joins per SM
 cudaError_t launch_pool_rows(AttnCall &c, AttnTab &t, int sms, cudaStream_t st);
 size_t pool_tiles_scratch(int D, int sms);
 cudaError_t launch_pool_tiles(AttnCall &c, AttnTab &t, int sms, cudaStream_t st);

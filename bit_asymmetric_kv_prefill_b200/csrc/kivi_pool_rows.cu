@@ -123,7 +123,8 @@ __host__ __device__ constexpr int code_place(int i) { return i < 5 ? i : i - 5; 
 __device__ __forceinline__ __half2 code_less_one(uint32_t w, uint32_t w10, int i, const uint32_t (&one)[5])
 {
     const int k = code_place(i);
-    const uint32_t x = ((i < 5 ? w : w10) & (0x00030003u << (2 * k))) | one[k];
+    uint32_t x;   // (w & mask) | one[k] in one instruction
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(x) : "r"(i < 5 ? w : w10), "r"(0x00030003u << (2 * k)), "r"(one[k]));
     return __hadd2(as_h2(x), __half2half2(__float2half_rn(-(float)((1 << (10 - 2 * k)) + 1))));
 }
 // c 4^k 2^-24 of pair i (fp16 subnormals).
@@ -150,17 +151,11 @@ __device__ __forceinline__ Seg find_segment(const AttnTab &t, const AttnCall &c,
     s.e = lo;
     const int raw = (t.r[lo] + 31) / 32 + (t.nk[lo] + 31) / 32;
     s.C = max(1, t.ng[lo] + raw * kRawWeight);
-    const int si = (int)((pos - t.off[lo]) / s.C);
+    const int si = (int)AttnTab::quotient(pos - t.off[lo], s.C);
     s.base = t.off[lo] + si * s.C;
     s.rt = si / c.v.H;
     s.h = si - s.rt * c.v.H;
     return s;
-}
-
-// w * tot < 2^63, see launch_pool_rows.
-__device__ __forceinline__ long long range_at(long long w, long long tot, long long warps)
-{
-    return (long long)((unsigned long long)(w * tot) / (unsigned long long)warps);
 }
 
 template <int D>
@@ -666,15 +661,15 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
 // Rows of tile a from output fragment f: transposed to (row 8a + tq, channels
 // 16f + 8y + 2cs, + 1).
 template <int DT>
-__device__ __forceinline__ void store_rows(const AttnCall &c, const AttnTab &t, const Seg &sg, int row, int d,
+__device__ __forceinline__ void store_rows(const AttnCall &c, const AttnTab &t, int e, int h, int row, int d,
                                            const float (&o)[4], float f0, float f1)
 {
     const int cs = threadIdx.x & 3;
     const uint32_t x = transpose8(pack2<DT>(o[0] * f0, o[1] * f1)), y = transpose8(pack2<DT>(o[2] * f0, o[3] * f1));
     const int tok = row / c.group;
-    if (tok >= t.n[sg.e]) return;
-    uint16_t *p = c.out
-                  + ((long long)(t.row0[sg.e] + tok) * c.H_q + sg.h * c.group + row - tok * c.group) * c.v.D + d + 2 * cs;
+    if (tok >= t.n[e]) return;
+    uint16_t *p =
+        c.out + ((long long)(t.row0[e] + tok) * c.H_q + h * c.group + row - tok * c.group) * c.v.D + d + 2 * cs;
     *(uint32_t *)p = x;
     *(uint32_t *)(p + 8) = y;
 }
@@ -686,11 +681,12 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas(NT))
     extern __shared__ __align__(128) uint8_t smem[];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, tq = lane >> 2, cs = lane & 3;
     uint8_t *sm = smem + wid * RowsSmem<D>::PER_WARP;
-    const long long w = (long long)blockIdx.x * kRowWarps + wid;
-    if (w >= c.warps) return;
-    const long long tot = t.off[t.nb];
-    const long long lo = range_at(w, tot, c.warps), hi = range_at(w + 1, tot, c.warps);
+    const int w = blockIdx.x * kRowWarps + wid;
+    if (w >= t.parts) return;
+    const long long lo = t.at(w), hi = t.at(w + 1);
     long long pos = lo;
+    int4 join = make_int4(-1, 0, 0, 0);
+    bool waited = false;
 #pragma unroll 1
     while (pos < hi) {
         const Seg sg = find_segment(t, c, pos);
@@ -703,6 +699,11 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas(NT))
         };
         const long long rb = min(sg.C, hi - sg.base);
         const int i0 = min(items, first_item(pos - sg.base)), i1 = rb == sg.C ? items : first_item(rb);
+        if (!waited) {
+            griddep_wait();   // nothing before this reads or writes memory
+            griddep_launch();
+            waited = true;
+        }
         State<D, NT> st;
         run_items<D, DT, NT>(c, t, sg, i0, max(i0, i1), sm, st);
         if (sg.base >= lo && rb == sg.C) {
@@ -712,10 +713,11 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas(NT))
                 const float f1 = st.l[a][1] == 0.0f ? 0.0f : 1.0f / st.l[a][1];
 #pragma unroll
                 for (int f = 0; f < D / 16; ++f)
-                    store_rows<DT>(c, t, sg, 8 * NT * sg.rt + 8 * a + tq, 16 * f, st.o[a][f], f0, f1);
+                    store_rows<DT>(c, t, e, sg.h, 8 * NT * sg.rt + 8 * a + tq, 16 * f, st.o[a][f], f0, f1);
             }
         } else {
-            float *part = c.part + (2 * w + (sg.base >= lo ? 1 : 0)) * kPartFloats<D, NT>;
+            if (sg.base >= lo) join = make_int4(t.part_of(sg.base + sg.C - 1), e, sg.rt, sg.h);
+            float *part = c.part + (long long)(2 * w + (sg.base >= lo ? 1 : 0)) * kPartFloats<D, NT>;
 #pragma unroll
             for (int a = 0; a < NT; ++a) {
                 if ((8 * NT * sg.rt + 8 * a) / c.group >= t.n[e]) break;
@@ -732,33 +734,22 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas(NT))
         }
         pos = sg.base + rb;
     }
+    if (lane == 0) c.joins[w] = join;
 }
 
-// Adds the partial results of the segment that starts in warp blockIdx.x's
-// range and ends behind it (if there is one), in the order of its warps; warp
-// (a, f) of the block takes output fragment f of tile a.
-template <int D, int DT, int NT>
-__global__ void __launch_bounds__(NT *D / 16 * 32) pool_join_kernel(const __grid_constant__ AttnCall c,
-                                                                    const __grid_constant__ AttnTab t)
-{
-    const long long w = blockIdx.x, tot = t.off[t.nb];
-    const long long lo = range_at(w, tot, c.warps), hi = range_at(w + 1, tot, c.warps);
-    if (hi >= tot || lo >= hi) return;
-    const Seg sg = find_segment(t, c, hi - 1);
-    if (sg.base < lo || sg.base + sg.C <= hi) return;
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, tq = lane >> 2, cs = lane & 3;
-    const int a = wid / (D / 16), f = wid % (D / 16);
-    const int row = 8 * NT * sg.rt + 8 * a;
-    if (row / c.group >= t.n[sg.e]) return;
-    // The warp that holds the segment's last position.
-    const long long last = ((sg.base + sg.C) * c.warps - 1) / tot;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (long long x = w; x <= last; ++x) {
-        const float *pa = c.part + (2 * x + (x == w ? 1 : 0)) * kPartFloats<D, NT> + a * (8 * D + 16);
-        const float4 ml = *(const float4 *)(pa + 8 * D + 4 * cs);   // of rows 2cs and 2cs + 1
-        float q[4];
+// A running sum of partial results: rows 2cs, 2cs + 1 (see State).
+template <int F>
+struct Joined {
+    float o[F][4], m[2], l[2];
+    __device__ __forceinline__ void clear()
+    {
 #pragma unroll
-        for (int y = 0; y < 4; ++y) q[y] = pa[(4 * f + y) * 32 + lane];
+        for (int f = 0; f < F; ++f) o[f][0] = o[f][1] = o[f][2] = o[f][3] = 0.0f;
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.0f;
+    }
+    __device__ __forceinline__ void add(const float (&q)[F][4], float4 ml)
+    {
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
             const float pm = y ? ml.z : ml.x, pl = y ? ml.w : ml.y;
@@ -766,13 +757,80 @@ __global__ void __launch_bounds__(NT *D / 16 * 32) pool_join_kernel(const __grid
             const float mn = fmaxf(m[y], pm);
             const float fo = m[y] == -INFINITY ? 0.0f : ex2(m[y] - mn), fn = ex2(pm - mn);
             l[y] = l[y] * fo + pl * fn;
-            o[y] = o[y] * fo + q[y] * fn;
-            o[2 + y] = o[2 + y] * fo + q[2 + y] * fn;
+#pragma unroll
+            for (int f = 0; f < F; ++f) {
+                o[f][y] = o[f][y] * fo + q[f][y] * fn;
+                o[f][2 + y] = o[f][2 + y] * fo + q[f][2 + y] * fn;
+            }
             m[y] = mn;
         }
     }
-    const float f0 = l[0] == 0.0f ? 0.0f : 1.0f / l[0], f1 = l[1] == 0.0f ? 0.0f : 1.0f / l[1];
-    store_rows<DT>(c, t, sg, row + tq, 16 * f, o, f0, f1);
+};
+
+constexpr int kJoinWarps = 8;   // warps per block, parts per block
+
+// Adds the partial results of the segments that start in the block's parts and
+// end behind them.  The warps take every kJoinWarps-th of a segment's partial
+// results and then their sums, fragment by fragment: a fixed order.
+template <int D, int DT, int NT>
+__global__ void __launch_bounds__(kJoinWarps * 32) pool_join_kernel(const __grid_constant__ AttnCall c,
+                                                                    const __grid_constant__ AttnTab t)
+{
+    constexpr int NF = D / 16;
+    __shared__ float sums[kJoinWarps][NF * 128 + 16];
+    __shared__ int4 list[kJoinWarps];
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, tq = lane >> 2, cs = lane & 3;
+    const int w0 = blockIdx.x * kJoinWarps;
+    griddep_wait();
+    griddep_launch();
+    if (threadIdx.x < kJoinWarps)
+        list[threadIdx.x] = w0 + (int)threadIdx.x < t.parts ? c.joins[w0 + threadIdx.x] : make_int4(-1, 0, 0, 0);
+    __syncthreads();
+#pragma unroll 1
+    for (int k = 0; k < kJoinWarps; ++k) {
+        const int4 j = list[k];
+        const int w = w0 + k, last = j.x, e = j.y;
+        if (last < 0) continue;
+#pragma unroll 1
+        for (int a = 0; a < NT; ++a) {
+            const int row = 8 * NT * j.z + 8 * a;
+            if (row / c.group >= t.n[e]) break;
+            Joined<NF> s;
+            s.clear();
+#pragma unroll 1
+            for (int x = w + wid; x <= last; x += kJoinWarps) {
+                const float *pa = c.part + (long long)(2 * x + (x == w ? 1 : 0)) * kPartFloats<D, NT> + a * (8 * D + 16);
+                const float4 ml = *(const float4 *)(pa + 8 * D + 4 * cs);
+                float q[NF][4];
+#pragma unroll
+                for (int f = 0; f < NF; ++f)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) q[f][y] = pa[(4 * f + y) * 32 + lane];
+                s.add(q, ml);
+            }
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) sums[wid][(4 * f + y) * 32 + lane] = s.o[f][y];
+            if (tq == 0) *(float4 *)(&sums[wid][NF * 128 + 4 * cs]) = make_float4(s.m[0], s.l[0], s.m[1], s.l[1]);
+            __syncthreads();
+#pragma unroll 1
+            for (int f = wid; f < NF; f += kJoinWarps) {
+                Joined<1> r;
+                r.clear();
+#pragma unroll
+                for (int x = 0; x < kJoinWarps; ++x) {
+                    float q[1][4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) q[0][y] = sums[x][(4 * f + y) * 32 + lane];
+                    r.add(q, *(const float4 *)(&sums[x][NF * 128 + 4 * cs]));
+                }
+                const float f0 = r.l[0] == 0.0f ? 0.0f : 1.0f / r.l[0], f1 = r.l[1] == 0.0f ? 0.0f : 1.0f / r.l[1];
+                store_rows<DT>(c, t, e, j.w, row + tq, 16 * f, r.o[0], f0, f1);
+            }
+            __syncthreads();
+        }
+    }
 }
 
 template <int D, int DT, int NT>
@@ -781,12 +839,11 @@ cudaError_t rows_t(AttnCall &c, AttnTab &t, cudaStream_t st)
     static PerDeviceOnce once;
     cudaError_t e = set_smem_once(once, pool_rows_kernel<D, DT, NT>, RowsSmem<D>::BYTES);
     if (e != cudaSuccess) return e;
-    pool_rows_kernel<D, DT, NT>
-        <<<(unsigned)((c.warps + kRowWarps - 1) / kRowWarps), kRowWarps * 32, RowsSmem<D>::BYTES, st>>>(c, t);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || c.warps == 1) return e;
-    pool_join_kernel<D, DT, NT><<<(unsigned)c.warps, NT * D / 16 * 32, 0, st>>>(c, t);
-    return cudaGetLastError();
+    e = launch_dependent(pool_rows_kernel<D, DT, NT>, dim3((t.parts + kRowWarps - 1) / kRowWarps), kRowWarps * 32,
+                         RowsSmem<D>::BYTES, st, c, t);
+    if (e != cudaSuccess || t.parts == 1) return e;
+    return launch_dependent(pool_join_kernel<D, DT, NT>, dim3((t.parts + kJoinWarps - 1) / kJoinWarps), kJoinWarps * 32, 0, st,
+                            c, t);
 }
 
 template <int D, int DT>
@@ -811,7 +868,7 @@ size_t pool_rows_scratch(int D, int sms)
     return most;
 }
 
-// Fills the split (t.off, c.warps) and launches.
+// Fills the split (t.off and its parts) and launches.
 cudaError_t launch_pool_rows(AttnCall &c, AttnTab &t, int sms, cudaStream_t st)
 {
     // As many tiles per warp as the most rows of an entry need: the decoded
@@ -827,11 +884,8 @@ cudaError_t launch_pool_rows(AttnCall &c, AttnTab &t, int sms, cudaStream_t st)
         const long long tiles = ((long long)t.n[e] * c.group + 8 * nt - 1) / (8 * nt);
         t.off[e + 1] = t.off[e] + tiles * c.v.H * (C > 0 ? C : 1);
     }
-    const long long tot = t.off[t.nb];
-    if (tot == 0) return cudaSuccess;
-    c.warps = split_warps(sms, nt);
-    if (c.warps > tot) c.warps = tot;
-    if (tot > (1LL << 62) / (c.warps + 1)) return cudaErrorInvalidValue;
+    if (t.off[t.nb] == 0) return cudaSuccess;
+    t.split(split_warps(sms, nt));
     if (c.v.D == 64) return c.v.dtype ? rows_n<64, 1>(c, t, nt, st) : rows_n<64, 0>(c, t, nt, st);
     return c.v.dtype ? rows_n<128, 1>(c, t, nt, st) : rows_n<128, 0>(c, t, nt, st);
 }

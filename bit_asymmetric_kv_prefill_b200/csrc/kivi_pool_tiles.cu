@@ -282,8 +282,8 @@ __device__ __forceinline__ TSeg find_segment(const AttnTab &t, const AttnCall &c
     }
     TSeg s;
     s.e = lo;
-    const long long per_head = (t.off[lo + 1] - t.off[lo]) / c.v.H;
-    s.h = (int)((pos - t.off[lo]) / per_head);
+    const long long per_head = AttnTab::quotient(t.off[lo + 1] - t.off[lo], c.v.H);
+    s.h = (int)AttnTab::quotient(pos - t.off[lo], per_head);
     s.base = t.off[lo] + s.h * per_head;
     s.nc = coded_tiles(t.ng[lo]);
     for (s.rt = 0;; ++s.rt) {
@@ -291,11 +291,6 @@ __device__ __forceinline__ TSeg find_segment(const AttnTab &t, const AttnCall &c
         if (pos < s.base + s.nc + s.nr) return s;
         s.base += s.nc + s.nr;
     }
-}
-
-__device__ __forceinline__ long long range_at(long long w, long long tot, long long parts)
-{
-    return (long long)((unsigned long long)(w * tot) / (unsigned long long)parts);
 }
 
 template <int D>
@@ -883,10 +878,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_after();
     const uint32_t tmem = *tmem_at;
     const Ctl ctl{stop, c.err};
-    const long long tot = t.off[t.nb];
     Walk w;
-    w.lo = w.pos = range_at(blockIdx.x, tot, c.warps);
-    w.hi = range_at(blockIdx.x + 1, tot, c.warps);
+    w.lo = w.pos = t.at(blockIdx.x);
+    w.hi = t.at(blockIdx.x + 1);
     if (wid < kSoftWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         softmax_role<D, DT>(c, t, sm, bars, ctl, wid >> 2, blockIdx.x, w);
@@ -926,14 +920,14 @@ template <int D, int DT>
 __global__ void __launch_bounds__(256) pool_tiles_join_kernel(const __grid_constant__ AttnCall c,
                                                               const __grid_constant__ AttnTab t)
 {
-    const long long w = blockIdx.x, tot = t.off[t.nb];
-    const long long lo = range_at(w, tot, c.warps), hi = range_at(w + 1, tot, c.warps);
-    if (hi >= tot || lo >= hi) return;
+    const int w = blockIdx.x;
+    const long long lo = t.at(w), hi = t.at(w + 1);
+    if (hi >= t.off[t.nb] || lo >= hi) return;
     const TSeg s = find_segment(t, c, hi - 1);
     const long long end = s.base + s.nc + s.nr;
     if (s.base < lo || end <= hi) return;
     const int lane = threadIdx.x & 31;
-    const long long last = (end * c.warps - 1) / tot;
+    const int last = t.part_of(end - 1);
     constexpr int E = D / 32;
     for (int k = threadIdx.x >> 5; k < kTileRows / 8; k += 8) {
         const int lr = blockIdx.y * (kTileRows / 8) + k;
@@ -943,8 +937,8 @@ __global__ void __launch_bounds__(256) pool_tiles_join_kernel(const __grid_const
         float m = -INFINITY, l = 0.0f, o[E];
 #pragma unroll
         for (int z = 0; z < E; ++z) o[z] = 0.0f;
-        for (long long x = w; x <= last; ++x) {
-            const float *po = c.part + x * 2 * kTilePart<D> + (x == w ? kTilePart<D> : 0);
+        for (int x = w; x <= last; ++x) {
+            const float *po = c.part + (long long)x * 2 * kTilePart<D> + (x == w ? kTilePart<D> : 0);
             const float2 ml = *(const float2 *)(po + (long long)kTileRows * D + 2 * lr);
             float y[E];
 #pragma unroll
@@ -971,10 +965,10 @@ cudaError_t tiles_t(AttnCall &c, AttnTab &t, cudaStream_t st)
     static PerDeviceOnce once;
     cudaError_t e = set_smem_once(once, pool_tiles_kernel<D, DT>, TileSmem<D>::BYTES);
     if (e != cudaSuccess) return e;
-    pool_tiles_kernel<D, DT><<<(unsigned)c.warps, kThreads, TileSmem<D>::BYTES, st>>>(c, t);
+    pool_tiles_kernel<D, DT><<<(unsigned)t.parts, kThreads, TileSmem<D>::BYTES, st>>>(c, t);
     e = cudaGetLastError();
-    if (e != cudaSuccess || c.warps == 1) return e;
-    pool_tiles_join_kernel<D, DT><<<dim3((unsigned)c.warps, 8), 256, 0, st>>>(c, t);
+    if (e != cudaSuccess || t.parts == 1) return e;
+    pool_tiles_join_kernel<D, DT><<<dim3((unsigned)t.parts, 8), 256, 0, st>>>(c, t);
     return cudaGetLastError();
 }
 
@@ -993,10 +987,8 @@ cudaError_t launch_pool_tiles(AttnCall &c, AttnTab &t, int sms, cudaStream_t st)
             per_head += coded_tiles(t.ng[e]) + (raw_seen(t.r[e], t.nk[e], t.n[e], c.group, rt) + kTileTok - 1) / kTileTok;
         t.off[e + 1] = t.off[e] + per_head * c.v.H;
     }
-    const long long tot = t.off[t.nb];
-    if (tot == 0) return cudaSuccess;
-    c.warps = sms < tot ? sms : tot;
-    if (tot > (1LL << 62) / (c.warps + 1)) return cudaErrorInvalidValue;
+    if (t.off[t.nb] == 0) return cudaSuccess;
+    t.split(sms);
     if (c.v.D == 64) return c.v.dtype ? tiles_t<64, 1>(c, t, st) : tiles_t<64, 0>(c, t, st);
     return c.v.dtype ? tiles_t<128, 1>(c, t, st) : tiles_t<128, 0>(c, t, st);
 }
