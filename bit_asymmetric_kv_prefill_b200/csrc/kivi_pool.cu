@@ -657,8 +657,11 @@ void unpack_page_group(const uint8_t *b, int t0, uint8_t *codesK, uint8_t *codes
             }
         }
     }
-    if (sK) std::memcpy(sK + (long long)t0 / kG * D, b + L::KS, 2 * D);
-    if (zK) std::memcpy(zK + (long long)t0 / kG * D, b + L::KZ, 2 * D);
+    for (int d = 0; d < D; ++d) {
+        const uint8_t *x = b + L::KM + d / 2 * 8 + d % 2 * 2;
+        if (zK) std::memcpy(zK + (long long)t0 / kG * D + d, x, 2);
+        if (sK) std::memcpy(sK + (long long)t0 / kG * D + d, x + 4, 2);
+    }
     for (int p = 0; p < 4; ++p)
         for (int cs = 0; cs < 4; ++cs)
             for (int j = 0; j < L::NJ; ++j) {

@@ -10,7 +10,8 @@
 //               channels {32u + 8cs + 0..7}: word j*(D/64) + w covers
 //               u = 2w, 2w + 1; pair i = 4(u - 2w) + p is channels
 //               32u + 8cs + 2p and the next one.
-//   [8D,  10D)  K scales, channel order.      [10D, 12D)  K zeros.
+//   [8D,  12D)  K zeros and scales: per channel pair its two zeros, then its two
+//               scales (8 bytes).
 //   [12D, 20D)  V codes.  Lane 4*n + cs holds channels 8c + n (c < D/8) of the
 //               token pairs 8p + 2cs, 8p + 2cs + 1 (p < 4): word
 //               p*(D/64) + c/8, pair i = c % 8 (the pair's halves are the two
@@ -33,7 +34,7 @@ namespace kivi {
 template <int D>
 struct PageLayout {
     static constexpr int GB = 24 * D;
-    static constexpr int KC = 0, KS = 8 * D, KZ = 10 * D, VC = 12 * D, VM = 20 * D;
+    static constexpr int KC = 0, KM = 8 * D, VC = 12 * D, VM = 20 * D;
     static constexpr int WPL = D / 16;   // code words per lane (K or V)
     static constexpr int KW = D / 64;    // K words per token, V words per token pair
     static constexpr int NJ = D / kG;    // value groups per token

@@ -45,14 +45,14 @@ namespace kivi {
 namespace {
 
 constexpr int kRowWarps = 4;        // warps per CTA
-constexpr int kRowStages = 4;       // group blocks in flight per warp
+constexpr int kRowStages = 6;       // group blocks in a warp's ring
 constexpr int kRawWeight = 2;       // cost of 32 uncoded tokens, in groups
 constexpr float kLazy = 3.0f;       // the running maximum follows when exceeded by 2^kLazy
 constexpr int kMaxTiles = 3;        // 8-row tiles per warp
 // CTAs per SM of a kernel with NT tiles (168 or 255 registers a thread).  One
 // tile would fit 128 registers and 4 CTAs: 80 us against 73 with 3 (24 x 8K
 // tokens, 8 kv heads of 4 query heads).
-constexpr int row_ctas(int nt) { return nt <= 2 ? 3 : 2; }
+constexpr int row_ctas(int nt) { return nt == 1 ? 3 : 2; }
 
 // ---- fragments ------------------------------------------------------------------
 template <int DT>
@@ -187,11 +187,11 @@ struct State {
     float m[NT][2], l[NT][2];
 };
 
-// Moves the reference of row x of tile a to m (-inf: nothing seen yet).
+// Moves the reference of row x of tile a to m.
 template <int D, int NT>
 __device__ __forceinline__ void rescale(State<D, NT> &st, float (*oz)[4], int a, int x, float m)
 {
-    const float f = st.m[a][x] == -INFINITY ? 0.0f : ex2(st.m[a][x] - m);
+    const float f = st.m[a][x] == -INFINITY ? 0.0f : ex2(st.m[a][x] - m);   // (-inf: nothing seen yet)
     st.m[a][x] = m;
     st.l[a][x] *= f;
 #pragma unroll
@@ -218,8 +218,8 @@ __device__ __forceinline__ void softmax_step(State<D, NT> &st, float (*oz)[4], f
     for (int a = 0; a < NT; ++a)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            mx[a][x] = fmaxf(fmaxf(S[a][0][x], S[a][0][2 + x]), fmaxf(S[a][1][x], S[a][1][2 + x])) * sc[a][x];
-            grow = grow || mx[a][x] > st.m[a][x] + (kLazy - e);
+            mx[a][x] = fmaxf(fmaxf(S[a][0][x], S[a][0][2 + x]), fmaxf(S[a][1][x], S[a][1][2 + x])) * sc[a][x] + e;
+            grow = grow || mx[a][x] > st.m[a][x] + kLazy;
         }
     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -229,8 +229,7 @@ __device__ __forceinline__ void softmax_step(State<D, NT> &st, float (*oz)[4], f
                 float v = mx[a][x];
 #pragma unroll
                 for (int b = 4; b < 32; b *= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, b));
-                v += e;
-                if (v > st.m[a][x]) rescale<D, NT>(st, oz, a, x, v);
+                rescale<D, NT>(st, oz, a, x, fmaxf(st.m[a][x], v));
             }
     }
 #pragma unroll
@@ -352,17 +351,8 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
                 ++in_page;
                 ++fetch;
             }
-            cp_async_commit();
         };
-        for (int k = 0; k < kRowStages - 1; ++k) issue(k);
-        int stage = 0;
-#pragma unroll 1
-        for (int g = i0; g < g1; ++g) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(kRowStages - 2) : "memory");
-            __syncwarp();
-            issue((stage + kRowStages - 1) % kRowStages);   // into the stage that the last iteration has read
-            const uint8_t *blk = sm + stage * L::GB;
-            stage = (stage + 1) % kRowStages;
+        auto step = [&](const uint8_t *blk) {
             float S[NT][2][4];
             {
                 // Rows 0..7 of A hold z, rows 8..15 s: elements 0, 1 and 2, 3
@@ -377,13 +367,16 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
                 uint32_t s[KU][4];
 #pragma unroll
                 for (int u = 0; u < KU; ++u) {
-                    uint32_t z[4];
-                    *(uint4 *)s[u] = *(const uint4 *)(blk + L::KS + u * 64 + cs * 16);
-                    *(uint4 *)z = *(const uint4 *)(blk + L::KZ + u * 64 + cs * 16);
+                    const uint4 z0 = *(const uint4 *)(blk + L::KM + (16 * u + 4 * cs) * 8);
+                    const uint4 z1 = *(const uint4 *)(blk + L::KM + (16 * u + 4 * cs) * 8 + 16);
+                    s[u][0] = z0.y;
+                    s[u][1] = z0.w;
+                    s[u][2] = z1.y;
+                    s[u][3] = z1.w;
 #pragma unroll
                     for (int a = 0; a < NT; ++a) {
-                        mma<KIVI_F16>(b[a], z[0], s[u][0], z[1], s[u][1], qf[a][u][0], qf[a][u][1]);
-                        mma<KIVI_F16>(b[a], z[2], s[u][2], z[3], s[u][3], qf[a][u][2], qf[a][u][3]);
+                        mma<KIVI_F16>(b[a], z0.x, z0.y, z0.z, z0.w, qf[a][u][0], qf[a][u][1]);
+                        mma<KIVI_F16>(b[a], z1.x, z1.y, z1.z, z1.w, qf[a][u][2], qf[a][u][3]);
                     }
                 }
 #pragma unroll
@@ -412,10 +405,7 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
                         }
                     }
             }
-            uint32_t vw[L::WPL], vs[4][NJ];
-#pragma unroll
-            for (int q = 0; q < L::WPL / 4; ++q)
-                *(uint4 *)(vw + 4 * q) = *(const uint4 *)(blk + L::VC + (q * 32 + lane) * 16);
+            uint32_t vs[4][NJ];
             uint32_t big = 0;
 #pragma unroll
             for (int p = 0; p < 4; ++p)
@@ -438,61 +428,82 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
 #pragma unroll
                     for (int a = 0; a < NT; ++a)
 #pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            if (st.m[a][x] != -INFINITY) rescale<D, NT>(st, oz, a, x, st.m[a][x] + (float)up);
+                        for (int x = 0; x < 2; ++x) rescale<D, NT>(st, oz, a, x, st.m[a][x] + (float)up);
                 }
             }
             softmax_step<D, NT>(st, oz, S, sc, (float)E);
-            // P transposed: rows 8a + tq, token pairs 8p + 2cs.
-            uint32_t pt[NT][4];
-#pragma unroll
-            for (int a = 0; a < NT; ++a)
-#pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                    pt[a][2 * f] = transpose8(pack2<KIVI_F16>(S[a][f][0], S[a][f][1]));
-                    pt[a][2 * f + 1] = transpose8(pack2<KIVI_F16>(S[a][f][2], S[a][f][3]));
-                }
             {
-                // Row tq of A: the zeros of channel group tq.
-                uint32_t z[4];
-#pragma unroll
-                for (int p = 0; p < 4; ++p)
-                    z[p] = tq < NJ ? *(const uint32_t *)(blk + L::VM + page_vm_offset<D>(p, cs, tq < NJ ? tq : 0) + 4) : 0u;
-#pragma unroll
-                for (int a = 0; a < NT; ++a) {
-                    mma<KIVI_F16>(oz[a], z[0], 0u, z[1], 0u, pt[a][0], pt[a][1]);
-                    mma<KIVI_F16>(oz[a], z[2], 0u, z[3], 0u, pt[a][2], pt[a][3]);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                uint32_t ps[NT][4];
+                // P transposed: rows 8a + tq, token pairs 8p + 2cs.
+                uint32_t pt[NT][4];
 #pragma unroll
                 for (int a = 0; a < NT; ++a)
 #pragma unroll
-                    for (int p = 0; p < 4; ++p) ps[a][p] = as_u(__hmul2(as_h2(pt[a][p]), as_h2(vs[p][j])));
-                uint32_t w[4], x10[4];
+                    for (int f = 0; f < 2; ++f) {
+                        pt[a][2 * f] = transpose8(pack2<KIVI_F16>(S[a][f][0], S[a][f][1]));
+                        pt[a][2 * f + 1] = transpose8(pack2<KIVI_F16>(S[a][f][2], S[a][f][3]));
+                    }
+                {
+                    // Row tq of A: the zeros of channel group tq (rows past
+                    // them hold some group's again and are not used).
+                    uint32_t z[4];
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    w[p] = vw[p * KW + j / 2];
-                    x10[p] = w[p] >> 10;
+                    for (int p = 0; p < 4; ++p)
+                        z[p] = *(const uint32_t *)(blk + L::VM + page_vm_offset<D>(p, cs, tq % NJ) + 4);
+#pragma unroll
+                    for (int a = 0; a < NT; ++a) {
+                        mma<KIVI_F16>(oz[a], z[0], z[0], z[1], z[1], pt[a][0], pt[a][1]);
+                        mma<KIVI_F16>(oz[a], z[2], z[2], z[3], z[3], pt[a][2], pt[a][3]);
+                    }
                 }
+                uint32_t vw[L::WPL];
 #pragma unroll
-                for (int ff = 0; ff < 2; ++ff) {
-                    // Channel tiles 4j + 2ff, + 1: pairs i, i + 1 of their words.
-                    const int i = 4 * (j % 2) + 2 * ff;
+                for (int q = 0; q < L::WPL / 4; ++q)
+                    *(uint4 *)(vw + 4 * q) = *(const uint4 *)(blk + L::VC + (q * 32 + lane) * 16);
 #pragma unroll
-                    for (int mm = 0; mm < 2; ++mm) {
-                        const uint32_t a0 = code_tiny(w[2 * mm], x10[2 * mm], i);
-                        const uint32_t a1 = code_tiny(w[2 * mm], x10[2 * mm], i + 1);
-                        const uint32_t a2 = code_tiny(w[2 * mm + 1], x10[2 * mm + 1], i);
-                        const uint32_t a3 = code_tiny(w[2 * mm + 1], x10[2 * mm + 1], i + 1);
+                for (int j = 0; j < NJ; ++j) {
+                    uint32_t ps[NT][4];
 #pragma unroll
-                        for (int a = 0; a < NT; ++a)
-                            mma<KIVI_F16>(st.o[a][2 * j + ff], a0, a1, a2, a3, ps[a][2 * mm], ps[a][2 * mm + 1]);
+                    for (int a = 0; a < NT; ++a)
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) ps[a][p] = as_u(__hmul2(as_h2(pt[a][p]), as_h2(vs[p][j])));
+                    uint32_t w[4], x10[4];
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        w[p] = vw[p * KW + j / 2];
+                        x10[p] = w[p] >> 10;
+                    }
+#pragma unroll
+                    for (int ff = 0; ff < 2; ++ff) {
+                        // Channel tiles 4j + 2ff, + 1: pairs i, i + 1 of their words.
+                        const int i = 4 * (j % 2) + 2 * ff;
+#pragma unroll
+                        for (int mm = 0; mm < 2; ++mm) {
+                            const uint32_t a0 = code_tiny(w[2 * mm], x10[2 * mm], i);
+                            const uint32_t a1 = code_tiny(w[2 * mm], x10[2 * mm], i + 1);
+                            const uint32_t a2 = code_tiny(w[2 * mm + 1], x10[2 * mm + 1], i);
+                            const uint32_t a3 = code_tiny(w[2 * mm + 1], x10[2 * mm + 1], i + 1);
+#pragma unroll
+                            for (int a = 0; a < NT; ++a)
+                                mma<KIVI_F16>(st.o[a][2 * j + ff], a0, a1, a2, a3, ps[a][2 * mm], ps[a][2 * mm + 1]);
+                        }
                     }
                 }
             }
+        };
+#pragma unroll
+        for (int k = 0; k < kRowStages - 1; ++k) {
+            issue(k);
+            cp_async_commit();
+        }
+        int stage = 0;
+#pragma unroll 1
+        for (int g = i0; g < g1; ++g) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kRowStages - 2) : "memory");
+            __syncwarp();
+            issue(stage == 0 ? kRowStages - 1 : stage - 1);   // into the stage that the last step has read
+            cp_async_commit();
+            step(sm + stage * L::GB);
+            stage = stage + 1 == kRowStages ? 0 : stage + 1;
         }
         cp_async_wait_all();
         __syncwarp();

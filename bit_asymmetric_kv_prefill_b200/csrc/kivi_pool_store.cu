@@ -105,8 +105,7 @@ __device__ __forceinline__ void page_key_tile(const uint8_t *tile, uint8_t *blk,
         T1[pp] = (uint32_t)(t1s >> (32 * pp));
         T2[pp] = (uint32_t)(t2s >> (32 * pp));
         T3[pp] = (uint32_t)(t3s >> (32 * pp));
-        *(uint32_t *)(blk + L::KS + (c0 + 2 * pp) * 2) = (uint32_t)(ss >> (32 * pp));
-        *(uint32_t *)(blk + L::KZ + (c0 + 2 * pp) * 2) = (uint32_t)(zs >> (32 * pp));
+        *(uint2 *)(blk + L::KM + (c0 / 2 + pp) * 8) = make_uint2((uint32_t)(zs >> (32 * pp)), (uint32_t)(ss >> (32 * pp)));
     }
     // The lane's channels: u = c0/32, cs = (c0%32)/8, pairs from i0 of word w.
     const int u = c0 / 32, cs = (c0 % 32) / 8, w = u / 2;
@@ -377,14 +376,14 @@ __global__ void __launch_bounds__(kStoreWarps * 32)
     }
 #pragma unroll
     for (int u = 0; u < D / 32; ++u) {
-        uint32_t s[4], z[4];
-        *(uint4 *)s = *(const uint4 *)(blk + L::KS + u * 64 + cs * 16);
-        *(uint4 *)z = *(const uint4 *)(blk + L::KZ + u * 64 + cs * 16);
+        uint2 zs[4];
+        *(uint4 *)zs = *(const uint4 *)(blk + L::KM + (16 * u + 4 * cs) * 8);
+        *(uint4 *)(zs + 2) = *(const uint4 *)(blk + L::KM + (16 * u + 4 * cs) * 8 + 16);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             uint32_t o[4];
 #pragma unroll
-            for (int p = 0; p < 4; ++p) o[p] = decode_pair<DT>(kw[j * L::KW + u / 2], 4 * (u % 2) + p, s[p], z[p]);
+            for (int p = 0; p < 4; ++p) o[p] = decode_pair<DT>(kw[j * L::KW + u / 2], 4 * (u % 2) + p, zs[p].y, zs[p].x);
             *(uint4 *)(ko + (tq + 8 * j) * ts + 32 * u + 8 * cs) = *(const uint4 *)o;
         }
     }

@@ -382,7 +382,7 @@ __device__ __forceinline__ void decode_role(const AttnCall &c, const AttnTab &t,
                              : "memory");
                 if (lane < kMeta / 16)
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 512),
-                                 "l"(blk + (VAL ? L::VM + hf * 2 * D : L::KS) + lane * 16)
+                                 "l"(blk + (VAL ? L::VM + hf * 2 * D : L::KM) + lane * 16)
                                  : "memory");
             }
             slot_in = slot_in + 1 == kRing ? 0 : slot_in + 1;
@@ -416,19 +416,27 @@ __device__ __forceinline__ void decode_role(const AttnCall &c, const AttnTab &t,
                         const uint32_t x = kw[k], x10 = x >> 10;
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            uint32_t s[4], o[4];
-                            *(uint4 *)s = *(const uint4 *)(slot + 512 + (2 * wd + h) * 64 + cs * 16);
+                            uint2 s[4];   // zeros and scales of the four channel pairs
+                            uint32_t o[4];
+                            const uint8_t *zs = slot + 512 + (16 * (2 * wd + h) + 4 * cs) * 8;
+                            *(uint4 *)s = *(const uint4 *)zs;
+                            *(uint4 *)(s + 2) = *(const uint4 *)(zs + 16);
 #pragma unroll
                             for (int p = 0; p < 4; ++p)
-                                o[p] = as_u(__hmul2(code_less(x, x10, 4 * h + p, 1, one), as_h2(s[p])));
+                                o[p] = as_u(__hmul2(code_less(x, x10, 4 * h + p, 1, one), as_h2(s[p].y)));
                             *(uint4 *)(tile + key_at<D>(row0 + octet_row(tq) + 8 * jj, 8 * wd + 4 * h + cs)) =
                                 *(const uint4 *)o;
                         }
                     }
                     // Row 96 + sub holds the group's z, row 99 + sub its s.
-                    if (lane < D / 8)
+                    if (lane < D / 8) {
+                        uint2 zs[4];
+                        *(uint4 *)zs = *(const uint4 *)(slot + 512 + lane * 32);
+                        *(uint4 *)(zs + 2) = *(const uint4 *)(slot + 512 + lane * 32 + 16);
                         *(uint4 *)(tile + key_at<D>(kTileTok + (hf ? 3 : 0) + sub, lane)) =
-                            *(const uint4 *)(slot + 512 + (hf ? 0 : 2 * D) + lane * 16);
+                            hf ? make_uint4(zs[0].y, zs[1].y, zs[2].y, zs[3].y)
+                               : make_uint4(zs[0].x, zs[1].x, zs[2].x, zs[3].x);
+                    }
                 } else {
                     // Words of token pairs 8(2hf + pp) + 2cs, 64 channels each.
                     const uint32_t *vw = (const uint32_t *)(slot + lane * 16) + (D == 128 ? 0 : 2 * hf);
