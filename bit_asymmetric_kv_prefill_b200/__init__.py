@@ -141,13 +141,14 @@ def lib():
     L.kivi_pool_copy.argtypes = [vp, pi, i32, pi, vp]
     L.kivi_pool_compact.argtypes = [vp, pi, vp]
     L.kivi_pool_length.argtypes = [vp, i32, P(i64), pi]
+    L.kivi_pool_tokens.argtypes = [vp, pi, i32, P(i64)]
     L.kivi_pool_pages.argtypes = [vp, i32, pi, i32, pi]
     L.kivi_pool_usage.argtypes = [vp, pi, pi, pi]
     L.kivi_pool_device_status.argtypes = [vp, pi]
     L.kivi_pool_export.argtypes = [vp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]
     for name in ("kivi_pool_required_bytes", "kivi_pool_create", "kivi_pool_destroy", "kivi_pool_open",
                  "kivi_pool_free", "kivi_pool_extend", "kivi_pool_attn", "kivi_pool_gather", "kivi_pool_fork",
-                 "kivi_pool_copy", "kivi_pool_compact", "kivi_pool_length", "kivi_pool_pages", "kivi_pool_usage",
+                 "kivi_pool_copy", "kivi_pool_compact", "kivi_pool_length", "kivi_pool_tokens", "kivi_pool_pages", "kivi_pool_usage",
                  "kivi_pool_device_status", "kivi_pool_export"):
         getattr(L, name).restype = st
     for name in ("kivi_rope", "kivi_rope_frequencies", "kivi_cache_create", "kivi_cache_create_ex", "kivi_cache_required_bytes",
@@ -198,14 +199,15 @@ def _dtype_code(dtype) -> int:
 
 
 class _on_device:
-    """The given device current for the calls inside (a call belongs to its
-    tensors' device, whichever device the caller has current)."""
+    """The device of this index current for the calls inside (a call belongs to
+    its tensors' device, whichever device the caller has current)."""
+    __slots__ = ("index", "before")
 
-    def __init__(self, device):
-        self.index = device.index
+    def __init__(self, index):
+        self.index = index
 
     def __enter__(self):
-        self.before = torch.cuda.current_device()
+        self.before = torch._C._cuda_getDevice()
         if self.before != self.index:
             torch.cuda.set_device(self.index)
 
@@ -215,8 +217,8 @@ class _on_device:
 
 
 def _stream_ptr(stream) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    # The current stream's handle without a Stream object around it (3 us).
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 class KiviCache:

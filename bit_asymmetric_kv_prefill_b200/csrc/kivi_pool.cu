@@ -156,7 +156,7 @@ std::vector<int> free_slots(const kivi_pool *p, int n)
 cudaError_t launch_pairs(const kivi_pool *p, const std::vector<int> &a, const std::vector<int> &b, bool moves,
                          cudaStream_t st)
 {
-    auto t = std::make_unique<PairTab>();
+    const std::unique_ptr<PairTab> t(new PairTab);
     for (size_t i = 0; i < a.size(); i += kPoolMaxPairs) {
         t->n = (int)std::min(a.size() - i, (size_t)kPoolMaxPairs);
         std::copy_n(a.begin() + i, t->n, t->a);
@@ -290,6 +290,16 @@ kivi_status kivi_pool_length(const kivi_pool *p, int seq, long long *n_q, int *r
     return KIVI_OK;
 }
 
+kivi_status kivi_pool_tokens(const kivi_pool *p, const int *seqs, int n, long long *tokens)
+{
+    if (!p || n < 0 || (n > 0 && (!seqs || !tokens))) return KIVI_ERR_ARG;
+    for (int i = 0; i < n; ++i)
+        if (!is_open(p, seqs[i])) return KIVI_ERR_ARG;
+    for (int i = 0; i < n; ++i)
+        tokens[i] = (long long)p->seqs[seqs[i]].pages.size() * p->cfg.R + p->seqs[seqs[i]].r;
+    return KIVI_OK;
+}
+
 kivi_status kivi_pool_pages(const kivi_pool *p, int seq, int *pages, int capacity, int *n)
 {
     if (!p || !n || capacity < 0 || !is_open(p, seq)) return KIVI_ERR_ARG;
@@ -332,7 +342,7 @@ kivi_status kivi_pool_extend(kivi_pool *p, const int *seqs, const int *n_new, in
     if (total > (1LL << 30)) return KIVI_ERR_UNSUPPORTED;
     return guarded([&]() -> kivi_status {
         const int R = p->cfg.R, H = p->cfg.H_kv;
-        auto t = std::make_unique<ExtendTab>();
+        const std::unique_ptr<ExtendTab> t(new ExtendTab);
         t->nb = n;
         t->item[0] = t->kept[0] = 0;
         std::vector<int> fresh, at, ids;   // new pages, their table entries
@@ -366,7 +376,7 @@ kivi_status kivi_pool_extend(kivi_pool *p, const int *seqs, const int *n_new, in
             s.pages.reserve(s.pages.size() + (t->item[i + 1] - t->item[i]) / (R / kG * H));
         }
         fresh.reserve(need);
-        auto tab = std::make_unique<PairTab>();
+        const std::unique_ptr<PairTab> tab(new PairTab);
         for (long long j = 0; j < need; ++j) {
             fresh.push_back(p->free_pages.top());
             p->free_pages.pop();
@@ -421,7 +431,7 @@ kivi_status kivi_pool_attn(kivi_pool *p, const int *seqs, const int *n_new, int 
     if (!good_rows(q) || (k && (!good_rows(k) || !good_rows(v))) || !out || !aligned16(out)) return KIVI_ERR_ARG;
     return guarded([&]() -> kivi_status {
         // Sequences of few rows and of many go to kernels of their own.
-        auto few = std::make_unique<AttnTab>(), many = std::make_unique<AttnTab>();
+        const std::unique_ptr<AttnTab> few(new AttnTab), many(new AttnTab);
         few->nb = many->nb = 0;
         const int group = H_q / p->cfg.H_kv;
         int row = 0;
@@ -466,7 +476,7 @@ kivi_status kivi_pool_gather(kivi_pool *p, const int *seqs, int n, void *K, void
     const kivi_status st = check_seqs(p, seqs, n, true);
     if (st != KIVI_OK) return st;
     return guarded([&]() -> kivi_status {
-        auto t = std::make_unique<GatherTab>();
+        const std::unique_ptr<GatherTab> t(new GatherTab);
         t->nb = n;
         t->item[0] = 0;
         long long row = 0, items = 0;
@@ -499,7 +509,7 @@ static kivi_status branch(kivi_pool *p, const int *src, int n, int *dst, bool ow
     return guarded([&]() -> kivi_status {
         const std::vector<int> slots = free_slots(p, n);
         if ((int)slots.size() != n) return KIVI_ERR_CAPACITY;
-        auto t = std::make_unique<ForkTab>();
+        const std::unique_ptr<ForkTab> t(new ForkTab);
         t->n = n;
         size_t need = 0;
         for (int i = 0; i < n; ++i) {
@@ -516,7 +526,7 @@ static kivi_status branch(kivi_pool *p, const int *src, int n, int *dst, bool ow
         from.reserve(need);
         to.reserve(need);
         at.reserve(need);
-        auto tab = std::make_unique<PairTab>();
+        const std::unique_ptr<PairTab> tab(new PairTab);
         if (own)
             for (int i = 0; i < n; ++i) {
                 const PoolSeq &s = p->seqs[src[i]];

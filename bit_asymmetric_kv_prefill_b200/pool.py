@@ -45,7 +45,7 @@ class KiviPool:
         return n.value
 
     def _rows(self, t: torch.Tensor, rows: int, heads: int, name: str):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != self.device:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != self.device.index:
             raise ValueError(f"{name} must be a CUDA tensor on {self.device}")
         if t.dtype != self.dtype:
             raise ValueError(f"{name} must be {self.dtype}, got {t.dtype}")
@@ -79,14 +79,14 @@ class KiviPool:
     def _branch(self, call, what, seqs, stream):
         n = len(seqs)
         a = (ctypes.c_int * max(n, 1))()
-        with _on_device(self.device):
+        with _on_device(self.device.index):
             _check(call(self._h, _ints(seqs, "seqs"), n, a, _stream_ptr(stream)), what)
         return a[:n]
 
     def compact(self, stream=None) -> int:
         """Move pages to the front of the pool; returns how many moved."""
         n = ctypes.c_int()
-        with _on_device(self.device):
+        with _on_device(self.device.index):
             _check(lib().kivi_pool_compact(self._h, ctypes.byref(n), _stream_ptr(stream)), "kivi_pool_compact")
         return n.value
 
@@ -101,7 +101,7 @@ class KiviPool:
             raise ValueError(f"lengths must hold {n} values")
         N = sum(lengths)
         k, v = self._rows(K, N, self.H_kv, "K"), self._rows(V, N, self.H_kv, "V")
-        with _on_device(self.device):
+        with _on_device(self.device.index):
             _check(lib().kivi_pool_extend(self._h, _ints(seqs, "seqs"), _ints(lengths, "lengths"), n, ctypes.byref(k),
                                           ctypes.byref(v), _stream_ptr(stream)), "kivi_pool_extend")
 
@@ -128,11 +128,11 @@ class KiviPool:
             kr = ctypes.byref(self._rows(K, N, self.H_kv, "K"))
             vr = ctypes.byref(self._rows(V, N, self.H_kv, "V"))
         if out is None:
-            out = torch.empty((N, H_q, self.D), dtype=self.dtype, device=self.device)
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
         elif (out.dtype != self.dtype or out.shape != (N, H_q, self.D) or not out.is_contiguous()
               or out.device != self.device):
             raise ValueError(f"out must be a contiguous {self.dtype} {(N, H_q, self.D)} tensor on {self.device}")
-        with _on_device(self.device):
+        with _on_device(self.device.index):
             _check(lib().kivi_pool_attn(self._h, _ints(seqs, "seqs"), _ints(lengths, "lengths"), n, ctypes.byref(qr),
                                         kr, vr, H_q, out.data_ptr(), _stream_ptr(stream)), "kivi_pool_attn")
         return out
@@ -140,16 +140,21 @@ class KiviPool:
     def gather(self, seqs, K: torch.Tensor | None = None, V: torch.Tensor | None = None, stream=None):
         """The cached tokens of ``seqs``, one sequence after another, decoded:
         (K, V) [tokens, H_kv, D] in the pool's dtype."""
-        N = sum(sum(self.length(s)) for s in seqs)
-        shape = (N, self.H_kv, self.D)
-        K, V = (torch.empty(shape, dtype=self.dtype, device=self.device) if t is None else t for t in (K, V))
+        ids, n = _ints(seqs, "seqs"), len(seqs)
+        tokens = (ctypes.c_longlong * max(n, 1))()
+        _check(lib().kivi_pool_tokens(self._h, ids, n, tokens), "kivi_pool_tokens")
+        N = sum(tokens)
+        if K is None:
+            K = torch.empty((N, self.H_kv, self.D), dtype=self.dtype, device=self.device)
+        if V is None:
+            V = torch.empty_like(K, memory_format=torch.contiguous_format)
         for name, t in (("K", K), ("V", V)):
             self._rows(t, N, self.H_kv, name)
             if not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
-        with _on_device(self.device):
-            _check(lib().kivi_pool_gather(self._h, _ints(seqs, "seqs"), len(seqs), K.data_ptr(), V.data_ptr(),
-                                          _stream_ptr(stream)), "kivi_pool_gather")
+        with _on_device(self.device.index):
+            _check(lib().kivi_pool_gather(self._h, ids, n, K.data_ptr(), V.data_ptr(), _stream_ptr(stream)),
+                   "kivi_pool_gather")
         return K, V
 
     # -- inspection ---------------------------------------------------------------
@@ -175,7 +180,7 @@ class KiviPool:
 
     def device_status(self) -> int:
         code = ctypes.c_int()
-        with _on_device(self.device):
+        with _on_device(self.device.index):
             _check(lib().kivi_pool_device_status(self._h, ctypes.byref(code)), "kivi_pool_device_status")
         return code.value
 
@@ -189,7 +194,7 @@ class KiviPool:
                  sV=np.zeros((n_q, D // G), np.uint16), zV=np.zeros((n_q, D // G), np.uint16),
                  resK=np.zeros((r, D), np.uint16), resV=np.zeros((r, D), np.uint16))
         ptr = {k: v.ctypes.data_as(ctypes.c_void_p) for k, v in a.items()}
-        with _on_device(self.device):
+        with _on_device(self.device.index):
             _check(lib().kivi_pool_export(self._h, seq, head, ptr["codesK"], ptr["codesV"], ptr["sK"], ptr["zK"],
                                           ptr["sV"], ptr["zV"], ptr["resK"], ptr["resV"]), "kivi_pool_export")
         return a

@@ -32,14 +32,15 @@ def rope_frequencies(rotary_dim: int, theta: float = 10000.0, scaling: str = PLA
     return t.to(device), m.value
 
 
-def _side(x, y, D, name):
-    if not isinstance(x, torch.Tensor) or not x.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if x.dim() != 3 or x.shape[2] != D or x.stride(2) != 1:
-        raise ValueError(f"{name} must have shape [tokens, heads, {D}] with contiguous channels")
-    if y.shape != x.shape or y.dtype != x.dtype or y.device != x.device or y.stride(2) != 1:
-        raise ValueError(f"the output of {name} must match its shape, type and device, channels contiguous")
-    return RopeTensor(x.data_ptr(), y.data_ptr(), x.shape[1], x.stride(0), x.stride(1), y.stride(0), y.stride(1))
+def _side(x, y, shape, dtype, device, name):
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.get_device() != device:
+        raise ValueError(f"{name} must be a CUDA tensor, on q's device")
+    if x.dtype != dtype or x.shape != shape or y.shape != shape or y.dtype != dtype or y.get_device() != device:
+        raise ValueError(f"{name} and its output must have shape {tuple(shape)} and type {dtype}")
+    (xt, xh, xd), (yt, yh, yd) = x.stride(), y.stride()
+    if xd != 1 or yd != 1:
+        raise ValueError(f"{name} and its output must have contiguous channels")
+    return (x.data_ptr(), y.data_ptr(), shape[1], xt, xh, yt, yh)
 
 
 def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_freq: torch.Tensor,
@@ -55,27 +56,28 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_f
     Returns (q_out, k_out)."""
     if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
         raise ValueError("q must be a CUDA tensor [tokens, heads, D]")
-    N, _, D = q.shape
+    shape, dtype, device = q.shape, q.dtype, q.get_device()
+    N, _, D = shape
     rot = D if rotary_dim is None else rotary_dim
-    if positions.dtype not in (torch.int32, torch.int64) or positions.device != q.device \
-            or tuple(positions.shape) != (N,) or not positions.is_contiguous():
+    pos64 = positions.dtype == torch.int64
+    if not (pos64 or positions.dtype == torch.int32) or positions.get_device() != device \
+            or positions.shape != (N,) or not positions.is_contiguous():
         raise ValueError(f"positions must be contiguous int32 or int64 [{N}] on {q.device}")
-    if inv_freq.dtype != torch.float32 or inv_freq.device != q.device or not inv_freq.is_contiguous() \
-            or inv_freq.numel() != rot // 2:
+    if inv_freq.dtype != torch.float32 or inv_freq.get_device() != device or inv_freq.numel() != rot // 2 \
+            or not inv_freq.is_contiguous():
         raise ValueError(f"inv_freq must be contiguous float32 [{rot // 2}] on {q.device}")
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if k is None:
-        t = (RopeTensor * 1)(_side(q, q_out, D, "q"))
+        t, n = (RopeTensor * 1)(_side(q, q_out, shape, dtype, device, "q")), 1
     else:
-        if not isinstance(k, torch.Tensor) or k.dtype != q.dtype or k.device != q.device or k.dim() != 3 \
-                or k.shape[0] != N:
-            raise ValueError("k must match q's tokens, type and device")
+        if not isinstance(k, torch.Tensor) or k.dim() != 3:
+            raise ValueError("k must be a CUDA tensor [tokens, kv heads, D]")
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        t = (RopeTensor * 2)(_side(q, q_out, D, "q"), _side(k, k_out, D, "k"))
-    with _on_device(q.device):
-        _check(lib().kivi_rope(t, len(t), _dtype_code(q.dtype), N, D, positions.data_ptr(),
-                               int(positions.dtype == torch.int64), inv_freq.data_ptr(), rot, int(interleaved),
-                               scale, int(inverse), int(fp32_angles), _stream_ptr(stream)), "kivi_rope")
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        t, n = (RopeTensor * 2)(_side(q, q_out, shape, dtype, device, "q"),
+                                _side(k, k_out, (N, k.shape[1], D), dtype, device, "k")), 2
+    with _on_device(device):
+        _check(lib().kivi_rope(t, n, _dtype_code(dtype), N, D, positions.data_ptr(), pos64, inv_freq.data_ptr(), rot,
+                               interleaved, scale, inverse, fp32_angles, _stream_ptr(stream)), "kivi_rope")
     return q_out, k_out

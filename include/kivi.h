@@ -492,6 +492,8 @@ KIVI_API kivi_status kivi_pool_compact(kivi_pool *p, int *moved, void *stream);
 
 /* Tokens in pages and in the residual. */
 KIVI_API kivi_status kivi_pool_length(const kivi_pool *p, int seq, long long *n_q, int *r);
+/* Tokens of each of n sequences. */
+KIVI_API kivi_status kivi_pool_tokens(const kivi_pool *p, const int *seqs, int n, long long *tokens);
 /* The pages of a sequence (pages may be NULL: only *n). */
 KIVI_API kivi_status kivi_pool_pages(const kivi_pool *p, int seq, int *pages, int capacity, int *n);
 /* Pages in use, one past the last used page, open sequences. */
