@@ -31,7 +31,7 @@ bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 struct PoolPlan {
     int max_pages;
-    size_t off_packed, off_resK, off_resV, off_table, off_part, off_joins, off_err, total;
+    size_t off_packed, off_resK, off_resV, off_table, off_part, off_joins, off_tickets, off_err, total;
 };
 
 struct PoolSeq {
@@ -73,6 +73,8 @@ void make_pool_plan(const kivi_pool_config *c, int sms, PoolPlan *p)
     off = align_up(off + std::max(pool_rows_scratch(c->D, sms), pool_tiles_scratch(c->D, sms)) * sizeof(float));
     p->off_joins = off;
     off = align_up(off + (size_t)sms * kJoinsPerSm * sizeof(int4));
+    p->off_tickets = off;
+    off = align_up(off + (size_t)sms * kJoinsPerSm * sizeof(int));
     p->off_err = off;
     off = align_up(off + sizeof(int));
     p->total = off;
@@ -232,6 +234,8 @@ kivi_status kivi_pool_create(const kivi_pool_config *cfg, kivi_pool **out)
         p->err = (int *)(p->base + p->plan.off_err);
         cudaError_t e = cudaMemset(p->view.table, 0, (size_t)cfg->sequences * p->plan.max_pages * sizeof(int));
         if (e == cudaSuccess) e = cudaMemset(p->err, 0, sizeof(int));
+        if (e == cudaSuccess)
+            e = cudaMemset(p->base + p->plan.off_tickets, 0, (size_t)p->sms * kJoinsPerSm * sizeof(int));
         if (e == cudaSuccess) e = cudaDeviceSynchronize();
         if (e != cudaSuccess) {
             if (p->owns) cudaFree(p->base);
@@ -460,6 +464,7 @@ kivi_status kivi_pool_attn(kivi_pool *p, const int *seqs, const int *n_new, int 
         c.scale = (float)(1.4426950408889634 / std::sqrt((double)p->cfg.D));
         c.part = p->part;
         c.joins = (int4 *)(p->base + p->plan.off_joins);
+        c.tickets = (int *)(p->base + p->plan.off_tickets);
         c.err = p->err;
         // One after the other on the stream: they share the scratch.
         cudaError_t e = many->nb ? launch_pool_tiles(c, *many, p->sms, (cudaStream_t)stream) : cudaSuccess;

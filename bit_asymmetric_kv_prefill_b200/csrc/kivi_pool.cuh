@@ -145,6 +145,7 @@ struct AttnCall {
     float scale;          // log2(e) / sqrt(D)
     float *part;          // partial results (attention scratch of the pool)
     int4 *joins;          // per part: the segment that starts there and ends behind it (kivi_pool_rows.cu)
+    int *tickets;         // per part: partial results of that segment written so far (zero between launches)
     int *err;             // status word
 };
 
@@ -179,7 +180,7 @@ cudaError_t launch_pool_fork(const PoolView &v, const ForkTab &t, cudaStream_t s
 // Attention of few rows (matrix fragments) and of many (tcgen05 tiles), and
 // the floats of scratch each needs on a device of `sms` SMs.
 size_t pool_rows_scratch(int D, int sms);
-constexpr int kJoinsPerSm = 16;   // entries of AttnCall::joins per SM
+constexpr int kJoinsPerSm = 16;   // entries of AttnCall::joins and tickets per SM
 cudaError_t launch_pool_rows(AttnCall &c, AttnTab &t, int sms, cudaStream_t st);
 size_t pool_tiles_scratch(int D, int sms);
 cudaError_t launch_pool_tiles(AttnCall &c, AttnTab &t, int sms, cudaStream_t st);

@@ -685,7 +685,45 @@ __device__ __forceinline__ void store_rows(const AttnCall &c, const AttnTab &t, 
     *(uint32_t *)(p + 8) = y;
 }
 
-template <int D, int DT, int NT>
+// A running sum of partial results: rows 2cs, 2cs + 1 (see State).
+template <int F>
+struct Joined {
+    float o[F][4], m[2], l[2];
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int f = 0; f < F; ++f) o[f][0] = o[f][1] = o[f][2] = o[f][3] = 0.0f;
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.0f;
+    }
+    __device__ __forceinline__ void add(const float (&q)[F][4], float4 ml)
+    {
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const float pm = y ? ml.z : ml.x, pl = y ? ml.w : ml.y;
+            if (pl == 0.0f) continue;   // nothing seen (a NaN sum counts)
+            const float mn = fmaxf(m[y], pm);
+            const float fo = m[y] == -INFINITY ? 0.0f : ex2(m[y] - mn), fn = ex2(pm - mn);
+            l[y] = l[y] * fo + pl * fn;
+#pragma unroll
+            for (int f = 0; f < F; ++f) {
+                o[f][y] = o[f][y] * fo + q[f][y] * fn;
+                o[f][2 + y] = o[f][2 + y] * fo + q[f][2 + y] * fn;
+            }
+            m[y] = mn;
+        }
+    }
+};
+
+// Partial result x of the segment that starts in part w: tile a.
+template <int D, int NT>
+__device__ __forceinline__ const float *partial(const AttnCall &c, int w, int x, int a)
+{
+    return c.part + (long long)(2 * x + (x == w ? 1 : 0)) * kPartFloats<D, NT> + a * (8 * D + 16);
+}
+
+// HERE: the last warp of a segment joins its partial results.
+template <int D, int DT, int NT, bool HERE>
 __global__ void __launch_bounds__(kRowWarps * 32, row_ctas(NT))
     pool_rows_kernel(const __grid_constant__ AttnCall c, const __grid_constant__ AttnTab t)
 {
@@ -727,8 +765,10 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas(NT))
                     store_rows<DT>(c, t, e, sg.h, 8 * NT * sg.rt + 8 * a + tq, 16 * f, st.o[a][f], f0, f1);
             }
         } else {
-            if (sg.base >= lo) join = make_int4(t.part_of(sg.base + sg.C - 1), e, sg.rt, sg.h);
-            float *part = c.part + (long long)(2 * w + (sg.base >= lo ? 1 : 0)) * kPartFloats<D, NT>;
+            const bool starts = sg.base >= lo;
+            const int last = t.part_of(sg.base + sg.C - 1);
+            if (starts) join = make_int4(last, e, sg.rt, sg.h);
+            float *part = c.part + (long long)(2 * w + (starts ? 1 : 0)) * kPartFloats<D, NT>;
 #pragma unroll
             for (int a = 0; a < NT; ++a) {
                 if ((8 * NT * sg.rt + 8 * a) / c.group >= t.n[e]) break;
@@ -742,41 +782,47 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas(NT))
                     for (int x = 0; x < 2; ++x)
                         *(float2 *)(pa + 8 * D + 2 * (2 * cs + x)) = make_float2(st.m[a][x], st.l[a][x]);
             }
+            if constexpr (HERE) {
+                // The last warp to arrive adds the segment's partial results,
+                // in the order of their parts.
+                const int first = starts ? w : t.part_of(sg.base);
+                __threadfence();
+                __syncwarp();
+                int n = 0;
+                if (lane == 0) n = atomicAdd(c.tickets + first, 1);
+                n = __shfl_sync(0xffffffffu, n, 0);
+                if (n == last - first) {
+                    __threadfence();
+                    if (lane == 0) c.tickets[first] = 0;
+#pragma unroll 1
+                    for (int a = 0; a < NT; ++a) {
+                        const int row = 8 * NT * sg.rt + 8 * a;
+                        if (row / c.group >= t.n[e]) break;
+                        Joined<D / 16> s;
+                        s.clear();
+#pragma unroll 1
+                        for (int x = first; x <= last; ++x) {
+                            const float *pa = partial<D, NT>(c, first, x, a);
+                            const float4 ml = __ldcg((const float4 *)(pa + 8 * D + 4 * cs));
+                            float q[D / 16][4];
+#pragma unroll
+                            for (int f = 0; f < D / 16; ++f)
+#pragma unroll
+                                for (int y = 0; y < 4; ++y) q[f][y] = __ldcg(pa + (4 * f + y) * 32 + lane);
+                            s.add(q, ml);
+                        }
+                        const float f0 = s.l[0] == 0.0f ? 0.0f : 1.0f / s.l[0], f1 = s.l[1] == 0.0f ? 0.0f : 1.0f / s.l[1];
+#pragma unroll
+                        for (int f = 0; f < D / 16; ++f)
+                            store_rows<DT>(c, t, e, sg.h, row + tq, 16 * f, s.o[f], f0, f1);
+                    }
+                }
+            }
         }
         pos = sg.base + rb;
     }
     if (lane == 0) c.joins[w] = join;
 }
-
-// A running sum of partial results: rows 2cs, 2cs + 1 (see State).
-template <int F>
-struct Joined {
-    float o[F][4], m[2], l[2];
-    __device__ __forceinline__ void clear()
-    {
-#pragma unroll
-        for (int f = 0; f < F; ++f) o[f][0] = o[f][1] = o[f][2] = o[f][3] = 0.0f;
-        m[0] = m[1] = -INFINITY;
-        l[0] = l[1] = 0.0f;
-    }
-    __device__ __forceinline__ void add(const float (&q)[F][4], float4 ml)
-    {
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            const float pm = y ? ml.z : ml.x, pl = y ? ml.w : ml.y;
-            if (pl == 0.0f) continue;   // nothing seen (a NaN sum counts)
-            const float mn = fmaxf(m[y], pm);
-            const float fo = m[y] == -INFINITY ? 0.0f : ex2(m[y] - mn), fn = ex2(pm - mn);
-            l[y] = l[y] * fo + pl * fn;
-#pragma unroll
-            for (int f = 0; f < F; ++f) {
-                o[f][y] = o[f][y] * fo + q[f][y] * fn;
-                o[f][2 + y] = o[f][2 + y] * fo + q[f][2 + y] * fn;
-            }
-            m[y] = mn;
-        }
-    }
-};
 
 constexpr int kJoinWarps = 8;   // warps per block, parts per block
 
@@ -810,7 +856,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) pool_join_kernel(const __grid
             s.clear();
 #pragma unroll 1
             for (int x = w + wid; x <= last; x += kJoinWarps) {
-                const float *pa = c.part + (long long)(2 * x + (x == w ? 1 : 0)) * kPartFloats<D, NT> + a * (8 * D + 16);
+                const float *pa = partial<D, NT>(c, w, x, a);
                 const float4 ml = *(const float4 *)(pa + 8 * D + 4 * cs);
                 float q[NF][4];
 #pragma unroll
@@ -845,24 +891,24 @@ __global__ void __launch_bounds__(kJoinWarps * 32) pool_join_kernel(const __grid
 }
 
 template <int D, int DT, int NT>
-cudaError_t rows_t(AttnCall &c, AttnTab &t, cudaStream_t st)
+cudaError_t rows_t(AttnCall &c, AttnTab &t, bool here, cudaStream_t st)
 {
-    static PerDeviceOnce once;
-    cudaError_t e = set_smem_once(once, pool_rows_kernel<D, DT, NT>, RowsSmem<D>::BYTES);
+    static PerDeviceOnce once[2];
+    const auto kernel = here ? pool_rows_kernel<D, DT, NT, true> : pool_rows_kernel<D, DT, NT, false>;
+    cudaError_t e = set_smem_once(once[here], kernel, RowsSmem<D>::BYTES);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(pool_rows_kernel<D, DT, NT>, dim3((t.parts + kRowWarps - 1) / kRowWarps), kRowWarps * 32,
-                         RowsSmem<D>::BYTES, st, c, t);
-    if (e != cudaSuccess || t.parts == 1) return e;
+    e = launch_dependent(kernel, dim3((t.parts + kRowWarps - 1) / kRowWarps), kRowWarps * 32, RowsSmem<D>::BYTES, st, c, t);
+    if (e != cudaSuccess || here) return e;
     return launch_dependent(pool_join_kernel<D, DT, NT>, dim3((t.parts + kJoinWarps - 1) / kJoinWarps), kJoinWarps * 32, 0, st,
                             c, t);
 }
 
 template <int D, int DT>
-cudaError_t rows_n(AttnCall &c, AttnTab &t, int nt, cudaStream_t st)
+cudaError_t rows_n(AttnCall &c, AttnTab &t, int nt, bool here, cudaStream_t st)
 {
-    if (nt == 1) return rows_t<D, DT, 1>(c, t, st);
-    if (nt == 2) return rows_t<D, DT, 2>(c, t, st);
-    return rows_t<D, DT, 3>(c, t, st);
+    if (nt == 1) return rows_t<D, DT, 1>(c, t, here, st);
+    if (nt == 2) return rows_t<D, DT, 2>(c, t, here, st);
+    return rows_t<D, DT, 3>(c, t, here, st);
 }
 
 long long split_warps(int sms, int nt) { return (long long)sms * row_ctas(nt) * kRowWarps; }
@@ -897,8 +943,14 @@ cudaError_t launch_pool_rows(AttnCall &c, AttnTab &t, int sms, cudaStream_t st)
     }
     if (t.off[t.nb] == 0) return cudaSuccess;
     t.split(split_warps(sms, nt));
-    if (c.v.D == 64) return c.v.dtype ? rows_n<64, 1>(c, t, nt, st) : rows_n<64, 0>(c, t, nt, st);
-    return c.v.dtype ? rows_n<128, 1>(c, t, nt, st) : rows_n<128, 0>(c, t, nt, st);
+    // Where the parts hold an item or two, the call is all latency and a
+    // segment's last warp joins it (2 x 256 tokens: 12.4 us a call against 14.5
+    // with a launch for it); else a launch of its own does, with eight warps
+    // per segment (24 x 8K tokens: 61 us against 65, 8 x 4K of 32 heads: 52
+    // against 57).
+    const bool here = t.parts == 1 || t.quo < 2;
+    if (c.v.D == 64) return c.v.dtype ? rows_n<64, 1>(c, t, nt, here, st) : rows_n<64, 0>(c, t, nt, here, st);
+    return c.v.dtype ? rows_n<128, 1>(c, t, nt, here, st) : rows_n<128, 0>(c, t, nt, here, st);
 }
 
 }  // namespace kivi
