@@ -117,10 +117,8 @@ struct AttnTab {
     // The part that holds position pos.
     __device__ __forceinline__ int part_of(long long pos) const
     {
-        int w = (int)min((long long)parts - 1, quo > 0 ? quotient(pos, quo) : (long long)parts);
-        while (at(w) > pos) --w;
-        while (at(w + 1) <= pos) ++w;
-        return w;
+        // at(w) <= pos < at(w + 1) where w = floor(((pos + 1) * parts - 1) / total).
+        return (int)quotient((pos + 1) * parts - 1, quo * parts + rem);
     }
     // a / b for a >= 0, b > 0: short where 32 bits hold both.
     __device__ static __forceinline__ long long quotient(long long a, long long b)

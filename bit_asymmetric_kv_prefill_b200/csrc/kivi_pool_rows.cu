@@ -160,11 +160,11 @@ __device__ __forceinline__ Seg find_segment(const AttnTab &t, const AttnCall &c,
 
 template <int D>
 struct RowsSmem {
-    static constexpr int RING = kRowStages * 24 * D;   // also the staging of 32 uncoded value rows
+    static constexpr int RING = kRowStages * 24 * D;   // also the staging of 32 uncoded tokens
     static constexpr int FIRST = RING;                 // per channel: first new token whose value is not finite
     static constexpr int PER_WARP = RING + D * 4;
     static constexpr int BYTES = kRowWarps * PER_WARP;
-    static_assert(32 * D * 2 <= RING, "value rows are staged in the ring");
+    static_assert(2 * 32 * D * 2 <= RING, "uncoded keys and values are staged in the ring");
 };
 
 // Partial result of a segment: per 8-row tile the D/16 output fragments
@@ -537,56 +537,86 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
         // The last new token that a row of the tile sees, the first row's token.
         const int last_row = min(row0 + 8 * NT - 1, n * c.group - 1);
         const int last_tok = min(nk - 1, last_row / c.group), first_tok = row0 / c.group;
-#pragma unroll 1
-        for (int it = max(i0, ng); it < i1; ++it) {
-            const bool is_new = it - ng >= nres;
-            const int t0 = 32 * (is_new ? it - ng - nres : it - ng);
-            if (is_new && t0 > last_tok) break;
-            const int cnt = min(32, is_new ? nk - t0 : r_res - t0);
-            const uint16_t *kp, *vp;
+        // Blocks go through the ring, keys in its first half and values in its
+        // second; the next block's keys follow as soon as this one's are used.
+        struct Block {
+            const uint16_t *k, *v;
             long long kts, vts;
-            if (is_new) {
-                kp = c.k.p + (long long)(t.row0[e] + t0) * c.k.ts + sg.h * c.k.hs;
-                vp = c.nv.p + (long long)(t.row0[e] + t0) * c.nv.ts + sg.h * c.nv.hs;
-                kts = c.k.ts;
-                vts = c.nv.ts;
+            int t0, cnt;
+            bool is_new;
+        };
+        auto block = [&](int it) {
+            Block x;
+            x.is_new = it - ng >= nres;
+            x.t0 = 32 * (x.is_new ? it - ng - nres : it - ng);
+            x.cnt = min(32, x.is_new ? nk - x.t0 : r_res - x.t0);
+            if (x.is_new) {
+                x.k = c.k.p + (long long)(t.row0[e] + x.t0) * c.k.ts + sg.h * c.k.hs;
+                x.v = c.nv.p + (long long)(t.row0[e] + x.t0) * c.nv.ts + sg.h * c.nv.hs;
+                x.kts = c.k.ts;
+                x.vts = c.nv.ts;
             } else {
-                const long long at = (((long long)seq * v.H + sg.h) * v.R + t0) * D;
-                kp = v.resK + at;
-                vp = v.resV + at;
-                kts = vts = D;
+                const long long at = (((long long)seq * v.H + sg.h) * v.R + x.t0) * D;
+                x.k = v.resK + at;
+                x.v = v.resV + at;
+                x.kts = x.vts = D;
             }
-            // Values to shared memory (rows past the end: zeros).
+            return x;
+        };
+        const uint32_t stage_k = (uint32_t)__cvta_generic_to_shared(sm), stage_v = stage_k + 32 * D * 2;
+        const uint8_t *sm_k = sm;
+        uint8_t *sm_v = sm + 32 * D * 2;
+        // 32 rows (rows past the end: zeros).
+        auto fetch = [&](uint32_t to, const uint16_t *p, long long ts, int cnt) {
 #pragma unroll
             for (int k = 0; k < D / 8; ++k) {
                 const int q = k * 32 + lane, row = q / (D / 8), ch = q % (D / 8);
-                const uint32_t to = (uint32_t)__cvta_generic_to_shared(sm) + chunk_at<D>(row, ch);
                 const int bytes = row < cnt ? 16 : 0;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
-                             "l"(vp + (row < cnt ? row : 0) * vts + ch * 8), "r"(bytes)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + chunk_at<D>(row, ch)),
+                             "l"(p + (row < cnt ? row : 0) * ts + ch * 8), "r"(bytes)
                              : "memory");
             }
+        };
+        // Blocks of new tokens behind the tile's last are not seen.
+        const int end = min(i1, ng + nres + (last_tok + 32) / 32);
+        int it = max(i0, ng);
+        Block nx = block(it);
+        if (it < end) {
+            fetch(stage_k, nx.k, nx.kts, nx.cnt);
             cp_async_commit();
+            fetch(stage_v, nx.v, nx.vts, nx.cnt);
+        }
+        cp_async_commit();
+#pragma unroll 1
+        for (; it < end; ++it) {
+            const Block cur = nx;
+            const int t0 = cur.t0, cnt = cur.cnt;
+            const bool is_new = cur.is_new, more = it + 1 < end;
+            asm volatile("cp.async.wait_group 1;" ::: "memory");   // the keys
+            __syncwarp();
             float S[NT][2][4];
 #pragma unroll
             for (int a = 0; a < NT; ++a)
 #pragma unroll
                 for (int f = 0; f < 2; ++f) S[a][f][0] = S[a][f][1] = S[a][f][2] = S[a][f][3] = 0.0f;
 #pragma unroll
-            for (int f = 0; f < 2; ++f) {
-                const int ra = 16 * f + tq, rb = ra + 8;
+            for (int f = 0; f < 2; ++f)
 #pragma unroll
                 for (int u = 0; u < KU; ++u) {
-                    uint32_t k0[4] = {0, 0, 0, 0}, k1[4] = {0, 0, 0, 0};
-                    if (ra < cnt) *(uint4 *)k0 = *(const uint4 *)(kp + ra * kts + 32 * u + 8 * cs);
-                    if (rb < cnt) *(uint4 *)k1 = *(const uint4 *)(kp + rb * kts + 32 * u + 8 * cs);
+                    const uint4 k0 = *(const uint4 *)(sm_k + chunk_at<D>(16 * f + tq, 4 * u + cs));
+                    const uint4 k1 = *(const uint4 *)(sm_k + chunk_at<D>(16 * f + tq + 8, 4 * u + cs));
 #pragma unroll
                     for (int a = 0; a < NT; ++a) {
-                        mma<DT>(S[a][f], k0[0], k1[0], k0[1], k1[1], qf[a][u][0], qf[a][u][1]);
-                        mma<DT>(S[a][f], k0[2], k1[2], k0[3], k1[3], qf[a][u][2], qf[a][u][3]);
+                        mma<DT>(S[a][f], k0.x, k1.x, k0.y, k1.y, qf[a][u][0], qf[a][u][1]);
+                        mma<DT>(S[a][f], k0.z, k1.z, k0.w, k1.w, qf[a][u][2], qf[a][u][3]);
                     }
                 }
+            __syncwarp();
+            if (more) {
+                nx = block(it + 1);
+                fetch(stage_k, nx.k, nx.kts, nx.cnt);
             }
+            cp_async_commit();
             const bool masked = is_new && t0 + cnt - 1 > first_tok;
 #pragma unroll
             for (int a = 0; a < NT; ++a)
@@ -607,7 +637,7 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
                     pt[a][2 * f] = transpose8(pack2<DT>(S[a][f][0], S[a][f][1]));
                     pt[a][2 * f + 1] = transpose8(pack2<DT>(S[a][f][2], S[a][f][3]));
                 }
-            cp_async_wait_all();
+            asm volatile("cp.async.wait_group 1;" ::: "memory");   // the values
             __syncwarp();
             if (masked) {
                 // Some rows do not see some of these tokens: their probability
@@ -618,7 +648,7 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
 #pragma unroll 1
                 for (int k = 0; k < D / 8; ++k) {
                     const int q = k * 32 + lane, row = q / (D / 8), ch = q % (D / 8);
-                    uint16_t *x = (uint16_t *)(sm + chunk_at<D>(row, ch));
+                    uint16_t *x = (uint16_t *)(sm_v + chunk_at<D>(row, ch));
                     uint32_t w[4];
                     *(uint4 *)w = *(const uint4 *)x;
                     bool bad = false;
@@ -643,14 +673,17 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
                     uint32_t x[4];
                     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                                  : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                                 : "r"((uint32_t)__cvta_generic_to_shared(sm) + chunk_at<D>(row, ch))
+                                 : "r"(stage_v + chunk_at<D>(row, ch))
                                  : "memory");
 #pragma unroll
                     for (int a = 0; a < NT; ++a)
                         mma<DT>(st.o[a][f], x[0], x[1], x[2], x[3], pt[a][2 * mm], pt[a][2 * mm + 1]);
                 }
             __syncwarp();   // the staged values have been read
+            if (more) fetch(stage_v, nx.v, nx.vts, nx.cnt);
+            cp_async_commit();
         }
+        cp_async_wait_all();
         __syncwarp();
 #pragma unroll
         for (int a = 0; a < NT; ++a)
