@@ -857,27 +857,29 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas(NT))
     if (lane == 0) c.joins[w] = join;
 }
 
-constexpr int kJoinWarps = 8;   // warps per block, parts per block
+constexpr int kJoinParts = 8;   // parts per block
 
 // Adds the partial results of the segments that start in the block's parts and
-// end behind them.  The warps take every kJoinWarps-th of a segment's partial
-// results and then their sums, fragment by fragment: a fixed order.
+// end behind them.  Warp (y, f) takes every Y-th partial result of output
+// fragment f, four at a time so that their loads overlap, and the Y sums are
+// added at the end: a fixed order.
 template <int D, int DT, int NT>
-__global__ void __launch_bounds__(kJoinWarps * 32) pool_join_kernel(const __grid_constant__ AttnCall c,
-                                                                    const __grid_constant__ AttnTab t)
+__global__ void __launch_bounds__(1024) pool_join_kernel(const __grid_constant__ AttnCall c, const __grid_constant__ AttnTab t)
 {
-    constexpr int NF = D / 16;
-    __shared__ float sums[kJoinWarps][NF * 128 + 16];
-    __shared__ int4 list[kJoinWarps];
+    constexpr int NF = D / 16, Y = 32 / NF;
+    __shared__ float sums[Y][NF][128];
+    __shared__ float4 stats[Y][NF][4];
+    __shared__ int4 list[kJoinParts];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, tq = lane >> 2, cs = lane & 3;
-    const int w0 = blockIdx.x * kJoinWarps;
+    const int f = wid % NF, y0 = wid / NF;
+    const int w0 = blockIdx.x * kJoinParts;
     griddep_wait();
     griddep_launch();
-    if (threadIdx.x < kJoinWarps)
+    if (threadIdx.x < kJoinParts)
         list[threadIdx.x] = w0 + (int)threadIdx.x < t.parts ? c.joins[w0 + threadIdx.x] : make_int4(-1, 0, 0, 0);
     __syncthreads();
 #pragma unroll 1
-    for (int k = 0; k < kJoinWarps; ++k) {
+    for (int k = 0; k < kJoinParts; ++k) {
         const int4 j = list[k];
         const int w = w0 + k, last = j.x, e = j.y;
         if (last < 0) continue;
@@ -885,38 +887,38 @@ __global__ void __launch_bounds__(kJoinWarps * 32) pool_join_kernel(const __grid
         for (int a = 0; a < NT; ++a) {
             const int row = 8 * NT * j.z + 8 * a;
             if (row / c.group >= t.n[e]) break;
-            Joined<NF> s;
+            Joined<1> s;
             s.clear();
 #pragma unroll 1
-            for (int x = w + wid; x <= last; x += kJoinWarps) {
-                const float *pa = partial<D, NT>(c, w, x, a);
-                const float4 ml = *(const float4 *)(pa + 8 * D + 4 * cs);
-                float q[NF][4];
+            for (int x = w + y0; x <= last; x += 4 * Y) {
+                float q[4][1][4];
+                float4 ml[4];
 #pragma unroll
-                for (int f = 0; f < NF; ++f)
+                for (int z = 0; z < 4; ++z) {
+                    const bool real = x + z * Y <= last;
+                    const float *pa = partial<D, NT>(c, w, real ? x + z * Y : x, a);
+                    ml[z] = *(const float4 *)(pa + 8 * D + 4 * cs);
+                    if (!real) ml[z].y = ml[z].w = 0.0f;   // (counts as nothing seen)
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) q[f][y] = pa[(4 * f + y) * 32 + lane];
-                s.add(q, ml);
+                    for (int g = 0; g < 4; ++g) q[z][0][g] = pa[(4 * f + g) * 32 + lane];
+                }
+#pragma unroll
+                for (int z = 0; z < 4; ++z) s.add(q[z], ml[z]);
             }
 #pragma unroll
-            for (int f = 0; f < NF; ++f)
-#pragma unroll
-                for (int y = 0; y < 4; ++y) sums[wid][(4 * f + y) * 32 + lane] = s.o[f][y];
-            if (tq == 0) *(float4 *)(&sums[wid][NF * 128 + 4 * cs]) = make_float4(s.m[0], s.l[0], s.m[1], s.l[1]);
+            for (int g = 0; g < 4; ++g) sums[y0][f][g * 32 + lane] = s.o[0][g];
+            if (tq == 0) stats[y0][f][cs] = make_float4(s.m[0], s.l[0], s.m[1], s.l[1]);
             __syncthreads();
-#pragma unroll 1
-            for (int f = wid; f < NF; f += kJoinWarps) {
-                Joined<1> r;
-                r.clear();
+            if (y0 == 0) {
 #pragma unroll
-                for (int x = 0; x < kJoinWarps; ++x) {
+                for (int z = 1; z < Y; ++z) {
                     float q[1][4];
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) q[0][y] = sums[x][(4 * f + y) * 32 + lane];
-                    r.add(q, *(const float4 *)(&sums[x][NF * 128 + 4 * cs]));
+                    for (int g = 0; g < 4; ++g) q[0][g] = sums[z][f][g * 32 + lane];
+                    s.add(q, stats[z][f][cs]);
                 }
-                const float f0 = r.l[0] == 0.0f ? 0.0f : 1.0f / r.l[0], f1 = r.l[1] == 0.0f ? 0.0f : 1.0f / r.l[1];
-                store_rows<DT>(c, t, e, j.w, row + tq, 16 * f, r.o[0], f0, f1);
+                const float f0 = s.l[0] == 0.0f ? 0.0f : 1.0f / s.l[0], f1 = s.l[1] == 0.0f ? 0.0f : 1.0f / s.l[1];
+                store_rows<DT>(c, t, e, j.w, row + tq, 16 * f, s.o[0], f0, f1);
             }
             __syncthreads();
         }
@@ -932,7 +934,7 @@ cudaError_t rows_t(AttnCall &c, AttnTab &t, bool here, cudaStream_t st)
     if (e != cudaSuccess) return e;
     e = launch_dependent(kernel, dim3((t.parts + kRowWarps - 1) / kRowWarps), kRowWarps * 32, RowsSmem<D>::BYTES, st, c, t);
     if (e != cudaSuccess || here) return e;
-    return launch_dependent(pool_join_kernel<D, DT, NT>, dim3((t.parts + kJoinWarps - 1) / kJoinWarps), kJoinWarps * 32, 0, st,
+    return launch_dependent(pool_join_kernel<D, DT, NT>, dim3((t.parts + kJoinParts - 1) / kJoinParts), 1024, 0, st,
                             c, t);
 }
 
@@ -978,8 +980,8 @@ cudaError_t launch_pool_rows(AttnCall &c, AttnTab &t, int sms, cudaStream_t st)
     t.split(split_warps(sms, nt));
     // Where the parts hold an item or two, the call is all latency and a
     // segment's last warp joins it (2 x 256 tokens: 12.4 us a call against 14.5
-    // with a launch for it); else a launch of its own does, with eight warps
-    // per segment (24 x 8K tokens: 61 us against 65, 8 x 4K of 32 heads: 52
+    // with a launch for it); else a launch of its own does, with 32 warps per
+    // segment (24 x 8K tokens: 61 us against 65, 8 x 4K of 32 heads: 52
     // against 57).
     const bool here = t.parts == 1 || t.quo < 2;
     if (c.v.D == 64) return c.v.dtype ? rows_n<64, 1>(c, t, nt, here, st) : rows_n<64, 0>(c, t, nt, here, st);
