@@ -36,6 +36,8 @@
 // The 24*D-byte group blocks come through a per-warp ring of cp.async stages;
 // fragments are decoded in registers: the codes of the block are ordered so
 // that one masked word is two codes of a fragment register.
+#include <algorithm>
+
 #include <cuda_runtime.h>
 
 #include "kivi_code.cuh"
@@ -49,6 +51,8 @@ constexpr int kRowStages = 6;       // group blocks in a warp's ring
 constexpr int kRawWeight = 2;       // cost of 32 uncoded tokens, in groups
 constexpr float kLazy = 3.0f;       // the running maximum follows when exceeded by 2^kLazy
 constexpr int kMaxTiles = 3;        // 8-row tiles per warp
+constexpr int kPartItems = 4;       // least work of a part
+constexpr int kJoinHere = 16;       // parts of a segment that its last warp joins
 // CTAs per SM of a kernel with NT tiles (168 or 255 registers a thread).  One
 // tile would fit 128 registers and 4 CTAs: 80 us against 73 with 3 (24 x 8K
 // tokens, 8 kv heads of 4 query heads).
@@ -977,13 +981,19 @@ cudaError_t launch_pool_rows(AttnCall &c, AttnTab &t, int sms, cudaStream_t st)
         t.off[e + 1] = t.off[e] + tiles * c.v.H * (C > 0 ? C : 1);
     }
     if (t.off[t.nb] == 0) return cudaSuccess;
-    t.split(split_warps(sms, nt));
-    // Where the parts hold an item or two, the call is all latency and a
-    // segment's last warp joins it (2 x 256 tokens: 12.4 us a call against 14.5
-    // with a launch for it); else a launch of its own does, with 32 warps per
-    // segment (24 x 8K tokens: 61 us against 65, 8 x 4K of 32 heads: 52
-    // against 57).
-    const bool here = t.parts == 1 || t.quo < 2;
+    // At least kPartItems items per part: a partial result costs as much.
+    t.split(std::max(1LL, std::min(split_warps(sms, nt), t.off[t.nb] / kPartItems)));
+    // A small call whose segments lie in a few parts each is all latency, and
+    // the last warp of a segment joins it (2 x 256 tokens: 12.4 us a call
+    // against 14.5); else a launch of its own does, with 32 warps per segment
+    // (24 x 8K tokens: 61 us against 65 with the last warp, 8 x 4K of 32 heads
+    // 52 against 57, 4000 tokens alone 19 against 99).
+    long long longest = 0;
+    for (int e = 0; e < t.nb; ++e) {
+        const long long tiles = ((long long)t.n[e] * c.group + 8 * nt - 1) / (8 * nt);
+        if (tiles > 0) longest = std::max(longest, (t.off[e + 1] - t.off[e]) / (tiles * c.v.H));
+    }
+    const bool here = t.parts == 1 || (t.quo <= kPartItems && longest / t.quo < kJoinHere);
     if (c.v.D == 64) return c.v.dtype ? rows_n<64, 1>(c, t, nt, here, st) : rows_n<64, 0>(c, t, nt, here, st);
     return c.v.dtype ? rows_n<128, 1>(c, t, nt, here, st) : rows_n<128, 0>(c, t, nt, here, st);
 }
