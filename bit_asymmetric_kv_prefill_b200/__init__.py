@@ -145,11 +145,12 @@ def lib():
     L.kivi_pool_pages.argtypes = [vp, i32, pi, i32, pi]
     L.kivi_pool_usage.argtypes = [vp, pi, pi, pi]
     L.kivi_pool_device_status.argtypes = [vp, pi]
+    L.kivi_debug_pool.argtypes = [vp, i32, i32]
     L.kivi_pool_export.argtypes = [vp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]
     for name in ("kivi_pool_required_bytes", "kivi_pool_create", "kivi_pool_destroy", "kivi_pool_open",
                  "kivi_pool_free", "kivi_pool_extend", "kivi_pool_attn", "kivi_pool_gather", "kivi_pool_fork",
                  "kivi_pool_copy", "kivi_pool_compact", "kivi_pool_length", "kivi_pool_tokens", "kivi_pool_pages", "kivi_pool_usage",
-                 "kivi_pool_device_status", "kivi_pool_export"):
+                 "kivi_pool_device_status", "kivi_debug_pool", "kivi_pool_export"):
         getattr(L, name).restype = st
     for name in ("kivi_rope", "kivi_rope_frequencies", "kivi_cache_create", "kivi_cache_create_ex", "kivi_cache_required_bytes",
                  "kivi_prefill", "kivi_prefill_ragged", "kivi_cache_length_at", "kivi_append", "kivi_decode_attn", "kivi_decode_attn_noalloc",

@@ -104,6 +104,7 @@ struct kivi_pool {
     PoolView view;
     float *part;
     int *err;
+    int path, expire;   // testing only (kivi_debug_pool)
     std::vector<PoolSeq> seqs;
     std::vector<int> refs;                                                    // sequences that hold each page
     std::priority_queue<int, std::vector<int>, std::greater<int>> free_pages; // lowest first
@@ -199,6 +200,7 @@ kivi_status kivi_pool_create(const kivi_pool_config *cfg, kivi_pool **out)
         auto p = std::make_unique<kivi_pool>();
         p->cfg = *cfg;
         p->owns = false;
+        p->path = p->expire = 0;
         if (cudaGetDevice(&p->dev) != cudaSuccess) return KIVI_ERR_CUDA;
         p->sms = num_sms();
         make_pool_plan(cfg, p->sms, &p->plan);
@@ -437,19 +439,30 @@ kivi_status kivi_pool_attn(kivi_pool *p, const int *seqs, const int *n_new, int 
         // Sequences of few rows and of many go to kernels of their own.
         const std::unique_ptr<AttnTab> few(new AttnTab), many(new AttnTab);
         few->nb = many->nb = 0;
-        const int group = H_q / p->cfg.H_kv;
+        const int group = H_q / p->cfg.H_kv, gpp = p->cfg.R / kG;
+        double rows_us = 0.0, tiles_us = kTilesFixedUs;   // for the sequences of many rows
+        for (int i = 0; i < n; ++i) {
+            const long long rows = (long long)n_new[i] * group;
+            if (rows <= kTileMinRows) continue;
+            const PoolSeq &s = p->seqs[seqs[i]];
+            const double groups = (double)s.pages.size() * gpp + (s.r + (k ? n_new[i] / 2 : 0)) / 16.0;
+            rows_us += kRowsUs / p->sms * p->cfg.H_kv * ((rows + 23) / 24) * groups;
+            tiles_us += kTileUs / p->sms * p->cfg.H_kv * ((rows + 255) / 256) * (groups / 3.0 + 1.0);
+        }
+        const bool tiles = p->path == 0 ? tiles_us < rows_us : p->path == 2;
+        const long long fewest = p->path == 2 ? 0 : kTileMinRows;
         int row = 0;
         for (int i = 0; i < n; ++i) {
             const PoolSeq &s = p->seqs[seqs[i]];
             if (n_new[i] == 0) continue;
             const bool sees = k || s.r > 0;
-            AttnTab &t = sees && (long long)n_new[i] * group > kTileMinRows ? *many : *few;
+            AttnTab &t = tiles && sees && (long long)n_new[i] * group > fewest ? *many : *few;
             const int e = t.nb++;
             t.seq[e] = seqs[i];
             t.row0[e] = row;
             t.n[e] = n_new[i];
             t.nk[e] = k ? n_new[i] : 0;
-            t.ng[e] = (int)(s.pages.size() * (p->cfg.R / kG));
+            t.ng[e] = (int)s.pages.size() * gpp;
             t.r[e] = s.r;
             row += n_new[i];
         }
@@ -466,6 +479,7 @@ kivi_status kivi_pool_attn(kivi_pool *p, const int *seqs, const int *n_new, int 
         c.joins = (int4 *)(p->base + p->plan.off_joins);
         c.tickets = (int *)(p->base + p->plan.off_tickets);
         c.err = p->err;
+        c.expire = p->expire;
         // One after the other on the stream: they share the scratch.
         cudaError_t e = many->nb ? launch_pool_tiles(c, *many, p->sms, (cudaStream_t)stream) : cudaSuccess;
         if (e == cudaSuccess && few->nb) e = launch_pool_rows(c, *few, p->sms, (cudaStream_t)stream);
@@ -627,6 +641,14 @@ kivi_status kivi_pool_compact(kivi_pool *p, int *moved, void *stream)
         p->free_pages = decltype(p->free_pages)(std::greater<int>(), std::move(ids));
         return KIVI_OK;
     });
+}
+
+kivi_status kivi_debug_pool(kivi_pool *p, int path, int expire)
+{
+    if (!p || path < 0 || path > 2) return KIVI_ERR_ARG;
+    p->path = path;
+    p->expire = expire != 0;
+    return KIVI_OK;
 }
 
 kivi_status kivi_pool_device_status(kivi_pool *p, int *code)

@@ -145,6 +145,7 @@ struct AttnCall {
     int4 *joins;          // per part: the segment that starts there and ends behind it (kivi_pool_rows.cu)
     int *tickets;         // per part: partial results of that segment written so far (zero between launches)
     int *err;             // status word
+    int expire;           // testing the failure path: waits give up at once
 };
 
 // Launch as a programmatic dependent of the launch before it on the stream: the
@@ -182,7 +183,13 @@ constexpr int kJoinsPerSm = 16;   // entries of AttnCall::joins and tickets per 
 cudaError_t launch_pool_rows(AttnCall &c, AttnTab &t, int sms, cudaStream_t st);
 size_t pool_tiles_scratch(int D, int sms);
 cudaError_t launch_pool_tiles(AttnCall &c, AttnTab &t, int sms, cudaStream_t st);
-// Entries with more rows per kv head than this take the tiles.
-constexpr int kTileMinRows = 32;
+// Entries with more rows per kv head than this take the tiles, unless the whole
+// call is cheaper in fragments.  Measured on one SM: 24 rows against 32 tokens
+// 0.35 us, 256 rows (or any fewer) against 96 tokens 2.4 us, so two passes of 24
+// rows are cheaper than tiles and three are not; and a launch of the tiles with
+// its join costs about 25 us more (one kv head pair, 100 tokens after 200: 54 us
+// against 27).
+constexpr int kTileMinRows = 48;
+constexpr double kRowsUs = 0.35, kTileUs = 2.4, kTilesFixedUs = 25.0;
 
 }  // namespace kivi

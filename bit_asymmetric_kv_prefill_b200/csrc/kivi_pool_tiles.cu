@@ -847,6 +847,9 @@ __device__ __forceinline__ void softmax_role(const AttnCall &c, const AttnTab &t
             }
         }
         if (real && !w.whole) *(float2 *)(po + (long long)kTileRows * D + 2 * (a * 128 + m_row)) = make_float2(m, l);
+        // (Only a range's last segment can start in it and end behind it.)
+        if (!w.whole && w.s.base >= w.lo && a == 0 && m_row == 0)
+            c.joins[part] = make_int4(t.part_of(w.s.base + w.s.nc + w.s.nr - 1), e, w.s.rt, w.s.h);
         tc_before();
     }
 }
@@ -880,6 +883,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (wid == kSoftWarps + kDecodeWarps) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(saddr(tmem_at)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    // Everything above touches no global memory and runs while the launch
+    // before this one finishes.
+    griddep_wait();
+    griddep_launch();
+    if (threadIdx.x == 0) {
+        c.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);   // (softmax_role may set it)
+        if (c.expire) {
+            *stop = 1;
+            atomicCAS(c.err, 0, KIVI_DEVICE_WAIT_TIMEOUT);
+        }
     }
     tc_before();
     __syncthreads();
@@ -922,49 +936,58 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (wid == kSoftWarps + kDecodeWarps) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
+constexpr int kJoinRows = 32;   // rows per block
+
 // Adds the partial results of the segment that starts in range blockIdx.x and
-// ends behind it (if there is one): a warp per row, rows by blockIdx.y.
+// ends behind it (if there is one): a warp per row, four partial results at a
+// time so that their loads overlap.
 template <int D, int DT>
-__global__ void __launch_bounds__(256) pool_tiles_join_kernel(const __grid_constant__ AttnCall c,
-                                                              const __grid_constant__ AttnTab t)
+__global__ void __launch_bounds__(kJoinRows * 32) pool_tiles_join_kernel(const __grid_constant__ AttnCall c,
+                                                                         const __grid_constant__ AttnTab t)
 {
+    griddep_wait();
+    griddep_launch();
     const int w = blockIdx.x;
-    const long long lo = t.at(w), hi = t.at(w + 1);
-    if (hi >= t.off[t.nb] || lo >= hi) return;
-    const TSeg s = find_segment(t, c, hi - 1);
-    const long long end = s.base + s.nc + s.nr;
-    if (s.base < lo || end <= hi) return;
-    const int lane = threadIdx.x & 31;
-    const int last = t.part_of(end - 1);
+    const int4 j = c.joins[w];
+    const int last = j.x, e = j.y, lane = threadIdx.x & 31;
+    if (last < 0) return;
     constexpr int E = D / 32;
-    for (int k = threadIdx.x >> 5; k < kTileRows / 8; k += 8) {
-        const int lr = blockIdx.y * (kTileRows / 8) + k;
-        const long long row = (long long)s.rt * kTileRows + lr;
-        const int tok = (int)(row / c.group);
-        if (tok >= t.n[s.e]) return;
-        float m = -INFINITY, l = 0.0f, o[E];
+    const int lr = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
+    const long long row = (long long)j.z * kTileRows + lr;
+    const int tok = (int)(row / c.group);
+    if (tok >= t.n[e]) return;
+    float m = -INFINITY, l = 0.0f, o[E];
 #pragma unroll
-        for (int z = 0; z < E; ++z) o[z] = 0.0f;
-        for (int x = w; x <= last; ++x) {
-            const float *po = c.part + (long long)x * 2 * kTilePart<D> + (x == w ? kTilePart<D> : 0);
-            const float2 ml = *(const float2 *)(po + (long long)kTileRows * D + 2 * lr);
-            float y[E];
+    for (int z = 0; z < E; ++z) o[z] = 0.0f;
+#pragma unroll 1
+    for (int x = w; x <= last; x += 4) {
+        float y[4][E];
+        float2 ml[4];
 #pragma unroll
-            for (int z = 0; z < E; ++z) y[z] = po[(long long)lr * D + lane * E + z];
-            if (ml.y == 0.0f) continue;   // nothing seen (a NaN sum counts)
-            const float mn = fmaxf(m, ml.x);
-            const float f = m == -INFINITY ? 0.0f : ex2(m - mn), g = ex2(ml.x - mn);
-            l = l * f + ml.y * g;
+        for (int k = 0; k < 4; ++k) {
+            const bool real = x + k <= last;
+            const int q = real ? x + k : x;
+            const float *po = c.part + (long long)q * 2 * kTilePart<D> + (q == w ? kTilePart<D> : 0);
+            ml[k] = *(const float2 *)(po + (long long)kTileRows * D + 2 * lr);
+            if (!real) ml[k].y = 0.0f;
 #pragma unroll
-            for (int z = 0; z < E; ++z) o[z] = o[z] * f + y[z] * g;
+            for (int z = 0; z < E; ++z) y[k][z] = po[(long long)lr * D + lane * E + z];
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (ml[k].y == 0.0f) continue;   // nothing seen (a NaN sum counts)
+            const float mn = fmaxf(m, ml[k].x);
+            const float f = m == -INFINITY ? 0.0f : ex2(m - mn), g = ex2(ml[k].x - mn);
+            l = l * f + ml[k].y * g;
+#pragma unroll
+            for (int z = 0; z < E; ++z) o[z] = o[z] * f + y[k][z] * g;
             m = mn;
         }
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        uint16_t *out = c.out
-                        + ((long long)(t.row0[s.e] + tok) * c.H_q + s.h * c.group + (row - (long long)tok * c.group)) * D;
-#pragma unroll
-        for (int z = 0; z < E; z += 2) *(uint32_t *)(out + lane * E + z) = pack2<DT>(o[z] * inv, o[z + 1] * inv);
     }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint16_t *out = c.out + ((long long)(t.row0[e] + tok) * c.H_q + j.w * c.group + (row - (long long)tok * c.group)) * D;
+#pragma unroll
+    for (int z = 0; z < E; z += 2) *(uint32_t *)(out + lane * E + z) = pack2<DT>(o[z] * inv, o[z + 1] * inv);
 }
 
 template <int D, int DT>
@@ -973,11 +996,9 @@ cudaError_t tiles_t(AttnCall &c, AttnTab &t, cudaStream_t st)
     static PerDeviceOnce once;
     cudaError_t e = set_smem_once(once, pool_tiles_kernel<D, DT>, TileSmem<D>::BYTES);
     if (e != cudaSuccess) return e;
-    pool_tiles_kernel<D, DT><<<(unsigned)t.parts, kThreads, TileSmem<D>::BYTES, st>>>(c, t);
-    e = cudaGetLastError();
+    e = launch_dependent(pool_tiles_kernel<D, DT>, dim3(t.parts), kThreads, TileSmem<D>::BYTES, st, c, t);
     if (e != cudaSuccess || t.parts == 1) return e;
-    pool_tiles_join_kernel<D, DT><<<dim3((unsigned)t.parts, 8), 256, 0, st>>>(c, t);
-    return cudaGetLastError();
+    return launch_dependent(pool_tiles_join_kernel<D, DT>, dim3(t.parts, kTileRows / kJoinRows), kJoinRows * 32, 0, st, c, t);
 }
 
 }  // namespace

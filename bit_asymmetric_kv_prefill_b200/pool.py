@@ -178,6 +178,10 @@ class KiviPool:
         _check(lib().kivi_pool_usage(self._h, *[ctypes.byref(x) for x in a]), "kivi_pool_usage")
         return dict(zip(("pages_used", "pages_end", "sequences_open"), (x.value for x in a)))
 
+    def debug(self, path: int = 0, expire: bool = False) -> None:
+        """Testing: fix the attention's form and try its failure path (see kivi_debug_pool)."""
+        _check(lib().kivi_debug_pool(self._h, path, int(expire)), "kivi_debug_pool")
+
     def device_status(self) -> int:
         code = ctypes.c_int()
         with _on_device(self.device.index):

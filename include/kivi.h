@@ -503,6 +503,14 @@ KIVI_API kivi_status kivi_pool_usage(const kivi_pool *p, int *pages_used, int *p
 /* As kivi_device_status: 0, or the code of the first failed bounded wait. */
 KIVI_API kivi_status kivi_pool_device_status(kivi_pool *p, int *code);
 
+/* Testing: later kivi_pool_attn calls take one form whatever their size (path
+ * 1: matrix fragments of few rows, 2: tiles of 256 rows, 0: as measured to be
+ * faster), and with expire != 0 the tiles' waits for data that is not there yet
+ * give up at once: the status word reports KIVI_DEVICE_WAIT_TIMEOUT, `out` is
+ * undefined, the next call with expire = 0 runs normally.  Nothing faults or
+ * hangs. */
+KIVI_API kivi_status kivi_debug_pool(kivi_pool *p, int path, int expire);
+
 /* One head of a sequence in the canonical layout of kivi_export (nseq = 1);
  * testing and inspection, synchronises the device. */
 KIVI_API kivi_status kivi_pool_export(const kivi_pool *p, int seq, int head, uint8_t *codesK,

@@ -64,6 +64,8 @@ def test_null_pools_are_refused():
     assert L.kivi_pool_pages(None, 0, None, 0, ctypes.byref(n)) == 1
     assert L.kivi_pool_usage(None, None, None, None) == 1
     assert L.kivi_pool_device_status(None, ctypes.byref(n)) == 1
+    assert L.kivi_debug_pool(None, 0, 0) == 1
+    assert L.kivi_pool_tokens(None, ctypes.byref(n), 1, ctypes.byref(i64)) == 1
     assert L.kivi_pool_export(None, 0, 0, *([None] * 8)) == 1
 
 
@@ -346,23 +348,56 @@ ATTN = [
 ]
 
 
+FORMS = pytest.mark.parametrize("form", [1, 2], ids=["fragments", "tiles"])
+
+
 @pytest.mark.gpu
+@FORMS
 @pytest.mark.parametrize("H,g,D,dtype,R,T,n", ATTN)
-def test_attention_of_new_tokens(H, g, D, dtype, R, T, n):
+def test_attention_of_new_tokens(H, g, D, dtype, R, T, n, form):
+    """Both forms of the attention, each at sizes that a call would give to the other."""
     pool, seqs, K, V, q, k, v = _case(H, g, D, dtype, R, T, n, seed=sum(T) + sum(n))
+    pool.debug(path=form)
     out = pool.attend(seqs, q, k, v, n)
     _verify(pool, out, T, n, K, V, q, k, v, R)
 
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("H,g,D,dtype,R,T,n", [
+    (8, 8, 64, "bf16", 128, [1300, 400], [150, 3]),      # tiles for the long chunk, fragments for the other
+    (4, 4, 128, "fp16", 64, [2600], [300]),
+])
+def test_attention_chooses_its_form(H, g, D, dtype, R, T, n):
+    pool, seqs, K, V, q, k, v = _case(H, g, D, dtype, R, T, n, seed=5)
+    out = pool.attend(seqs, q, k, v, n)
+    _verify(pool, out, T, n, K, V, q, k, v, R)
+
+
+@pytest.mark.gpu
+def test_an_expired_wait_is_reported_and_the_next_call_is_clean():
+    H, g, D, R, T, n = 2, 4, 128, 128, [500], [40]
+    pool, seqs, K, V, q, k, v = _case(H, g, D, "bf16", R, T, n, seed=3)
+    pool.debug(path=2)
+    want = pool.attend(seqs, q, k, v, n)
+    pool.debug(path=2, expire=True)
+    pool.attend(seqs, q, k, v, n)
+    assert pool.device_status() == 1 and pool.device_status() == 0
+    pool.debug(path=2)
+    assert torch.equal(pool.attend(seqs, q, k, v, n), want)
+    assert pool.device_status() == 0
+
+
+@pytest.mark.gpu
+@FORMS
+@pytest.mark.parametrize("H,g,D,dtype,R,T,n", [
     (2, 4, 128, "bf16", 128, [1000, 0, 5], [1, 2, 1]),
     (2, 1, 64, "fp16", 32, [96, 97], [1, 1]),
     (1, 2, 128, "fp16", 64, [300, 0], [70, 90]),
 ])
-def test_attention_over_the_cache_alone(H, g, D, dtype, R, T, n):
+def test_attention_over_the_cache_alone(H, g, D, dtype, R, T, n, form):
     """Without new keys every row sees what is cached; a row that sees nothing is zero."""
     pool, seqs, K, V, q, _, _ = _case(H, g, D, dtype, R, T, n, seed=7)
+    pool.debug(path=form)
     out = pool.attend(seqs, q, None, None, n)
     _verify(pool, out, T, n, K, V, q, None, None, R)
     for i, t in enumerate(T):
@@ -371,11 +406,13 @@ def test_attention_over_the_cache_alone(H, g, D, dtype, R, T, n):
 
 
 @pytest.mark.gpu
+@FORMS
 @pytest.mark.parametrize("n", [3, 150])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
-def test_values_that_are_not_finite_stay_with_the_rows_that_see_them(n, dtype):
+def test_values_that_are_not_finite_stay_with_the_rows_that_see_them(n, dtype, form):
     H, g, D, R, T = 1, 4, 128, 128, 200
     pool, seqs, K, V, q, k, v = _case(H, g, D, dtype, R, [T], [n], seed=12)
+    pool.debug(path=form)
     late = n - 2
     v[late, 0, 5] = float("nan")
     v[late + 1, 0, 9] = float("inf")
@@ -389,10 +426,12 @@ def test_values_that_are_not_finite_stay_with_the_rows_that_see_them(n, dtype):
 
 
 @pytest.mark.gpu
+@FORMS
 @pytest.mark.parametrize("n", [2, 140])
-def test_strided_rows_repeats_and_rows_left_alone(n):
+def test_strided_rows_repeats_and_rows_left_alone(n, form):
     H, g, D, R = 2, 2, 64, 32
     pool, seqs, K, V, q, k, v = _case(H, g, D, "fp16", R, [150, 70], [n, n], seed=21)
+    pool.debug(path=form)
     buf = torch.zeros(2 * n, (H * g + 2 * H + 1) * D, device="cuda", dtype=torch.float16)
     view = lambda h0, h: buf[:, h0 * D:(h0 + h) * D].unflatten(1, (h, D))  # noqa: E731
     view(0, H * g).copy_(q), view(H * g, H).copy_(k), view(H * g + H, H).copy_(v)
@@ -408,11 +447,13 @@ def test_strided_rows_repeats_and_rows_left_alone(n):
 
 
 @pytest.mark.gpu
-def test_attention_on_streams_and_in_graphs():
+@FORMS
+def test_attention_on_streams_and_in_graphs(form):
     """Repeats are bit-equal; a captured call replays on new inputs; two graphs that share the scratch, replayed one
     after the other, keep their results."""
     H, g, D, R = 2, 4, 128, 128
     pool, seqs, K, V, q, k, v = _case(H, g, D, "bf16", R, [2000, 900], [1, 130], seed=4)
+    pool.debug(path=form)
     args = (q, k, v)
     want = pool.attend(seqs, *args, [1, 130])
     assert torch.equal(want, pool.attend(seqs, *args, [1, 130]))
