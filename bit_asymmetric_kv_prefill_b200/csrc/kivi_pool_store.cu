@@ -6,6 +6,8 @@
 // the residual and in the new rows, at any strides.
 // All kernels here are HBM bound: a quantized element costs 2 bytes read and
 // 0.375 written, a gathered one 0.375 read and 2 written.
+#include <algorithm>
+
 #include <cuda_runtime.h>
 
 #include "kivi_code.cuh"
@@ -53,8 +55,9 @@ __device__ __forceinline__ int tile_at(int t, int c)
 // so the statistics are its own.  A word of the block (one token, 16 channels)
 // is shared by 4 (D = 128) or 8 lanes: they exchange codes in a transposing
 // OR-shuffle over lane bits LB, after which each lane stores whole words.
-template <int D, int DT>
-__device__ __forceinline__ void page_key_tile(const uint8_t *tile, uint8_t *blk, int lane)
+// loaded(): the tile has been read.
+template <int D, int DT, typename F>
+__device__ __forceinline__ void page_key_tile(const uint8_t *tile, uint8_t *blk, int lane, F &&loaded)
 {
     using L = PageLayout<D>;
     using H = In<DT>;
@@ -74,6 +77,7 @@ __device__ __forceinline__ void page_key_tile(const uint8_t *tile, uint8_t *blk,
             x[t][0] = *(const uint32_t *)s;
         }
     }
+    loaded();
     uint32_t T1[NP], T2[NP], T3[NP];
     uint64_t mn64 = 0, mx64 = 0;
 #pragma unroll
@@ -151,8 +155,8 @@ __device__ __forceinline__ void page_key_tile(const uint8_t *tile, uint8_t *blk,
 // transposing shuffle over lane bits 2, 3, 4, compute the parameters of their
 // share and publish the thresholds (packed for the two tokens) in `thr`
 // [4 pairs][NJ][4 cs].
-template <int D, int DT>
-__device__ __forceinline__ void page_value_tile(const uint8_t *tile, uint8_t *blk, int lane, uint4 *thr)
+template <int D, int DT, typename F>
+__device__ __forceinline__ void page_value_tile(const uint8_t *tile, uint8_t *blk, int lane, uint4 *thr, F &&loaded)
 {
     using L = PageLayout<D>;
     using H = In<DT>;
@@ -167,9 +171,11 @@ __device__ __forceinline__ void page_value_tile(const uint8_t *tile, uint8_t *bl
             const uint32_t a = base + tile_at<D>(8 * p + (lane & 7), c + (lane >> 3));
             asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                          : "=r"(x[p][c]), "=r"(x[p][c + 1]), "=r"(x[p][c + 2]), "=r"(x[p][c + 3])
-                         : "r"(a));
+                         : "r"(a)
+                         : "memory");
         }
     }
+    loaded();
     // mn, nx [combination p*NJ + j]: per token min and -max (as a min).
     uint32_t mn[NV], nx[NV];
 #pragma unroll
@@ -256,38 +262,56 @@ struct StoreSmem {
     static constexpr int BYTES = kStoreWarps * PER_WARP;
 };
 
-// One warp per (32-token group, head) item and kind of tile.
+// Units: the key and the value tile of each (32-token group, head) item.  A
+// warp takes every W-th; the next unit's tile is fetched as soon as this one's
+// is in registers, so its load runs under the codes.
 template <int D, int DT>
-__global__ void __launch_bounds__(kStoreWarps * 32)
+__global__ void __launch_bounds__(kStoreWarps * 32, 4)
     pool_quant_kernel(const PoolView v, const Rows k, const Rows nv, const __grid_constant__ ExtendTab t)
 {
     extern __shared__ __align__(128) uint8_t sm[];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     uint8_t *tile = sm + wid * StoreSmem<D>::PER_WARP;
-    const int unit = blockIdx.x * kStoreWarps + wid;
-    if (unit >= 2 * t.item[t.nb]) return;
-    const int item = unit >> 1, vhalf = unit & 1;
-    const int e = entry_of(t.item, t.nb, item);
-    const int local = item - t.item[e], g = local / v.H, h = local - g * v.H;
-    const int seq = t.seq[e], r = t.r[e];
-    const uint16_t *res = (vhalf ? v.resV : v.resK) + ((long long)seq * v.H + h) * v.R * D;
-    const Rows &src = vhalf ? nv : k;
+    const int units = 2 * t.item[t.nb], step = gridDim.x * kStoreWarps;
     constexpr int C = D / 8;
     const uint32_t base = (uint32_t)__cvta_generic_to_shared(tile);
+    // Fetches unit u's tile; returns its block.
+    auto fetch = [&](int u) -> uint8_t * {
+        const int item = u >> 1, vhalf = u & 1;
+        const int e = entry_of(t.item, t.nb, item);
+        const int local = item - t.item[e], g = local / v.H, h = local - g * v.H;
+        const int seq = t.seq[e], r = t.r[e];
+        const uint16_t *res = (vhalf ? v.resV : v.resK) + ((long long)seq * v.H + h) * v.R * D;
+        const uint16_t *rows = vhalf ? nv.p : k.p;
+        const long long ts = vhalf ? nv.ts : k.ts, hs = vhalf ? nv.hs : k.hs;
+        const uint16_t *fresh = rows + (long long)(t.row0[e] + 32 * g - r) * ts + h * hs;   // token 32 g, were it new
 #pragma unroll
-    for (int it = 0; it < C; ++it) {
-        const int q = it * 32 + lane, row = q / C, c = q % C;
-        const int tok = 32 * g + row;   // from the sequence's first unquantized token
-        const uint16_t *p = tok < r ? res + (long long)tok * D
-                                    : src.p + (long long)(t.row0[e] + tok - r) * src.ts + h * src.hs;
-        cp_async16_zfill(base + tile_at<D>(row, c), p + c * 8, true);
+        for (int it = 0; it < C; ++it) {
+            const int q = it * 32 + lane, row = q / C, c = q % C;
+            const int tok = 32 * g + row;   // from the sequence's first unquantized token
+            const uint16_t *p = tok < r ? res + (long long)tok * D : fresh + row * ts;
+            cp_async16_zfill(base + tile_at<D>(row, c), p + c * 8, true);
+        }
+        cp_async_commit();
+        return page_block(v, seq, t.g0[e] + g, h, PageLayout<D>::GB);
+    };
+    int u = blockIdx.x * kStoreWarps + wid;
+    if (u >= units) return;
+    uint8_t *blk = fetch(u);
+    for (;;) {
+        cp_async_wait_all();
+        __syncwarp();
+        uint8_t *next = nullptr;
+        auto loaded = [&]() {
+            __syncwarp();
+            if (u + step < units) next = fetch(u + step);
+        };
+        if (!(u & 1)) page_key_tile<D, DT>(tile, blk, lane, loaded);
+        else page_value_tile<D, DT>(tile, blk, lane, (uint4 *)(tile + StoreSmem<D>::TILE), loaded);
+        if (next == nullptr) break;
+        u += step;
+        blk = next;
     }
-    cp_async_commit();
-    uint8_t *blk = page_block(v, seq, t.g0[e] + g, h, PageLayout<D>::GB);
-    cp_async_wait_all();
-    __syncwarp();
-    if (!vhalf) page_key_tile<D, DT>(tile, blk, lane);
-    else page_value_tile<D, DT>(tile, blk, lane, (uint4 *)(tile + StoreSmem<D>::TILE));
 }
 
 // New rows that stay unquantized go to their residual slots: one 16-byte chunk
@@ -326,15 +350,23 @@ __device__ __forceinline__ uint32_t round2(float a, float b)
     }
     return r;
 }
-__device__ __forceinline__ float half_lo(uint32_t x) { return __half2float(__ushort_as_half((uint16_t)x)); }
-__device__ __forceinline__ float half_hi(uint32_t x) { return __half2float(__ushort_as_half((uint16_t)(x >> 16))); }
-
-// Pair i of a code word, decoded and rounded to the pool's type: s, z packed.
-template <int DT>
-__device__ __forceinline__ uint32_t decode_pair(uint32_t w, int i, uint32_t s, uint32_t z)
+__device__ __forceinline__ float2 halves(uint32_t x)
 {
-    const float a = (float)((w >> (2 * i)) & 3u), b = (float)((w >> (16 + 2 * i)) & 3u);
-    return round2<DT>(__fmaf_rn(a, half_lo(s), half_lo(z)), __fmaf_rn(b, half_hi(s), half_hi(z)));
+    __half2 h;
+    memcpy(&h, &x, 4);
+    return __half22float2(h);
+}
+
+// Pair i of a code word, decoded (in fp32) and rounded to the pool's type.  The
+// codes come as fp16: on top of 1024, minus 1024 (exact).
+template <int DT>
+__device__ __forceinline__ uint32_t decode_pair(uint32_t w, int i, float2 s, float2 z)
+{
+    const uint32_t x = ((w >> (2 * i)) & 0x00030003u) | 0x64006400u;
+    __half2 h;
+    memcpy(&h, &x, 4);
+    const float2 c = __half22float2(__hadd2(h, __float2half2_rn(-1024.0f)));
+    return round2<DT>(__fmaf_rn(c.x, s.x, z.x), __fmaf_rn(c.y, s.y, z.y));
 }
 
 // One warp per (32 tokens, head): decode K and V (values through shared memory,
@@ -379,11 +411,17 @@ __global__ void __launch_bounds__(kStoreWarps * 32)
         uint2 zs[4];
         *(uint4 *)zs = *(const uint4 *)(blk + L::KM + (16 * u + 4 * cs) * 8);
         *(uint4 *)(zs + 2) = *(const uint4 *)(blk + L::KM + (16 * u + 4 * cs) * 8 + 16);
+        float2 z[4], s[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            z[p] = halves(zs[p].x);
+            s[p] = halves(zs[p].y);
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             uint32_t o[4];
 #pragma unroll
-            for (int p = 0; p < 4; ++p) o[p] = decode_pair<DT>(kw[j * L::KW + u / 2], 4 * (u % 2) + p, zs[p].y, zs[p].x);
+            for (int p = 0; p < 4; ++p) o[p] = decode_pair<DT>(kw[j * L::KW + u / 2], 4 * (u % 2) + p, s[p], z[p]);
             *(uint4 *)(ko + (tq + 8 * j) * ts + 32 * u + 8 * cs) = *(const uint4 *)o;
         }
     }
@@ -393,9 +431,10 @@ __global__ void __launch_bounds__(kStoreWarps * 32)
 #pragma unroll
         for (int j = 0; j < L::NJ; ++j) {
             const uint2 sz = *(const uint2 *)(blk + L::VM + page_vm_offset<D>(p, cs, j));
+            const float2 s = halves(sz.x), z = halves(sz.y);
             uint32_t o[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) o[c] = decode_pair<DT>(vw[p * L::KW + j / 2], 4 * (j % 2) + c, sz.x, sz.y);
+            for (int c = 0; c < 4; ++c) o[c] = decode_pair<DT>(vw[p * L::KW + j / 2], 4 * (j % 2) + c, s, z);
             const uint32_t a = base + tile_at<D>(8 * p + (lane & 7), 4 * j + (lane >> 3));
             asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(o[0]),
                          "r"(o[1]), "r"(o[2]), "r"(o[3])
@@ -426,19 +465,28 @@ __global__ void __launch_bounds__(256)
     for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += step) to[i] = from[i];
 }
 
-// Blocks (head, entry): the residual rows of one head; head 0's block also the
-// table row.
+// Blocks (slice, head, entry): a slice of the residual rows of one head; the
+// first block of an entry also the table row.
+constexpr int kForkSlices = 4;
 __global__ void __launch_bounds__(256) pool_fork_kernel(const PoolView v, const __grid_constant__ ForkTab t)
 {
-    const int e = blockIdx.y, h = blockIdx.x;
+    const int e = blockIdx.z, h = blockIdx.y;
     const long long a = ((long long)t.src[e] * v.H + h) * v.R * v.D, b = ((long long)t.dst[e] * v.H + h) * v.R * v.D;
     const int n = t.r[e] * v.D / 8;
-    for (int i = threadIdx.x; i < n; i += 256) {
-        const uint4 x = ((const uint4 *)(v.resK + a))[i], y = ((const uint4 *)(v.resV + a))[i];
-        ((uint4 *)(v.resK + b))[i] = x;
-        ((uint4 *)(v.resV + b))[i] = y;
+    const uint4 *ka = (const uint4 *)(v.resK + a), *va = (const uint4 *)(v.resV + a);
+    uint4 *kb = (uint4 *)(v.resK + b), *vb = (uint4 *)(v.resV + b);
+    constexpr int step = kForkSlices * 256;
+    for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += 2 * step) {
+        const bool two = i + step < n;
+        const uint4 x = ka[i], y = va[i], z = two ? ka[i + step] : x, w = two ? va[i + step] : y;
+        kb[i] = x;
+        vb[i] = y;
+        if (two) {
+            kb[i + step] = z;
+            vb[i + step] = w;
+        }
     }
-    if (h == 0)
+    if (h == 0 && blockIdx.x == 0)
         for (int i = threadIdx.x; i < t.np[e]; i += 256)
             v.table[(long long)t.dst[e] * v.max_pages + i] = v.table[(long long)t.src[e] * v.max_pages + i];
 }
@@ -449,7 +497,7 @@ cudaError_t quant_t(const PoolView &v, const Rows &k, const Rows &nv, const Exte
     static PerDeviceOnce once;
     const cudaError_t e = set_smem_once(once, pool_quant_kernel<D, DT>, StoreSmem<D>::BYTES);
     if (e != cudaSuccess) return e;
-    const unsigned grid = (2u * t.item[t.nb] + kStoreWarps - 1) / kStoreWarps;
+    const unsigned grid = std::min((2u * t.item[t.nb] + kStoreWarps - 1) / kStoreWarps, 4u * num_sms());
     pool_quant_kernel<D, DT><<<grid, kStoreWarps * 32, StoreSmem<D>::BYTES, st>>>(v, k, nv, t);
     return cudaGetLastError();
 }
@@ -508,7 +556,7 @@ cudaError_t launch_pool_move(const PoolView &v, const PairTab &t, cudaStream_t s
 cudaError_t launch_pool_fork(const PoolView &v, const ForkTab &t, cudaStream_t st)
 {
     if (t.n == 0) return cudaSuccess;
-    pool_fork_kernel<<<dim3(v.H, t.n), 256, 0, st>>>(v, t);
+    pool_fork_kernel<<<dim3(kForkSlices, v.H, t.n), 256, 0, st>>>(v, t);
     return cudaGetLastError();
 }
 
