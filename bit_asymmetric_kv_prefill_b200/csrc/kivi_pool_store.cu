@@ -369,61 +369,61 @@ __device__ __forceinline__ uint32_t decode_pair(uint32_t w, int i, float2 s, flo
     return round2<DT>(__fmaf_rn(c.x, s.x, z.x), __fmaf_rn(c.y, s.y, z.y));
 }
 
-// One warp per (32 tokens, head): decode K and V (values through shared memory,
-// since a lane holds columns of them) or copy residual rows.
+// One warp per 32 tokens of K or of V of a head: decode (values through shared
+// memory, since a lane holds columns of them) or copy residual rows.
 template <int D, int DT>
-__global__ void __launch_bounds__(kStoreWarps * 32)
+__global__ void __launch_bounds__(kStoreWarps * 32, 8)
     pool_gather_kernel(const PoolView v, const __grid_constant__ GatherTab t, uint16_t *K, uint16_t *V)
 {
     using L = PageLayout<D>;
     extern __shared__ __align__(128) uint8_t sm[];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     uint8_t *tile = sm + wid * StoreSmem<D>::TILE;
-    const int item = blockIdx.x * kStoreWarps + wid;
+    const int unit = blockIdx.x * kStoreWarps + wid, item = unit >> 1;
+    const bool values = unit & 1;
     if (item >= t.item[t.nb]) return;
     const int e = entry_of(t.item, t.nb, item);
     const int local = item - t.item[e], g = local / v.H, h = local - g * v.H;
     const int seq = t.seq[e], ng = t.ng[e];
     const long long ts = (long long)v.H * D;
     constexpr int C = D / 8;
-    uint16_t *ko = K + (long long)(t.row0[e] + 32 * g) * ts + h * D;
-    uint16_t *vo = V + (long long)(t.row0[e] + 32 * g) * ts + h * D;
+    uint16_t *out = (values ? V : K) + (long long)(t.row0[e] + 32 * g) * ts + h * D;
     if (g >= ng) {
         const int s0 = 32 * (g - ng), n = min(32, t.r[e] - s0);
-        const long long from = (((long long)seq * v.H + h) * v.R + s0) * D;
+        const uint16_t *from = (values ? v.resV : v.resK) + (((long long)seq * v.H + h) * v.R + s0) * D;
         for (int q = lane; q < n * C; q += 32) {
             const int row = q / C, c = q % C;
-            *(uint4 *)(ko + row * ts + c * 8) = *(const uint4 *)(v.resK + from + q * 8);
-            *(uint4 *)(vo + row * ts + c * 8) = *(const uint4 *)(v.resV + from + q * 8);
+            *(uint4 *)(out + row * ts + c * 8) = *(const uint4 *)(from + q * 8);
         }
         return;
     }
     const uint8_t *blk = page_block(v, seq, g, h, L::GB);
     const int tq = lane >> 2, cs = lane & 3;
-    uint32_t kw[L::WPL], vw[L::WPL];
+    uint32_t w[L::WPL];
 #pragma unroll
-    for (int c = 0; c < L::WPL / 4; ++c) {
-        *(uint4 *)(kw + 4 * c) = *(const uint4 *)(blk + L::KC + (c * 32 + lane) * 16);
-        *(uint4 *)(vw + 4 * c) = *(const uint4 *)(blk + L::VC + (c * 32 + lane) * 16);
-    }
+    for (int c = 0; c < L::WPL / 4; ++c)
+        *(uint4 *)(w + 4 * c) = *(const uint4 *)(blk + (values ? L::VC : L::KC) + (c * 32 + lane) * 16);
+    if (!values) {
 #pragma unroll
-    for (int u = 0; u < D / 32; ++u) {
-        uint2 zs[4];
-        *(uint4 *)zs = *(const uint4 *)(blk + L::KM + (16 * u + 4 * cs) * 8);
-        *(uint4 *)(zs + 2) = *(const uint4 *)(blk + L::KM + (16 * u + 4 * cs) * 8 + 16);
-        float2 z[4], s[4];
+        for (int u = 0; u < D / 32; ++u) {
+            uint2 zs[4];
+            *(uint4 *)zs = *(const uint4 *)(blk + L::KM + (16 * u + 4 * cs) * 8);
+            *(uint4 *)(zs + 2) = *(const uint4 *)(blk + L::KM + (16 * u + 4 * cs) * 8 + 16);
+            float2 z[4], s[4];
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            z[p] = halves(zs[p].x);
-            s[p] = halves(zs[p].y);
+            for (int p = 0; p < 4; ++p) {
+                z[p] = halves(zs[p].x);
+                s[p] = halves(zs[p].y);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t o[4];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) o[p] = decode_pair<DT>(w[j * L::KW + u / 2], 4 * (u % 2) + p, s[p], z[p]);
+                *(uint4 *)(out + (tq + 8 * j) * ts + 32 * u + 8 * cs) = *(const uint4 *)o;
+            }
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t o[4];
-#pragma unroll
-            for (int p = 0; p < 4; ++p) o[p] = decode_pair<DT>(kw[j * L::KW + u / 2], 4 * (u % 2) + p, s[p], z[p]);
-            *(uint4 *)(ko + (tq + 8 * j) * ts + 32 * u + 8 * cs) = *(const uint4 *)o;
-        }
+        return;
     }
     const uint32_t base = (uint32_t)__cvta_generic_to_shared(tile);
 #pragma unroll
@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kStoreWarps * 32)
             const float2 s = halves(sz.x), z = halves(sz.y);
             uint32_t o[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) o[c] = decode_pair<DT>(vw[p * L::KW + j / 2], 4 * (j % 2) + c, s, z);
+            for (int c = 0; c < 4; ++c) o[c] = decode_pair<DT>(w[p * L::KW + j / 2], 4 * (j % 2) + c, s, z);
             const uint32_t a = base + tile_at<D>(8 * p + (lane & 7), 4 * j + (lane >> 3));
             asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(o[0]),
                          "r"(o[1]), "r"(o[2]), "r"(o[3])
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kStoreWarps * 32)
 #pragma unroll
     for (int it = 0; it < C; ++it) {
         const int q = it * 32 + lane, row = q / C, c = q % C;
-        *(uint4 *)(vo + row * ts + c * 8) = *(const uint4 *)(tile + tile_at<D>(row, c));
+        *(uint4 *)(out + row * ts + c * 8) = *(const uint4 *)(tile + tile_at<D>(row, c));
     }
 }
 
@@ -505,7 +505,7 @@ cudaError_t quant_t(const PoolView &v, const Rows &k, const Rows &nv, const Exte
 template <int D, int DT>
 cudaError_t gather_t(const PoolView &v, const GatherTab &t, uint16_t *K, uint16_t *V, cudaStream_t st)
 {
-    const unsigned grid = ((unsigned)t.item[t.nb] + kStoreWarps - 1) / kStoreWarps;
+    const unsigned grid = (2u * t.item[t.nb] + kStoreWarps - 1) / kStoreWarps;
     pool_gather_kernel<D, DT><<<grid, kStoreWarps * 32, kStoreWarps * StoreSmem<D>::TILE, st>>>(v, t, K, V);
     return cudaGetLastError();
 }
