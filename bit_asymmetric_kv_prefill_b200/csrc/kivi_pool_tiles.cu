@@ -40,7 +40,7 @@ namespace {
 constexpr int kTileTok = 96;             // tokens per key tile
 constexpr int kKeyRows = 112;            // rows of the key tile: tokens, 3 z, 3 s, unused
 constexpr int kTileRows = 256;           // query rows per CTA
-constexpr int kSoftWarps = 8, kDecodeWarps = 12;
+constexpr int kSoftWarps = 8, kDecodeWarps = 12, kIssueWarp = 8;
 constexpr int kThreads = 24 * 32;        // three warps idle: registers move by warpgroups
 // Registers: 80 a thread at launch (61,440), then 256 x 128 + 512 x 56.
 constexpr int kSoftRegs = 128, kWorkRegs = 56;
@@ -880,7 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int k = threadIdx.x; k < 2 * kFirstBufs * D; k += kThreads) ((unsigned long long *)(sm + S::FIRST))[k] = ~0ull;
     if (threadIdx.x < 2 * kFirstBufs) ((int *)(sm + S::FLAG))[threadIdx.x] = -1;
-    if (wid == kSoftWarps + kDecodeWarps) {
+    if (wid == kIssueWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(saddr(tmem_at)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -908,15 +908,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         softmax_role<D, DT>(c, t, sm, bars, ctl, wid >> 2, blockIdx.x, w);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWorkRegs));
-        const int d = wid - kSoftWarps;
-        if (d < kDecodeWarps / 2) decode_role<D, DT, 0>(c, t, sm, bars, ctl, d >> 1, d & 1, w);
-        else if (d < kDecodeWarps) decode_role<D, DT, 1>(c, t, sm, bars, ctl, (d - kDecodeWarps / 2) >> 1, d & 1, w);
-        else if (d == kDecodeWarps) {
+        // Warps 8, 12, 16 and 20 share a scheduler: no decoding warp is among
+        // them, so that only two softmax warps delay the issue.
+        const int x = wid - kSoftWarps, d = x % 4 ? x / 4 * 3 + x % 4 - 1 : -1;
+        if (d >= kDecodeWarps / 2) decode_role<D, DT, 1>(c, t, sm, bars, ctl, (d - kDecodeWarps / 2) >> 1, d & 1, w);
+        else if (d >= 0) decode_role<D, DT, 0>(c, t, sm, bars, ctl, d >> 1, d & 1, w);
+        else if (wid == kIssueWarp) {
             // (All 512 columns are this CTA's: they start at 0.)
             if (tmem == 0) issue_role<D, DT>(c, t, sm, bars, ctl, w);
             else *stop = 1;
             __syncwarp();
-            if (*ctl.stop && lane == 0) {
+            if (*ctl.stop && elected()) {
                 // Some wait gave up: let the products issued so far finish
                 // before their memory goes away (a barrier of its own, with a
                 // limit).
@@ -933,7 +935,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_after();
     __syncwarp();
-    if (wid == kSoftWarps + kDecodeWarps) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    if (wid == kIssueWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
 constexpr int kJoinRows = 32;   // rows per block
