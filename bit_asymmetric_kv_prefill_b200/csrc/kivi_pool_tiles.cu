@@ -265,13 +265,24 @@ struct TSeg {
 
 __host__ __device__ __forceinline__ int coded_tiles(int ng) { return (ng + 2) / 3; }
 // Uncoded tokens that rows of tile rt may see (residual, then new tokens).
+// (n * group rows of output fit the memory, so they are below 2^31.)
 __host__ __device__ __forceinline__ int raw_seen(int r, int nk, int n, int group, int rt)
 {
-    const long long last = (long long)rt * kTileRows + kTileRows - 1, end = (long long)n * group - 1;
-    const int tok = (int)((last < end ? last : end) / group);
+    const unsigned last = (unsigned)rt * kTileRows + kTileRows - 1, end = (unsigned)n * group - 1;
+    const int tok = (int)((last < end ? last : end) / (unsigned)group);
     return r + (nk < tok + 1 ? nk : tok + 1);
 }
+__host__ __device__ __forceinline__ int raw_tiles(int r, int nk, int n, int group, int rt)
+{
+    return (raw_seen(r, nk, n, group, rt) + kTileTok - 1) / kTileTok;
+}
+__host__ __device__ __forceinline__ int row_tiles(int n, int group)
+{
+    return (int)(((unsigned)n * group + kTileRows - 1) / kTileRows);
+}
 
+// The segment that holds position pos: the warp's lanes count the key tiles of
+// 32 row tiles at a time.
 __device__ __forceinline__ TSeg find_segment(const AttnTab &t, const AttnCall &c, long long pos)
 {
     int lo = 0, hi = t.nb - 1;
@@ -286,11 +297,42 @@ __device__ __forceinline__ TSeg find_segment(const AttnTab &t, const AttnCall &c
     s.h = (int)AttnTab::quotient(pos - t.off[lo], per_head);
     s.base = t.off[lo] + s.h * per_head;
     s.nc = coded_tiles(t.ng[lo]);
-    for (s.rt = 0;; ++s.rt) {
-        s.nr = (raw_seen(t.r[lo], t.nk[lo], t.n[lo], c.group, s.rt) + kTileTok - 1) / kTileTok;
-        if (pos < s.base + s.nc + s.nr) return s;
-        s.base += s.nc + s.nr;
+    s.rt = s.nr = 0;
+    const int lane = threadIdx.x & 31, tiles = row_tiles(t.n[lo], c.group);
+    for (int b = 0; b < tiles; b += 32) {
+        const int nr = b + lane < tiles ? raw_tiles(t.r[lo], t.nk[lo], t.n[lo], c.group, b + lane) : 0;
+        const long long own = b + lane < tiles ? s.nc + nr : 0;
+        long long sum = own;
+        for (int k = 1; k < 32; k *= 2) {
+            const long long x = __shfl_up_sync(0xffffffffu, sum, k);
+            if (lane >= k) sum += x;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, s.base + sum > pos);
+        if (past) {
+            const int k = __ffs(past) - 1;
+            s.rt = b + k;
+            s.nr = __shfl_sync(0xffffffffu, nr, k);
+            s.base += __shfl_sync(0xffffffffu, sum - own, k);
+            break;
+        }
+        s.base += __shfl_sync(0xffffffffu, sum, 31);
     }
+    return s;
+}
+// The segment after s, which ends at pos (there is one).
+__device__ __forceinline__ void next_segment(const AttnTab &t, const AttnCall &c, long long pos, TSeg &s)
+{
+    s.base = pos;
+    if (++s.rt == row_tiles(t.n[s.e], c.group)) {
+        s.rt = 0;
+        if (++s.h == c.v.H) {
+            s.h = 0;
+            do ++s.e;
+            while (t.off[s.e + 1] == pos);   // (an entry without rows has no work)
+            s.nc = coded_tiles(t.ng[s.e]);
+        }
+    }
+    s.nr = raw_tiles(t.r[s.e], t.nk[s.e], t.n[s.e], c.group, s.rt);
 }
 
 template <int D>
@@ -306,7 +348,8 @@ struct Walk {
     __device__ __forceinline__ bool next(const AttnCall &c, const AttnTab &t)
     {
         if (pos >= hi) return false;
-        s = find_segment(t, c, pos);
+        if (pos == lo) s = find_segment(t, c, pos);
+        else next_segment(t, c, pos, s);
         const int C = s.nc + s.nr;
         i0 = (int)(pos - s.base);
         i1 = (int)(hi - s.base < C ? hi - s.base : C);
@@ -805,6 +848,7 @@ __device__ __forceinline__ void softmax_role(const AttnCall &c, const AttnTab &t
             const bool cut = __any_sync(0xffffffffu, lim < kTileTok), first = i == w.i0;
             if (coded && !cut) softmax_step<D, true, false, false>(s_t, o_t, sc, lim, first, m, l);
             else if (coded) softmax_step<D, true, true, false>(s_t, o_t, sc, lim, first, m, l);
+            else if (!cut) softmax_step<D, false, false, DT == KIVI_BF16>(s_t, o_t, sc, lim, first, m, l);
             else softmax_step<D, false, true, DT == KIVI_BF16>(s_t, o_t, sc, lim, first, m, l);
             tc_wait_st();
             tc_before();
@@ -860,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 {
     using S = TileSmem<D>;
     extern __shared__ __align__(1024) uint8_t sm[];
-    const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int wid = threadIdx.x >> 5;
     const uint32_t bars = saddr(sm) + S::BAR;
     uint32_t *tmem_at = (uint32_t *)(sm + S::BAR + kBars * 8);
     int *stop = (int *)(sm + S::BAR + kBars * 8 + 8);
@@ -1013,9 +1057,8 @@ cudaError_t launch_pool_tiles(AttnCall &c, AttnTab &t, int sms, cudaStream_t st)
     t.off[0] = 0;
     for (int e = 0; e < t.nb; ++e) {
         long long per_head = 0;
-        const int tiles = (int)(((long long)t.n[e] * c.group + kTileRows - 1) / kTileRows);
-        for (int rt = 0; rt < tiles; ++rt)
-            per_head += coded_tiles(t.ng[e]) + (raw_seen(t.r[e], t.nk[e], t.n[e], c.group, rt) + kTileTok - 1) / kTileTok;
+        for (int rt = 0; rt < row_tiles(t.n[e], c.group); ++rt)
+            per_head += coded_tiles(t.ng[e]) + raw_tiles(t.r[e], t.nk[e], t.n[e], c.group, rt);
         t.off[e + 1] = t.off[e] + per_head * c.v.H;
     }
     if (t.off[t.nb] == 0) return cudaSuccess;
