@@ -185,11 +185,11 @@ size_t pool_tiles_scratch(int D, int sms);
 cudaError_t launch_pool_tiles(AttnCall &c, AttnTab &t, int sms, cudaStream_t st);
 // Entries with more rows per kv head than this take the tiles, unless the whole
 // call is cheaper in fragments.  Measured on one SM: 24 rows against 32 tokens
-// 0.35 us, 256 rows (or any fewer) against 96 tokens 2.4 us, so two passes of 24
+// 0.35 us, 256 rows (or any fewer) against 96 tokens 2.2 us, so two passes of 24
 // rows are cheaper than tiles and three are not; and a launch of the tiles with
 // its join costs about 25 us more (one kv head pair, 100 tokens after 200: 54 us
 // against 27).
 constexpr int kTileMinRows = 48;
-constexpr double kRowsUs = 0.35, kTileUs = 2.4, kTilesFixedUs = 25.0;
+constexpr double kRowsUs = 0.35, kTileUs = 2.2, kTilesFixedUs = 25.0;
 
 }  // namespace kivi
