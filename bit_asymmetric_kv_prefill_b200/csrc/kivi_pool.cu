@@ -435,6 +435,7 @@ kivi_status kivi_pool_attn(kivi_pool *p, const int *seqs, const int *n_new, int 
     if (total == 0) return KIVI_OK;
     if (total > (1LL << 30) / (H_q / p->cfg.H_kv)) return KIVI_ERR_UNSUPPORTED;
     if (!good_rows(q) || (k && (!good_rows(k) || !good_rows(v))) || !out || !aligned16(out)) return KIVI_ERR_ARG;
+    if (out == q->data || (k && (out == k->data || out == v->data))) return KIVI_ERR_ARG;
     return guarded([&]() -> kivi_status {
         // Sequences of few rows and of many go to kernels of their own.
         const std::unique_ptr<AttnTab> few(new AttnTab), many(new AttnTab);
@@ -507,11 +508,11 @@ kivi_status kivi_pool_gather(kivi_pool *p, const int *seqs, int n, void *K, void
             t->r[i] = s.r;
             row += (long long)s.pages.size() * p->cfg.R + s.r;
             items += (long long)(t->ng[i] + (s.r + 31) / 32) * p->cfg.H_kv;
-            if (row > (1LL << 30) || items > (1LL << 30)) return KIVI_ERR_UNSUPPORTED;
+            if (row > (1LL << 30) || items > (1LL << 29)) return KIVI_ERR_UNSUPPORTED;
             t->item[i + 1] = (int)items;
         }
         if (row == 0) return KIVI_OK;
-        if (!K || !V || !aligned16(K) || !aligned16(V)) return KIVI_ERR_ARG;
+        if (!K || !V || K == V || !aligned16(K) || !aligned16(V)) return KIVI_ERR_ARG;
         return cuda_status(launch_pool_gather(p->view, *t, (uint16_t *)K, (uint16_t *)V, (cudaStream_t)stream));
     });
 }

@@ -239,6 +239,8 @@ extern "C" kivi_status kivi_rope(const kivi_rope_tensor *tensors, int n_tensors,
               && ((t.x_token | t.x_head | t.y_token | t.y_head) & 7) == 0;
     }
     if (tokens == 0) return KIVI_OK;
+    // One tensor's output must not be the other's output or input.
+    if (n_tensors == 2 && (p.t[0].y == p.t[1].y || p.t[0].y == p.t[1].x || p.t[1].y == p.t[0].x)) return KIVI_ERR_ARG;
     if ((double)tokens * p.heads * D > 5e11) return KIVI_ERR_UNSUPPORTED;   // keeps the grid below 2^31 blocks
     p.heads0 = tensors[0].heads;
     p.tokens = tokens;

@@ -30,8 +30,10 @@ class KiviPool:
         cfg = PoolConfig(H_kv, D, G, R, _dtype_code(dtype), pages, sequences, T_max, None, 0)
         self._workspace = workspace
         if workspace is not None:
-            if not workspace.is_cuda:
-                raise ValueError("workspace must be a CUDA tensor")
+            if not workspace.is_cuda or workspace.get_device() != torch.cuda.current_device():
+                raise ValueError("workspace must be a tensor on the current CUDA device")
+            if not workspace.is_contiguous():
+                raise ValueError("workspace must be contiguous")
             cfg.workspace = workspace.data_ptr()
             cfg.workspace_bytes = workspace.numel() * workspace.element_size()
         self.device = torch.device("cuda", torch.cuda.current_device())

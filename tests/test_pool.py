@@ -303,6 +303,30 @@ def test_a_workspace_holds_everything():
     assert e.value.code == 1
 
 
+@pytest.mark.gpu
+def test_results_over_inputs_and_strided_workspaces_are_refused():
+    H, D, R = 2, 64, 32
+    pool = _pool(H, D, torch.float16, R, pages=8, sequences=2, T_max=256)
+    K, V = _tokens(40, H, D, torch.float16, 3)
+    a, = pool.open()
+    pool.extend([a], K, V, [40])
+    q, k, v = K[:2].clone(), K[2:4].clone(), V[:2].clone()
+    for out in (q, k, v):
+        with pytest.raises(kivi.KiviError) as e:
+            pool.attend([a], q, k, v, [2], out=out)
+        assert e.value.code == 1
+    both = torch.empty_like(K)
+    with pytest.raises(kivi.KiviError) as e:
+        pool.gather([a], K=both, V=both)
+    assert e.value.code == 1
+    n = kivi.KiviPool.required_bytes(8, 2, H, D, dtype=torch.float16, T_max=1024)
+    with pytest.raises(ValueError):
+        kivi.KiviPool(8, 2, H, D, dtype=torch.float16, T_max=1024,
+                      workspace=torch.zeros((n, 2), dtype=torch.uint8, device="cuda")[:, 0])
+    with pytest.raises(ValueError):
+        pool.extend([1 << 40], K[:1], V[:1], [1])   # not a 32-bit integer
+
+
 # ---- attention (GPU) ------------------------------------------------------------------
 def _case(H, g, D, dtype, R, T, n, seed, with_new=True, pages=None):
     """A pool with sequences of T[i] tokens, and n[i] new rows each, checked against the 64-bit form."""

@@ -94,6 +94,15 @@ def test_rope_rejects_bad_arguments(t, a, code):
                                 a["rot"], 0, a["scale"], 0, 0, None) == code
 
 
+@pytest.mark.parametrize("x1,y1", [(2048, 512), (512, 4096), (2048, 256)])
+def test_rope_rejects_outputs_over_the_other_tensor(x1, y1):
+    """x, y of the first tensor are 256 and 512: the second's output is the first's, its input is the first's output,
+    or its output is the first's input."""
+    t = [dict(_T), dict(_T, x=x1, y=y1)]
+    arr = (kivi.RopeTensor * 2)(*[kivi.RopeTensor(*[x[f] for f, _ in kivi.RopeTensor._fields_]) for x in t])
+    assert kivi.lib().kivi_rope(arr, 2, kivi.KIVI_BF16, 8, 128, 256, 0, 512, 128, 0, 1.0, 0, 0, None) == 1
+
+
 def test_rope_of_no_tokens_launches_nothing():
     arr = (kivi.RopeTensor * 1)(kivi.RopeTensor(None, None, 4, 512, 128, 512, 128))
     assert kivi.lib().kivi_rope(arr, 1, kivi.KIVI_F16, 0, 128, None, 0, 512, 128, 0, 1.0, 0, 0, None) == 0
