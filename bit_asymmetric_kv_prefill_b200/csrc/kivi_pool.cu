@@ -155,13 +155,13 @@ std::vector<int> free_slots(const kivi_pool *p, int n)
     return s;
 }
 
-// Table and move launches take kPoolMaxPairs entries each.
+// Table and move launches take kTabPairs entries each.
 cudaError_t launch_pairs(const kivi_pool *p, const std::vector<int> &a, const std::vector<int> &b, bool moves,
                          cudaStream_t st)
 {
     const std::unique_ptr<PairTab> t(new PairTab);
-    for (size_t i = 0; i < a.size(); i += kPoolMaxPairs) {
-        t->n = (int)std::min(a.size() - i, (size_t)kPoolMaxPairs);
+    for (size_t i = 0; i < a.size(); i += kTabPairs) {
+        t->n = (int)std::min(a.size() - i, (size_t)kTabPairs);
         std::copy_n(a.begin() + i, t->n, t->a);
         std::copy_n(b.begin() + i, t->n, t->b);
         const cudaError_t e = moves ? launch_pool_move(p->view, *t, st) : launch_pool_table(p->view, *t, st);
@@ -336,7 +336,6 @@ kivi_status kivi_pool_extend(kivi_pool *p, const int *seqs, const int *n_new, in
 {
     if (!p || n < 0 || (n > 0 && (!seqs || !n_new))) return KIVI_ERR_ARG;
     if (!on_pool_device(p)) return KIVI_ERR_ARG;
-    if (n > kPoolMaxBatch) return KIVI_ERR_UNSUPPORTED;
     kivi_status st = check_seqs(p, seqs, n, false);
     if (st != KIVI_OK) return st;
     long long total = 0;
@@ -348,30 +347,34 @@ kivi_status kivi_pool_extend(kivi_pool *p, const int *seqs, const int *n_new, in
     if (total > (1LL << 30)) return KIVI_ERR_UNSUPPORTED;
     return guarded([&]() -> kivi_status {
         const int R = p->cfg.R, H = p->cfg.H_kv;
-        const std::unique_ptr<ExtendTab> t(new ExtendTab);
-        t->nb = n;
-        t->item[0] = t->kept[0] = 0;
-        std::vector<int> fresh, at, ids;   // new pages, their table entries
+        const std::unique_ptr<ExtendTab[]> tabs(new ExtendTab[(n + kTabSeqs - 1) / kTabSeqs]);
+        std::vector<int> fresh, at, grows(n), left(n);   // new pages, their table entries; pages and residual of each
         long long need = 0, items = 0;
         int row = 0;
         for (int i = 0; i < n; ++i) {
+            ExtendTab *t = &tabs[i / kTabSeqs];
+            const int x = i % kTabSeqs;
+            if (x == 0) t->item[0] = t->kept[0] = items = 0;
+            t->nb = x + 1;
             const PoolSeq &s = p->seqs[seqs[i]];
             const long long n_q = (long long)s.pages.size() * R, len = n_q + s.r + n_new[i];
             if (len > p->cfg.T_max) return KIVI_ERR_CAPACITY;
             const long long coded = std::max(n_q, coded_tokens(len, R));
             const int grown = (int)((coded - n_q) / R);
-            t->seq[i] = seqs[i];
-            t->row0[i] = row;
-            t->r[i] = s.r;
-            t->g0[i] = (int)(n_q / kG);
+            grows[i] = grown;
+            t->seq[x] = seqs[i];
+            t->row0[x] = row;
+            t->r[x] = s.r;
+            t->g0[x] = (int)(n_q / kG);
             // Kept: everything behind the coded tokens.  A flush takes the
             // whole residual with it, so what is kept then is new rows only.
-            t->from[i] = grown ? (int)(coded - n_q - s.r) : 0;
-            t->slot0[i] = grown ? 0 : s.r;
+            t->from[x] = grown ? (int)(coded - n_q - s.r) : 0;
+            t->slot0[x] = grown ? 0 : s.r;
+            left[i] = t->slot0[x] + n_new[i] - t->from[x];
             items += (long long)grown * (R / kG) * H;
             if (items > (1LL << 29)) return KIVI_ERR_UNSUPPORTED;
-            t->item[i + 1] = (int)items;
-            t->kept[i + 1] = t->kept[i] + n_new[i] - t->from[i];
+            t->item[x + 1] = (int)items;
+            t->kept[x + 1] = t->kept[x] + n_new[i] - t->from[x];
             row += n_new[i];
             need += grown;
             for (int j = 0; j < grown; ++j) at.push_back(seqs[i] * p->view.max_pages + (int)s.pages.size() + j);
@@ -379,7 +382,7 @@ kivi_status kivi_pool_extend(kivi_pool *p, const int *seqs, const int *n_new, in
         if (need > (long long)p->free_pages.size()) return KIVI_ERR_CAPACITY;
         for (int i = 0; i < n; ++i) {   // every allocation before anything changes
             PoolSeq &s = p->seqs[seqs[i]];
-            s.pages.reserve(s.pages.size() + (t->item[i + 1] - t->item[i]) / (R / kG * H));
+            s.pages.reserve(s.pages.size() + grows[i]);
         }
         fresh.reserve(need);
         const std::unique_ptr<PairTab> tab(new PairTab);
@@ -389,16 +392,19 @@ kivi_status kivi_pool_extend(kivi_pool *p, const int *seqs, const int *n_new, in
         }
         cudaError_t e = cudaSuccess;
         const cudaStream_t cs = (cudaStream_t)stream;
-        for (size_t i = 0; i < at.size() && e == cudaSuccess; i += kPoolMaxPairs) {
-            tab->n = (int)std::min(at.size() - i, (size_t)kPoolMaxPairs);
+        for (size_t i = 0; i < at.size() && e == cudaSuccess; i += kTabPairs) {
+            tab->n = (int)std::min(at.size() - i, (size_t)kTabPairs);
             std::copy_n(at.begin() + i, tab->n, tab->a);
             std::copy_n(fresh.begin() + i, tab->n, tab->b);
             e = launch_pool_table(p->view, *tab, cs);
         }
-        if (total > 0 && e == cudaSuccess) e = launch_pool_quant(p->view, rows_of(k), rows_of(v), *t, cs);
-        // The residual is overwritten by a launch of its own: the quantizer's
-        // warps read it.
-        if (total > 0 && e == cudaSuccess) e = launch_pool_keep(p->view, rows_of(k), rows_of(v), *t, cs);
+        for (int i = 0; total > 0 && i < n && e == cudaSuccess; i += kTabSeqs) {
+            const ExtendTab &t = tabs[i / kTabSeqs];
+            e = launch_pool_quant(p->view, rows_of(k), rows_of(v), t, cs);
+            // The residual is overwritten by a launch of its own: the
+            // quantizer's warps read it.
+            if (e == cudaSuccess) e = launch_pool_keep(p->view, rows_of(k), rows_of(v), t, cs);
+        }
         if (e != cudaSuccess) {
             for (const int page : fresh) p->free_pages.push(page);
             return KIVI_ERR_CUDA;
@@ -406,12 +412,11 @@ kivi_status kivi_pool_extend(kivi_pool *p, const int *seqs, const int *n_new, in
         size_t j = 0;
         for (int i = 0; i < n; ++i) {
             PoolSeq &s = p->seqs[seqs[i]];
-            const int grown = (t->item[i + 1] - t->item[i]) / (R / kG * H);
-            for (int q = 0; q < grown; ++q, ++j) {
+            for (int q = 0; q < grows[i]; ++q, ++j) {
                 s.pages.push_back(fresh[j]);
                 p->refs[fresh[j]] = 1;
             }
-            s.r = grown ? n_new[i] - t->from[i] : s.r + n_new[i];
+            s.r = left[i];
         }
         return KIVI_OK;
     });
@@ -424,7 +429,7 @@ kivi_status kivi_pool_attn(kivi_pool *p, const int *seqs, const int *n_new, int 
     if (!on_pool_device(p)) return KIVI_ERR_ARG;
     if (H_q < 1 || H_q % p->cfg.H_kv != 0) return KIVI_ERR_ARG;
     if ((k == nullptr) != (v == nullptr)) return KIVI_ERR_ARG;
-    if (n > kPoolMaxBatch || H_q > 65536) return KIVI_ERR_UNSUPPORTED;
+    if (H_q > 65536) return KIVI_ERR_UNSUPPORTED;
     const kivi_status st = check_seqs(p, seqs, n, true);
     if (st != KIVI_OK) return st;
     long long total = 0;
@@ -452,21 +457,6 @@ kivi_status kivi_pool_attn(kivi_pool *p, const int *seqs, const int *n_new, int 
         }
         const bool tiles = p->path == 0 ? tiles_us < rows_us : p->path == 2;
         const long long fewest = p->path == 2 ? 0 : kTileMinRows;
-        int row = 0;
-        for (int i = 0; i < n; ++i) {
-            const PoolSeq &s = p->seqs[seqs[i]];
-            if (n_new[i] == 0) continue;
-            const bool sees = k || s.r > 0;
-            AttnTab &t = tiles && sees && (long long)n_new[i] * group > fewest ? *many : *few;
-            const int e = t.nb++;
-            t.seq[e] = seqs[i];
-            t.row0[e] = row;
-            t.n[e] = n_new[i];
-            t.nk[e] = k ? n_new[i] : 0;
-            t.ng[e] = (int)s.pages.size() * gpp;
-            t.r[e] = s.r;
-            row += n_new[i];
-        }
         AttnCall c;
         c.v = p->view;
         c.q = rows_of(q);
@@ -482,9 +472,31 @@ kivi_status kivi_pool_attn(kivi_pool *p, const int *seqs, const int *n_new, int 
         c.err = p->err;
         c.expire = p->expire;
         // One after the other on the stream: they share the scratch.
-        cudaError_t e = many->nb ? launch_pool_tiles(c, *many, p->sms, (cudaStream_t)stream) : cudaSuccess;
-        if (e == cudaSuccess && few->nb) e = launch_pool_rows(c, *few, p->sms, (cudaStream_t)stream);
-        return cuda_status(e);
+        cudaError_t err = cudaSuccess;
+        auto launch = [&](AttnTab &t) {
+            if (t.nb && err == cudaSuccess)
+                err = (&t == many.get() ? launch_pool_tiles : launch_pool_rows)(c, t, p->sms, (cudaStream_t)stream);
+            t.nb = 0;
+        };
+        int row = 0;
+        for (int i = 0; i < n; ++i) {
+            const PoolSeq &s = p->seqs[seqs[i]];
+            if (n_new[i] == 0) continue;
+            const bool sees = k || s.r > 0;
+            AttnTab &t = tiles && sees && (long long)n_new[i] * group > fewest ? *many : *few;
+            if (t.nb == kTabSeqs) launch(t);
+            const int e = t.nb++;
+            t.seq[e] = seqs[i];
+            t.row0[e] = row;
+            t.n[e] = n_new[i];
+            t.nk[e] = k ? n_new[i] : 0;
+            t.ng[e] = (int)s.pages.size() * gpp;
+            t.r[e] = s.r;
+            row += n_new[i];
+        }
+        launch(*many);
+        launch(*few);
+        return cuda_status(err);
     });
 }
 
@@ -492,28 +504,32 @@ kivi_status kivi_pool_gather(kivi_pool *p, const int *seqs, int n, void *K, void
 {
     if (!p || n < 0 || (n > 0 && !seqs)) return KIVI_ERR_ARG;
     if (!on_pool_device(p)) return KIVI_ERR_ARG;
-    if (n > kPoolMaxBatch) return KIVI_ERR_UNSUPPORTED;
     const kivi_status st = check_seqs(p, seqs, n, true);
     if (st != KIVI_OK) return st;
     return guarded([&]() -> kivi_status {
-        const std::unique_ptr<GatherTab> t(new GatherTab);
-        t->nb = n;
-        t->item[0] = 0;
+        const std::unique_ptr<GatherTab[]> tabs(new GatherTab[(n + kTabSeqs - 1) / kTabSeqs]);
         long long row = 0, items = 0;
         for (int i = 0; i < n; ++i) {
+            GatherTab *t = &tabs[i / kTabSeqs];
+            const int x = i % kTabSeqs;
+            if (x == 0) t->item[0] = items = 0;
+            t->nb = x + 1;
             const PoolSeq &s = p->seqs[seqs[i]];
-            t->seq[i] = seqs[i];
-            t->row0[i] = (int)row;
-            t->ng[i] = (int)(s.pages.size() * (p->cfg.R / kG));
-            t->r[i] = s.r;
+            t->seq[x] = seqs[i];
+            t->row0[x] = (int)row;
+            t->ng[x] = (int)(s.pages.size() * (p->cfg.R / kG));
+            t->r[x] = s.r;
             row += (long long)s.pages.size() * p->cfg.R + s.r;
-            items += (long long)(t->ng[i] + (s.r + 31) / 32) * p->cfg.H_kv;
+            items += (long long)(t->ng[x] + (s.r + 31) / 32) * p->cfg.H_kv;
             if (row > (1LL << 30) || items > (1LL << 29)) return KIVI_ERR_UNSUPPORTED;
-            t->item[i + 1] = (int)items;
+            t->item[x + 1] = (int)items;
         }
         if (row == 0) return KIVI_OK;
         if (!K || !V || K == V || !aligned16(K) || !aligned16(V)) return KIVI_ERR_ARG;
-        return cuda_status(launch_pool_gather(p->view, *t, (uint16_t *)K, (uint16_t *)V, (cudaStream_t)stream));
+        cudaError_t e = cudaSuccess;
+        for (int i = 0; i < n && e == cudaSuccess; i += kTabSeqs)
+            e = launch_pool_gather(p->view, tabs[i / kTabSeqs], (uint16_t *)K, (uint16_t *)V, (cudaStream_t)stream);
+        return cuda_status(e);
     });
 }
 
@@ -522,7 +538,6 @@ static kivi_status branch(kivi_pool *p, const int *src, int n, int *dst, bool ow
 {
     if (!p || n < 0 || (n > 0 && (!src || !dst))) return KIVI_ERR_ARG;
     if (!on_pool_device(p)) return KIVI_ERR_ARG;
-    if (n > kPoolMaxBatch) return KIVI_ERR_UNSUPPORTED;
     const kivi_status st = check_seqs(p, src, n, true);
     if (st != KIVI_OK) return st;
     if (n == 0) return KIVI_OK;
@@ -530,14 +545,9 @@ static kivi_status branch(kivi_pool *p, const int *src, int n, int *dst, bool ow
         const std::vector<int> slots = free_slots(p, n);
         if ((int)slots.size() != n) return KIVI_ERR_CAPACITY;
         const std::unique_ptr<ForkTab> t(new ForkTab);
-        t->n = n;
         size_t need = 0;
         for (int i = 0; i < n; ++i) {
             const PoolSeq &s = p->seqs[src[i]];
-            t->src[i] = src[i];
-            t->dst[i] = slots[i];
-            t->np[i] = own ? 0 : (int)s.pages.size();
-            t->r[i] = s.r;
             if (own) need += s.pages.size();
             p->seqs[slots[i]].pages.reserve(s.pages.size());
         }
@@ -558,9 +568,20 @@ static kivi_status branch(kivi_pool *p, const int *src, int n, int *dst, bool ow
                 }
             }
         const cudaStream_t cs = (cudaStream_t)stream;
-        cudaError_t e = launch_pool_fork(p->view, *t, cs);
-        for (size_t i = 0; i < need && e == cudaSuccess; i += kPoolMaxPairs) {
-            tab->n = (int)std::min(need - i, (size_t)kPoolMaxPairs);
+        cudaError_t e = cudaSuccess;
+        for (int i = 0; i < n && e == cudaSuccess; i += kTabSeqs) {
+            t->n = std::min(n - i, kTabSeqs);
+            for (int x = 0; x < t->n; ++x) {
+                const PoolSeq &s = p->seqs[src[i + x]];
+                t->src[x] = src[i + x];
+                t->dst[x] = slots[i + x];
+                t->np[x] = own ? 0 : (int)s.pages.size();
+                t->r[x] = s.r;
+            }
+            e = launch_pool_fork(p->view, *t, cs);
+        }
+        for (size_t i = 0; i < need && e == cudaSuccess; i += kTabPairs) {
+            tab->n = (int)std::min(need - i, (size_t)kTabPairs);
             std::copy_n(at.begin() + i, tab->n, tab->a);
             std::copy_n(to.begin() + i, tab->n, tab->b);
             e = launch_pool_table(p->view, *tab, cs);

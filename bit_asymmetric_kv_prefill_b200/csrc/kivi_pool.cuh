@@ -47,8 +47,10 @@ __host__ __device__ inline int page_vm_offset(int p, int cs, int j)
     return (((p * (D / 64) + j / 2) * 4 + cs) * 2 + j % 2) * 8;
 }
 
-constexpr int kPoolMaxBatch = 512;    // sequences per call
-constexpr int kPoolMaxPairs = 1024;   // entries of one table or copy launch
+// Entries of one launch (calls of more sequences take several launches): the
+// tables travel as kernel parameters, and 16 KB of them cost a launch 1.5 us.
+constexpr int kTabSeqs = 96;
+constexpr int kTabPairs = 448;
 
 // The pool's device memory, as kernels see it.
 struct PoolView {
@@ -71,31 +73,31 @@ struct Rows {
 // then keeps `keep` new rows from `from` in residual slots slot0...
 struct ExtendTab {
     int nb;
-    int seq[kPoolMaxBatch], row0[kPoolMaxBatch], r[kPoolMaxBatch], g0[kPoolMaxBatch];
-    int from[kPoolMaxBatch], slot0[kPoolMaxBatch];
-    int item[kPoolMaxBatch + 1];   // first (group, head) item of each entry
-    int kept[kPoolMaxBatch + 1];   // first kept row of each entry
+    int seq[kTabSeqs], row0[kTabSeqs], r[kTabSeqs], g0[kTabSeqs];
+    int from[kTabSeqs], slot0[kTabSeqs];
+    int item[kTabSeqs + 1];   // first (group, head) item of each entry
+    int kept[kTabSeqs + 1];   // first kept row of each entry
 };
 
 // kivi_pool_gather: entry e reads ng groups and r residual tokens into rows
 // row0.. of the output; items are (32 tokens, head).
 struct GatherTab {
     int nb;
-    int seq[kPoolMaxBatch], row0[kPoolMaxBatch], ng[kPoolMaxBatch], r[kPoolMaxBatch];
-    int item[kPoolMaxBatch + 1];
+    int seq[kTabSeqs], row0[kTabSeqs], ng[kTabSeqs], r[kTabSeqs];
+    int item[kTabSeqs + 1];
 };
 
 // Pairs of integers: (table index, page), (page from, page to).
 struct PairTab {
     int n;
-    int a[kPoolMaxPairs], b[kPoolMaxPairs];
+    int a[kTabPairs], b[kTabPairs];
 };
 
 // kivi_pool_fork, kivi_pool_copy: np table entries and r residual tokens of
 // sequence src go to sequence dst.
 struct ForkTab {
     int n;
-    int src[kPoolMaxBatch], dst[kPoolMaxBatch], np[kPoolMaxBatch], r[kPoolMaxBatch];
+    int src[kTabSeqs], dst[kTabSeqs], np[kTabSeqs], r[kTabSeqs];
 };
 
 // kivi_pool_attn: entry e has n new rows from row0 and sees ng cached groups,
@@ -103,9 +105,9 @@ struct ForkTab {
 // starts in the flattened split (see kivi_pool_rows.cu).
 struct AttnTab {
     int nb;
-    int seq[kPoolMaxBatch], row0[kPoolMaxBatch], n[kPoolMaxBatch], nk[kPoolMaxBatch], ng[kPoolMaxBatch],
-        r[kPoolMaxBatch];
-    long long off[kPoolMaxBatch + 1];
+    int seq[kTabSeqs], row0[kTabSeqs], n[kTabSeqs], nk[kTabSeqs], ng[kTabSeqs],
+        r[kTabSeqs];
+    long long off[kTabSeqs + 1];
     // The split: part w of `parts` is positions [at(w), at(w + 1)), at(w) =
     // floor(w * total / parts) with total = quo * parts + rem.
     long long quo;

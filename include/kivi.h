@@ -413,9 +413,8 @@ KIVI_API kivi_status kivi_rope_frequencies(int rot, double theta, const kivi_rop
  *     and the pool is unchanged; KIVI_ERR_CUDA leaves the contents of the
  *     sequences of the call undefined.  Calls that launch need the pool's
  *     device current (else KIVI_ERR_ARG).
- *   - At most 512 sequences per call (else KIVI_ERR_UNSUPPORTED); n = 0 does
- *     nothing.  No call allocates device memory except kivi_pool_create
- *     without a workspace.  A pool is not thread-safe.
+ *   - n = 0 does nothing.  No call allocates device memory except
+ *     kivi_pool_create without a workspace.  A pool is not thread-safe.
  *   - A value group whose zero + 3*scale passes 65504 (values near the fp16
  *     limit) may decode to infinity in kivi_pool_attn.
  *

@@ -472,6 +472,35 @@ def test_strided_rows_repeats_and_rows_left_alone(n, form):
 
 @pytest.mark.gpu
 @FORMS
+def test_calls_of_many_sequences(form):
+    """More sequences than the entries of one launch (96): every call takes several, and none loses its place."""
+    H, g, D, R, B = 1, 2, 64, 32, 230
+    T, n = [i % 75 for i in range(B)], [(7 * i) % 5 for i in range(B)]
+    pool, seqs, K, V, q, k, v = _case(H, g, D, "fp16", R, T, n, seed=33, pages=700)
+    pool.debug(path=form)
+    out = pool.attend(seqs, q, k, v, n)
+    _verify(pool, out, T, n, K, V, q, k, v, R)
+    pool.free(seqs[200:])
+    seqs = seqs[:200]
+    pool.extend(seqs, k[:sum(n[:200])], v[:sum(n[:200])], n[:200])
+    more = pool.fork(seqs[:30])
+    more += pool.copy(seqs[:1])
+    gK, gV = pool.gather(seqs + more)
+    at = h = x = 0
+    for i, s in enumerate(seqs):
+        Ki, Vi = torch.cat([K[h:h + T[i]], k[x:x + n[i]]]), torch.cat([V[h:h + T[i]], v[x:x + n[i]]])
+        if i % 19 == 0:
+            _same_store(pool, s, Ki, Vi)
+        if i < 30:
+            _same_store(pool, more[i], Ki, Vi)
+        Kc, Vc, _ = ref.cached(Ki, Vi, R)
+        rows = slice(at, at + T[i] + n[i])
+        assert torch.equal(gK[rows], Kc.float().to(gK.dtype)) and torch.equal(gV[rows], Vc.float().to(gV.dtype))
+        at, h, x = at + T[i] + n[i], h + T[i], x + n[i]
+
+
+@pytest.mark.gpu
+@FORMS
 def test_attention_on_streams_and_in_graphs(form):
     """Repeats are bit-equal; a captured call replays on new inputs; two graphs that share the scratch, replayed one
     after the other, keep their results."""
