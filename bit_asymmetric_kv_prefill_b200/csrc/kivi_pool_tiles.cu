@@ -936,14 +936,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int k = threadIdx.x; k < 2 * kFirstBufs * D; k += kThreads) ((unsigned long long *)(sm + S::FIRST))[k] = ~0ull;
     if (threadIdx.x < 2 * kFirstBufs) ((int *)(sm + S::FLAG))[threadIdx.x] = -1;
+    // Everything above touches no global memory and runs while the launch
+    // before this one finishes.  TMEM is taken after the wait: a kernel before
+    // this one that takes its own late would otherwise wait for this one's,
+    // and this one for its end.
+    griddep_wait();
+    griddep_launch();
     if (wid == kIssueWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(saddr(tmem_at)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    // Everything above touches no global memory and runs while the launch
-    // before this one finishes.
-    griddep_wait();
-    griddep_launch();
     if (threadIdx.x == 0) {
         c.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);   // (softmax_role may set it)
         if (c.expire) {
