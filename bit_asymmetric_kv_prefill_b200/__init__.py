@@ -219,7 +219,22 @@ class _on_device:
 
 def _stream_ptr(stream) -> int:
     # The current stream's handle without a Stream object around it (3 us).
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    device = torch._C._cuda_getDevice()
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    if stream.device_index != device:
+        raise ValueError(f"stream must be a stream of cuda:{device}, got one of cuda:{stream.device_index}")
+    return stream.cuda_stream
+
+
+def _empty(shape, dtype, device: int, stream):
+    """A new tensor for a call on ``stream``: its memory belongs to the stream
+    that writes it, so that work on the current one that still uses a freed
+    tensor there is not overtaken."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 class KiviCache:

@@ -143,6 +143,22 @@ bool good_rows(const kivi_rows *r)
 {
     return r && r->data && aligned16(r->data) && r->token_stride % 8 == 0 && r->head_stride % 8 == 0;
 }
+// Does a row of r (n tokens of `heads` heads; the space between heads counted
+// in) share bytes with [p, p + len)?
+bool rows_touch(const kivi_rows *r, long long n, int heads, int D, const void *p, long long len)
+{
+    const long long hs = r->head_stride * 2 * (heads - 1);
+    long long ts = r->token_stride * 2, at = (long long)(uintptr_t)r->data + std::min(hs, 0LL);
+    const long long wide = std::max(hs, -hs) + 2LL * D, o = (long long)(uintptr_t)p;
+    if (ts < 0) {
+        at += (n - 1) * ts;
+        ts = -ts;
+    }
+    if (o + len <= at || o >= at + (n - 1) * ts + wide) return false;
+    if (ts <= wide || o < at) return true;
+    const long long past = (o - at) % ts;   // from the start of the row before p
+    return past < wide || past + len > ts;
+}
 Rows rows_of(const kivi_rows *r) { return Rows{(const uint16_t *)r->data, r->token_stride, r->head_stride}; }
 
 // n sequence slots that are not open (empty: too few).
@@ -440,7 +456,11 @@ kivi_status kivi_pool_attn(kivi_pool *p, const int *seqs, const int *n_new, int 
     if (total == 0) return KIVI_OK;
     if (total > (1LL << 30) / (H_q / p->cfg.H_kv)) return KIVI_ERR_UNSUPPORTED;
     if (!good_rows(q) || (k && (!good_rows(k) || !good_rows(v))) || !out || !aligned16(out)) return KIVI_ERR_ARG;
-    if (out == q->data || (k && (out == k->data || out == v->data))) return KIVI_ERR_ARG;
+    const long long written = total * H_q * p->cfg.D * 2;
+    if (rows_touch(q, total, H_q, p->cfg.D, out, written)
+        || (k && (rows_touch(k, total, p->cfg.H_kv, p->cfg.D, out, written)
+                  || rows_touch(v, total, p->cfg.H_kv, p->cfg.D, out, written))))
+        return KIVI_ERR_ARG;
     return guarded([&]() -> kivi_status {
         // Sequences of few rows and of many go to kernels of their own.
         const std::unique_ptr<AttnTab> few(new AttnTab), many(new AttnTab);
@@ -525,7 +545,9 @@ kivi_status kivi_pool_gather(kivi_pool *p, const int *seqs, int n, void *K, void
             t->item[x + 1] = (int)items;
         }
         if (row == 0) return KIVI_OK;
-        if (!K || !V || K == V || !aligned16(K) || !aligned16(V)) return KIVI_ERR_ARG;
+        if (!K || !V || !aligned16(K) || !aligned16(V)) return KIVI_ERR_ARG;
+        const long long apart = (long long)((intptr_t)V - (intptr_t)K), bytes = row * p->cfg.H_kv * p->cfg.D * 2;
+        if (apart < bytes && -apart < bytes) return KIVI_ERR_ARG;   // one's rows over the other's
         cudaError_t e = cudaSuccess;
         for (int i = 0; i < n && e == cudaSuccess; i += kTabSeqs)
             e = launch_pool_gather(p->view, tabs[i / kTabSeqs], (uint16_t *)K, (uint16_t *)V, (cudaStream_t)stream);

@@ -7,7 +7,7 @@ from array import array
 
 import torch
 
-from . import PoolConfig, PoolRows, _check, _dtype_code, _on_device, _stream_ptr, lib
+from . import PoolConfig, PoolRows, _check, _dtype_code, _empty, _on_device, _stream_ptr, lib
 
 
 def _ints(values, what):
@@ -132,7 +132,7 @@ class KiviPool:
             kr = ctypes.byref(self._rows(K, N, self.H_kv, "K"))
             vr = ctypes.byref(self._rows(V, N, self.H_kv, "V"))
         if out is None:
-            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            out = _empty(q.shape, self.dtype, self.device.index, stream)
         elif (out.dtype != self.dtype or out.shape != (N, H_q, self.D) or not out.is_contiguous()
               or out.device != self.device):
             raise ValueError(f"out must be a contiguous {self.dtype} {(N, H_q, self.D)} tensor on {self.device}")
@@ -149,9 +149,9 @@ class KiviPool:
         _check(lib().kivi_pool_tokens(self._h, ids, n, tokens), "kivi_pool_tokens")
         N = sum(tokens)
         if K is None:
-            K = torch.empty((N, self.H_kv, self.D), dtype=self.dtype, device=self.device)
+            K = _empty((N, self.H_kv, self.D), self.dtype, self.device.index, stream)
         if V is None:
-            V = torch.empty_like(K, memory_format=torch.contiguous_format)
+            V = _empty((N, self.H_kv, self.D), self.dtype, self.device.index, stream)
         for name, t in (("K", K), ("V", V)):
             self._rows(t, N, self.H_kv, name)
             if not t.is_contiguous():

@@ -1,6 +1,7 @@
 """The pool of cache pages: refusals on the CPU; codes, forks, copies,
 compaction and attention on the GPU against 64-bit forms."""
 import ctypes
+import types
 
 import numpy as np
 import pytest
@@ -325,6 +326,61 @@ def test_results_over_inputs_and_strided_workspaces_are_refused():
                       workspace=torch.zeros((n, 2), dtype=torch.uint8, device="cuda")[:, 0])
     with pytest.raises(ValueError):
         pool.extend([1 << 40], K[:1], V[:1], [1])   # not a 32-bit integer
+
+
+@pytest.mark.gpu
+def test_results_partly_over_inputs_are_refused_and_gaps_between_rows_are_fine():
+    H, D, R = 2, 64, 32
+    pool = _pool(H, D, torch.float16, R, pages=8, sequences=2, T_max=256)
+    K, V = _tokens(40, H, D, torch.float16, 3)
+    a, = pool.open()
+    pool.extend([a], K, V, [40])
+    wide = torch.randn((3, 12, D), device="cuda").half()   # rows of 12 heads: q, then room for a result of two rows
+    q, k, v = wide[:2, :4], K[:2].clone(), V[:2].clone()
+    want = pool.attend([a], q, k, v, [2])
+    line = wide.view(36, D)
+    for first in (1, 5, 11, 12):   # over the end of row 0, the start of row 1, from before it, all of it
+        with pytest.raises(kivi.KiviError) as e:
+            pool.attend([a], q, k, v, [2], out=line[first:first + 8].view(2, 4, D))
+        assert e.value.code == 1
+    both = torch.cat([k.view(-1, D), v.view(-1, D), k.view(-1, D)])   # over the end of k, over the start of v
+    for x in ((both[:4].view(2, H, D), v), (k, both[8:12].view(2, H, D))):
+        with pytest.raises(kivi.KiviError) as e:
+            pool.attend([a], q, *x, [2], out=both[3:11].view(2, 4, D))
+        assert e.value.code == 1
+    assert torch.equal(pool.attend([a], q, k, v, [2], out=wide[0, 4:].view(2, 4, D)), want)
+    both = torch.empty((41, H, D), device="cuda", dtype=torch.float16)
+    for x, y in ((both[:40], both[1:]), (both[1:], both[:40])):
+        with pytest.raises(kivi.KiviError) as e:
+            pool.gather([a], K=x, V=y)
+        assert e.value.code == 1
+
+
+@pytest.mark.gpu
+def test_new_results_belong_to_the_stream_that_writes_them():
+    H, D, R = 2, 64, 32
+    pool = _pool(H, D, torch.float16, R, pages=8, sequences=2, T_max=256)
+    K, V = _tokens(40, H, D, torch.float16, 3)
+    a, = pool.open()
+    pool.extend([a], K, V, [40])
+    q, f = torch.randn((2, 4, D), device="cuda").half(), kivi.rope_frequencies(D)[0]
+    pos = torch.arange(2, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for call in (lambda: (pool.attend([a], q, K[:2], V[:2], [2], stream=s),), lambda: pool.gather([a], stream=s),
+                 lambda: kivi.rope(q, K[:2], pos, f, stream=s)):
+        got = call()
+        at = {x.data_ptr() for x in got}
+        shapes = [x.shape for x in got]
+        s.synchronize()
+        del got
+        # The memory is free again, for its own stream only.
+        new = [torch.empty(x, dtype=torch.float16, device="cuda") for x in shapes]
+        assert at.isdisjoint(x.data_ptr() for x in new)
+    other = types.SimpleNamespace(cuda_stream=0, device_index=torch.cuda.current_device() + 1)
+    with pytest.raises(ValueError):
+        pool.extend([a], K[:1], V[:1], [1], stream=other)
+    assert pool.length(a) == (32, 8)
 
 
 # ---- attention (GPU) ------------------------------------------------------------------
