@@ -119,6 +119,12 @@ __device__ __forceinline__ uint32_t pack2(float a, float b)
     }
     return r;
 }
+template <int DT>
+__device__ __forceinline__ float2 unpack2(uint32_t p)
+{
+    if constexpr (DT == KIVI_BF16) return make_float2(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u));
+    else return __half22float2(as_h2(p));
+}
 __device__ __forceinline__ float ex2(float x)
 {
     float r;
@@ -194,7 +200,7 @@ __device__ __forceinline__ int chunk_at(int t, int c)
 
 // Running softmax of the lane's rows 8a + 2cs, + 1 of every tile a, and their
 // outputs: fragment f holds channels 16f + tq (elements 0, 1) and + 8 (2, 3).
-// m is the reference of p: p = 2^(score - m).  l is the lane's own sum.
+// m is the reference of p: p = 2^(score - m).  l is the lane's own share of the sum.
 template <int D, int NT>
 struct State {
     float o[NT][D / 16][4];
@@ -255,7 +261,6 @@ __device__ __forceinline__ void softmax_step(State<D, NT> &st, float (*oz)[4], f
             for (int f = 0; f < 2; ++f) {
                 S[a][f][x] = ex2(fmaf(S[a][f][x], sc[a][x], -m));
                 S[a][f][2 + x] = ex2(fmaf(S[a][f][2 + x], sc[a][x], -m));
-                st.l[a][x] += S[a][f][x] + S[a][f][2 + x];
             }
         }
 }
@@ -343,7 +348,7 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
                 for (int x = 0; x < 2; ++x) sc[a][x] *= pow2(-__shfl_sync(0xffffffffu, k, 4 * (2 * cs + x)));
             }
         }
-        float oz[NT][4];   // sum p z of channel group tq (tq < NJ)
+        float oz[NT][4];   // sum p z of channel group tq (tq < NJ), sum p (tq = NJ)
 #pragma unroll
         for (int a = 0; a < NT; ++a) oz[a][0] = oz[a][1] = oz[a][2] = oz[a][3] = 0.0f;
         const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm);
@@ -462,12 +467,17 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
                         pt[a][2 * f + 1] = transpose8(pack2<KIVI_F16>(S[a][f][2], S[a][f][3]));
                     }
                 {
-                    // Row tq of A: the zeros of channel group tq (rows past
-                    // them hold some group's again and are not used), row
-                    // 8 + tq its scales, which c - 1 leaves out.
+                    // Row tq of A: the zeros of channel group tq, row 8 + tq
+                    // its scales, which c - 1 leaves out.  Row NJ holds ones:
+                    // the sum of the row's probabilities, as rounded, so that
+                    // where one token has most of the weight its rounding
+                    // cancels.  (The other rows are not used.)
                     uint2 z[4];
 #pragma unroll
-                    for (int p = 0; p < 4; ++p) z[p] = *(const uint2 *)(blk + L::VM + page_vm_offset<D>(p, cs, tq % NJ));
+                    for (int p = 0; p < 4; ++p) {
+                        z[p] = *(const uint2 *)(blk + L::VM + page_vm_offset<D>(p, cs, tq % NJ));
+                        if (tq == NJ) z[p].y = 0x3c003c00u;
+                    }
 #pragma unroll
                     for (int a = 0; a < NT; ++a) {
                         mma<KIVI_F16>(oz[a], z[0].y, z[0].x, z[1].y, z[1].x, pt[a][0], pt[a][1]);
@@ -530,6 +540,8 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
         // Outputs in their own units: take out 4^k 2^-24, add the zeros' part.
 #pragma unroll
         for (int a = 0; a < NT; ++a) {
+            st.l[a][0] = tq == NJ ? oz[a][0] : 0.0f;
+            st.l[a][1] = tq == NJ ? oz[a][1] : 0.0f;
             if (kLessOne) {
                 oz[a][0] += oz[a][2];
                 oz[a][1] += oz[a][3];
@@ -659,10 +671,15 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
 #pragma unroll
             for (int a = 0; a < NT; ++a)
 #pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                    pt[a][2 * f] = transpose8(pack2<DT>(S[a][f][0], S[a][f][1]));
-                    pt[a][2 * f + 1] = transpose8(pack2<DT>(S[a][f][2], S[a][f][3]));
-                }
+                for (int f = 0; f < 2; ++f)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint32_t p = pack2<DT>(S[a][f][2 * x], S[a][f][2 * x + 1]);
+                        const float2 q = unpack2<DT>(p);   // the sum takes them as rounded, too
+                        st.l[a][0] += q.x;
+                        st.l[a][1] += q.y;
+                        pt[a][2 * f + x] = transpose8(p);
+                    }
             asm volatile("cp.async.wait_group 1;" ::: "memory");   // the values
             __syncwarp();
             if (masked) {

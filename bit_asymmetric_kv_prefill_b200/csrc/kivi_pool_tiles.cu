@@ -725,8 +725,10 @@ __device__ __forceinline__ void row_exp(const uint32_t (&x)[32], uint32_t p_t, u
             u = c0 + 2 * k < lim ? u : 0.0f;
             v = c0 + 2 * k + 1 < lim ? v : 0.0f;
         }
-        sum = add2(sum, pair(u, v));
         p[k] = pack2<BF16 ? KIVI_BF16 : KIVI_F16>(u, v);
+        // bf16 ones as rounded: where one token has most of the weight, its
+        // rounding (as large as the result's own) cancels.
+        sum = add2(sum, BF16 ? pair(__uint_as_float(p[k] << 16), __uint_as_float(p[k] & 0xffff0000u)) : pair(u, v));
     }
     tc_st16(p_t, p);
 }
