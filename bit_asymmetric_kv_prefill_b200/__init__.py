@@ -227,14 +227,14 @@ def _stream_ptr(stream) -> int:
     return stream.cuda_stream
 
 
-def _empty(shape, dtype, device: int, stream):
-    """A new tensor for a call on ``stream``: its memory belongs to the stream
-    that writes it, so that work on the current one that still uses a freed
-    tensor there is not overtaken."""
+def _empty_like(x, stream):
+    """A new contiguous tensor like ``x`` for a call on ``stream``: its memory
+    belongs to the stream that writes it, so that work on the current one that
+    still uses a freed tensor there is not overtaken."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
 class KiviCache:

@@ -2,12 +2,13 @@
 grow, branch and go at their own pace, and attention of their new tokens."""
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from array import array
 
 import torch
 
-from . import PoolConfig, PoolRows, _check, _dtype_code, _empty, _on_device, _stream_ptr, lib
+from . import PoolConfig, PoolRows, _check, _dtype_code, _empty_like, _on_device, _stream_ptr, lib
 
 
 def _ints(values, what):
@@ -132,7 +133,7 @@ class KiviPool:
             kr = ctypes.byref(self._rows(K, N, self.H_kv, "K"))
             vr = ctypes.byref(self._rows(V, N, self.H_kv, "V"))
         if out is None:
-            out = _empty(q.shape, self.dtype, self.device.index, stream)
+            out = _empty_like(q, stream)
         elif (out.dtype != self.dtype or out.shape != (N, H_q, self.D) or not out.is_contiguous()
               or out.device != self.device):
             raise ValueError(f"out must be a contiguous {self.dtype} {(N, H_q, self.D)} tensor on {self.device}")
@@ -149,9 +150,10 @@ class KiviPool:
         _check(lib().kivi_pool_tokens(self._h, ids, n, tokens), "kivi_pool_tokens")
         N = sum(tokens)
         if K is None:
-            K = _empty((N, self.H_kv, self.D), self.dtype, self.device.index, stream)
+            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+                K = torch.empty((N, self.H_kv, self.D), dtype=self.dtype, device=self.device)
         if V is None:
-            V = _empty((N, self.H_kv, self.D), self.dtype, self.device.index, stream)
+            V = _empty_like(K, stream)
         for name, t in (("K", K), ("V", V)):
             self._rows(t, N, self.H_kv, name)
             if not t.is_contiguous():

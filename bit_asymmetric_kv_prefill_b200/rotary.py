@@ -6,7 +6,7 @@ import ctypes
 
 import torch
 
-from . import RopeScaling, RopeTensor, _check, _dtype_code, _empty, _on_device, _stream_ptr, lib
+from . import RopeScaling, RopeTensor, _check, _dtype_code, _empty_like, _on_device, _stream_ptr, lib
 
 PLAIN, LINEAR, BASE, YARN, BANDS = "plain", "linear", "base", "yarn", "bands"
 _KINDS = {PLAIN: 0, LINEAR: 1, BASE: 2, YARN: 3, BANDS: 4}
@@ -67,14 +67,14 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_f
             or not inv_freq.is_contiguous():
         raise ValueError(f"inv_freq must be contiguous float32 [{rot // 2}] on {q.device}")
     if q_out is None:
-        q_out = _empty(shape, dtype, device, stream)
+        q_out = _empty_like(q, stream)
     if k is None:
         t, n = (RopeTensor * 1)(_side(q, q_out, shape, dtype, device, "q")), 1
     else:
         if not isinstance(k, torch.Tensor) or k.dim() != 3:
             raise ValueError("k must be a CUDA tensor [tokens, kv heads, D]")
         if k_out is None:
-            k_out = _empty(k.shape, k.dtype, device, stream)
+            k_out = _empty_like(k, stream)
         t, n = (RopeTensor * 2)(_side(q, q_out, shape, dtype, device, "q"),
                                 _side(k, k_out, (N, k.shape[1], D), dtype, device, "k")), 2
     with _on_device(device):
