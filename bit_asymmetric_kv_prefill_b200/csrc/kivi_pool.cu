@@ -512,6 +512,10 @@ kivi_status kivi_pool_attn(kivi_pool *p, const int *seqs, const int *n_new, int 
             t.nk[e] = k ? n_new[i] : 0;
             t.ng[e] = (int)s.pages.size() * gpp;
             t.r[e] = s.r;
+            // A page has one place in every list that holds it, behind the
+            // same pages: fork is what shares them, and shares whole lists.
+            t.same[e] = e > 0 && t.ng[e] > 0 && t.ng[e] == t.ng[e - 1] && t.row0[e] == t.row0[e - 1] + t.n[e - 1]
+                        && s.pages.back() == p->seqs[t.seq[e - 1]].pages.back();
             row += n_new[i];
         }
         launch(*many);

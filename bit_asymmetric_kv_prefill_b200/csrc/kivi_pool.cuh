@@ -103,10 +103,18 @@ struct ForkTab {
 // kivi_pool_attn: entry e has n new rows from row0 and sees ng cached groups,
 // r residual tokens and nk of its new keys.  off: where each entry's work
 // starts in the flattened split (see kivi_pool_rows.cu).
+//
+// Few rows: entries that follow one another and hold the same pages (forks)
+// may be taken as one unit, whose rows share the pass over the pages.  Unit u
+// is entries first[u] .. first[u + 1] - 1, has toks[u] new rows and raw[u]
+// blocks of 32 uncoded tokens; off counts units then.
 struct AttnTab {
     int nb;
     int seq[kTabSeqs], row0[kTabSeqs], n[kTabSeqs], nk[kTabSeqs], ng[kTabSeqs],
         r[kTabSeqs];
+    int units;
+    int first[kTabSeqs + 1], toks[kTabSeqs], raw[kTabSeqs];
+    bool same[kTabSeqs];   // entry e holds the pages of entry e - 1, and its rows follow (host only)
     long long off[kTabSeqs + 1];
     // The split: part w of `parts` is positions [at(w), at(w + 1)), at(w) =
     // floor(w * total / parts) with total = quo * parts + rem.
@@ -128,9 +136,8 @@ struct AttnTab {
         if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
         return a / b;
     }
-    __host__ void split(long long most)
+    __host__ void split(long long total, long long most)
     {
-        const long long total = off[nb];
         parts = (int)(most < total ? most : total);
         quo = parts > 0 ? total / parts : 0;
         rem = parts > 0 ? (int)(total % parts) : 0;

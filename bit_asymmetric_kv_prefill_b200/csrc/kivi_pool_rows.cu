@@ -154,14 +154,14 @@ __device__ __forceinline__ uint32_t code_tiny(uint32_t w, uint32_t w10, int i)
 }
 
 struct Seg {
-    int e, rt, h;          // entry, row tile, kv head
+    int e, rt, h;          // unit, row tile, kv head
     long long base, C;     // where the segment starts, its weight
 };
 
 // The segment that contains position pos of the split.
 __device__ __forceinline__ Seg find_segment(const AttnTab &t, const AttnCall &c, long long pos)
 {
-    int lo = 0, hi = t.nb - 1;
+    int lo = 0, hi = t.units - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (t.off[mid] <= pos) lo = mid;
@@ -169,8 +169,7 @@ __device__ __forceinline__ Seg find_segment(const AttnTab &t, const AttnCall &c,
     }
     Seg s;
     s.e = lo;
-    const int raw = (t.r[lo] + 31) / 32 + (t.nk[lo] + 31) / 32;
-    s.C = max(1, t.ng[lo] + raw * kRawWeight);
+    s.C = max(1, t.ng[t.first[lo]] + t.raw[lo] * kRawWeight);
     const int si = (int)AttnTab::quotient(pos - t.off[lo], s.C);
     s.base = t.off[lo] + si * s.C;
     s.rt = si / c.v.H;
@@ -181,7 +180,7 @@ __device__ __forceinline__ Seg find_segment(const AttnTab &t, const AttnCall &c,
 template <int D>
 struct RowsSmem {
     static constexpr int RING = kRowStages * 24 * D;   // also the staging of 32 uncoded tokens
-    static constexpr int FIRST = RING;                 // per channel: first new token whose value is not finite
+    static constexpr int FIRST = RING;                 // per channel: first token of a block whose value is not finite
     static constexpr int PER_WARP = RING + D * 4;
     static constexpr int BYTES = kRowWarps * PER_WARP;
     static_assert(2 * 32 * D * 2 <= RING, "uncoded keys and values are staged in the ring");
@@ -265,8 +264,8 @@ __device__ __forceinline__ void softmax_step(State<D, NT> &st, float (*oz)[4], f
         }
 }
 
-// One segment's items [i0, i1): groups below ng, then blocks of 32 residual
-// tokens, then blocks of 32 new tokens.
+// One segment's items [i0, i1): groups below ng, then, entry by entry of the
+// unit, blocks of 32 residual tokens and blocks of 32 new tokens.
 template <int D, int DT, int NT>
 __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, const Seg &sg, int i0, int i1,
                                           uint8_t *sm, State<D, NT> &st)
@@ -274,7 +273,7 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
     using L = PageLayout<D>;
     constexpr int KU = D / 32, NF = D / 16, KW = L::KW, NJ = L::NJ;
     const int lane = threadIdx.x & 31, tq = lane >> 2, cs = lane & 3;
-    const int e = sg.e, n = t.n[e], ng = t.ng[e], r_res = t.r[e], nk = t.nk[e], seq = t.seq[e];
+    const int e0 = t.first[sg.e], n = t.toks[sg.e], ng = t.ng[e0], tok_row0 = t.row0[e0];
     const PoolView &v = c.v;
     const int row0 = 8 * NT * sg.rt;
 #pragma unroll
@@ -293,7 +292,7 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
 #pragma unroll
         for (int a = 0; a < NT; ++a) {
             const int row = row0 + 8 * a + tq, tok = row / c.group;
-            const uint16_t *p = c.q.p + (long long)(t.row0[e] + tok) * c.q.ts
+            const uint16_t *p = c.q.p + (long long)(tok_row0 + tok) * c.q.ts
                                 + (long long)(sg.h * c.group + row - tok * c.group) * c.q.hs;
 #pragma unroll
             for (int u = 0; u < KU; ++u)
@@ -353,7 +352,7 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
         for (int a = 0; a < NT; ++a) oz[a][0] = oz[a][1] = oz[a][2] = oz[a][3] = 0.0f;
         const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm);
         const long long head_bytes = (long long)v.gpp * L::GB;
-        const int *table = v.table + (long long)seq * v.max_pages;
+        const int *table = v.table + (long long)t.seq[e0] * v.max_pages;
         // The next group to fetch: page by page.
         int fetch = i0, in_page = i0 % v.gpp;
         int page_i = i0 / v.gpp, next_page = table[page_i];
@@ -559,7 +558,6 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
     }
 
     // ---- uncoded tokens, 32 at a time ----
-    const int nres = (r_res + 31) / 32;
     if (i1 > ng) {
         load_q();
         float sc[NT][2];
@@ -572,29 +570,39 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
                 tok[a][x] = (row0 + 8 * a + 2 * cs + x) / c.group;
                 if (tok[a][x] >= n) tok[a][x] = -1;
             }
-        // The last new token that a row of the tile sees, the first row's token.
-        const int last_row = min(row0 + 8 * NT - 1, n * c.group - 1);
-        const int last_tok = min(nk - 1, last_row / c.group), first_tok = row0 / c.group;
+        const bool shared = t.first[sg.e + 1] - e0 > 1;   // (then all rows are in one tile)
         // Blocks go through the ring, keys in its first half and values in its
         // second; the next block's keys follow as soon as this one's are used.
         struct Block {
             const uint16_t *k, *v;
             long long kts, vts;
-            int t0, cnt;
+            int t0, cnt, tok0, n;   // first token, tokens; the unit's rows (in tokens) that see them
             bool is_new;
         };
+        int e = e0, e_tok = 0, e_it = ng;   // the block's entry, its first row and item
         auto block = [&](int it) {
+            int nres, items;
+            for (;;) {
+                nres = (t.r[e] + 31) / 32;
+                items = nres + (t.nk[e] + 31) / 32;
+                if (it < e_it + items || e + 1 >= t.first[sg.e + 1]) break;
+                e_it += items;
+                e_tok += t.n[e];
+                ++e;
+            }
             Block x;
-            x.is_new = it - ng >= nres;
-            x.t0 = 32 * (x.is_new ? it - ng - nres : it - ng);
-            x.cnt = min(32, x.is_new ? nk - x.t0 : r_res - x.t0);
+            x.is_new = it - e_it >= nres;
+            x.t0 = 32 * (x.is_new ? it - e_it - nres : it - e_it);
+            x.cnt = min(32, x.is_new ? t.nk[e] - x.t0 : t.r[e] - x.t0);
+            x.tok0 = e_tok;
+            x.n = t.n[e];
             if (x.is_new) {
                 x.k = c.k.p + (long long)(t.row0[e] + x.t0) * c.k.ts + sg.h * c.k.hs;
                 x.v = c.nv.p + (long long)(t.row0[e] + x.t0) * c.nv.ts + sg.h * c.nv.hs;
                 x.kts = c.k.ts;
                 x.vts = c.nv.ts;
             } else {
-                const long long at = (((long long)seq * v.H + sg.h) * v.R + x.t0) * D;
+                const long long at = (((long long)t.seq[e] * v.H + sg.h) * v.R + x.t0) * D;
                 x.k = v.resK + at;
                 x.v = v.resV + at;
                 x.kts = x.vts = D;
@@ -615,8 +623,9 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
                              : "memory");
             }
         };
-        // Blocks of new tokens behind the tile's last are not seen.
-        const int end = min(i1, ng + nres + (last_tok + 32) / 32);
+        // Blocks of new tokens behind the tile's last row are not seen.
+        const int first_tok = row0 / c.group, last_tok = min(t.nk[e0] - 1, min(row0 + 8 * NT - 1, n * c.group - 1) / c.group);
+        const int end = shared ? i1 : min(i1, ng + (t.r[e0] + 31) / 32 + (last_tok + 32) / 32);
         int it = max(i0, ng);
         Block nx = block(it);
         if (it < end) {
@@ -629,7 +638,7 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
         for (; it < end; ++it) {
             const Block cur = nx;
             const int t0 = cur.t0, cnt = cur.cnt;
-            const bool is_new = cur.is_new, more = it + 1 < end;
+            const bool more = it + 1 < end;
             asm volatile("cp.async.wait_group 1;" ::: "memory");   // the keys
             __syncwarp();
             float S[NT][2][4];
@@ -655,17 +664,22 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
                 fetch(stage_k, nx.k, nx.kts, nx.cnt);
             }
             cp_async_commit();
-            const bool masked = is_new && t0 + cnt - 1 > first_tok;
+            const bool masked = shared || (cur.is_new && t0 + cnt - 1 > first_tok);
+            int lim[NT][2];   // tokens of the block that the lane's rows see
+#pragma unroll
+            for (int a = 0; a < NT; ++a)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int own = tok[a][x] - cur.tok0;   // the row's new token in its entry
+                    lim[a][x] = own < 0 || own >= cur.n ? 0 : cur.is_new ? min(cnt, own - t0 + 1) : cnt;
+                }
 #pragma unroll
             for (int a = 0; a < NT; ++a)
 #pragma unroll
                 for (int f = 0; f < 2; ++f)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int col = 16 * f + tq + 8 * (x >> 1);
-                        const bool seen = col < cnt && (!is_new || t0 + col <= tok[a][x & 1]);
-                        if (!seen) S[a][f][x] = -INFINITY;
-                    }
+                    for (int x = 0; x < 4; ++x)
+                        if (16 * f + tq + 8 * (x >> 1) >= lim[a][x & 1]) S[a][f][x] = -INFINITY;
             softmax_step<D, NT>(st, nullptr, S, sc, (float)E);
             uint32_t pt[NT][4];
 #pragma unroll
@@ -686,7 +700,8 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
                 // Some rows do not see some of these tokens: their probability
                 // is 0, and 0 times a value that is not finite would still
                 // spoil the row.  Such values leave the product; a row that
-                // sees one becomes NaN in that channel at the end.
+                // sees one becomes NaN in that channel.
+                bool any = false;
                 constexpr uint32_t kExp = DT == KIVI_BF16 ? 0x7f80u : 0x7c00u;
 #pragma unroll 1
                 for (int k = 0; k < D / 8; ++k) {
@@ -701,9 +716,22 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
                     if (bad)
                         for (int z = 0; z < 8; ++z)
                             if ((x[z] & kExp) == kExp) {
-                                atomicMin(first + ch * 8 + z, t0 + row);
+                                atomicMin(first + ch * 8 + z, row);
                                 x[z] = 0;
+                                any = true;
                             }
+                }
+                if (__any_sync(0xffffffffu, any)) {
+                    __syncwarp();
+#pragma unroll
+                    for (int a = 0; a < NT; ++a)
+#pragma unroll
+                        for (int f = 0; f < NF; ++f)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                if (lim[a][x & 1] > first[16 * f + tq + 8 * (x >> 1)]) st.o[a][f][x] = NAN;
+                    __syncwarp();
+                    for (int d = lane; d < D; d += 32) first[d] = 0x7fffffff;
                 }
                 __syncwarp();
             }
@@ -728,13 +756,6 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
         }
         cp_async_wait_all();
         __syncwarp();
-#pragma unroll
-        for (int a = 0; a < NT; ++a)
-#pragma unroll
-            for (int f = 0; f < NF; ++f)
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    if (tok[a][x & 1] >= first[16 * f + tq + 8 * (x >> 1)]) st.o[a][f][x] = NAN;
     }
 #pragma unroll
     for (int a = 0; a < NT; ++a)
@@ -754,9 +775,9 @@ __device__ __forceinline__ void store_rows(const AttnCall &c, const AttnTab &t, 
     const int cs = threadIdx.x & 3;
     const uint32_t x = transpose8(pack2<DT>(o[0] * f0, o[1] * f1)), y = transpose8(pack2<DT>(o[2] * f0, o[3] * f1));
     const int tok = row / c.group;
-    if (tok >= t.n[e]) return;
+    if (tok >= t.toks[e]) return;
     uint16_t *p =
-        c.out + ((long long)(t.row0[e] + tok) * c.H_q + h * c.group + row - tok * c.group) * c.v.D + d + 2 * cs;
+        c.out + ((long long)(t.row0[t.first[e]] + tok) * c.H_q + h * c.group + row - tok * c.group) * c.v.D + d + 2 * cs;
     *(uint32_t *)p = x;
     *(uint32_t *)(p + 8) = y;
 }
@@ -815,8 +836,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas(NT))
 #pragma unroll 1
     while (pos < hi) {
         const Seg sg = find_segment(t, c, pos);
-        const int e = sg.e, ng = t.ng[e];
-        const int items = ng + (t.r[e] + 31) / 32 + (t.nk[e] + 31) / 32;
+        const int e = sg.e, ng = t.ng[t.first[e]], items = ng + t.raw[e];
         // Items whose start lies in the warp's range.
         auto first_item = [&](long long rel) {
             if (rel <= ng) return (int)rel;
@@ -847,7 +867,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas(NT))
             float *part = c.part + (long long)(2 * w + (starts ? 1 : 0)) * kPartFloats<D, NT>;
 #pragma unroll
             for (int a = 0; a < NT; ++a) {
-                if ((8 * NT * sg.rt + 8 * a) / c.group >= t.n[e]) break;
+                if ((8 * NT * sg.rt + 8 * a) / c.group >= t.toks[e]) break;
                 float *pa = part + a * (8 * D + 16);
 #pragma unroll
                 for (int f = 0; f < D / 16; ++f)
@@ -873,7 +893,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas(NT))
 #pragma unroll 1
                     for (int a = 0; a < NT; ++a) {
                         const int row = 8 * NT * sg.rt + 8 * a;
-                        if (row / c.group >= t.n[e]) break;
+                        if (row / c.group >= t.toks[e]) break;
                         Joined<D / 16> s;
                         s.clear();
 #pragma unroll 1
@@ -929,7 +949,7 @@ __global__ void __launch_bounds__(1024) pool_join_kernel(const __grid_constant__
 #pragma unroll 1
         for (int a = 0; a < NT; ++a) {
             const int row = 8 * NT * j.z + 8 * a;
-            if (row / c.group >= t.n[e]) break;
+            if (row / c.group >= t.toks[e]) break;
             Joined<1> s;
             s.clear();
 #pragma unroll 1
@@ -1003,34 +1023,65 @@ size_t pool_rows_scratch(int D, int sms)
     return most;
 }
 
+// What an entry's (or unit's) groups cost with 1, 2 or 3 tiles a warp, measured
+// (24 x 8K tokens, 8 kv heads; 8, 16 and 24 rows): the decoding is shared, the
+// products are not, and two and three tiles run on 8 warps an SM, not 12.
+constexpr double kTileCost[kMaxTiles + 1] = {0.0, 1.0, 1.7, 2.5};
+
+// Units of the entries, their rows and tokens, and the split's positions.
+// share: entries of the same pages go together as long as their rows fit one
+// warp.  Returns the cost; nt: the tiles per warp.
+double plan_units(const AttnCall &c, AttnTab &t, bool share, int &nt)
+{
+    t.units = 0;
+    long long most = 0;
+    for (int e = 0; e < t.nb; ++e) {
+        const bool joins = share && e > 0 && t.same[e]
+                           && ((long long)t.toks[t.units - 1] + t.n[e]) * c.group <= 8 * kMaxTiles;
+        if (!joins) {
+            t.first[t.units] = e;
+            t.toks[t.units] = t.raw[t.units] = 0;
+            ++t.units;
+        }
+        const int u = t.units - 1;
+        t.toks[u] += t.n[e];
+        t.raw[u] += (t.r[e] + 31) / 32 + (t.nk[e] + 31) / 32;
+        most = std::max(most, (long long)t.toks[u]);
+    }
+    t.first[t.units] = t.nb;
+    // As many tiles per warp as the most rows of a unit need: the decoded
+    // fragments serve all of them.
+    most = (most * c.group + 7) / 8;
+    nt = most < kMaxTiles ? (int)most : kMaxTiles;
+    if (nt == 0) return 0.0;
+    t.off[0] = 0;
+    for (int u = 0; u < t.units; ++u) {
+        const long long C = t.ng[t.first[u]] + (long long)t.raw[u] * kRawWeight;
+        const long long tiles = ((long long)t.toks[u] * c.group + 8 * nt - 1) / (8 * nt);
+        t.off[u + 1] = t.off[u] + tiles * c.v.H * (C > 0 ? C : 1);
+    }
+    return kTileCost[nt] * (double)t.off[t.units];
+}
+
 // Fills the split (t.off and its parts) and launches.
 cudaError_t launch_pool_rows(AttnCall &c, AttnTab &t, int sms, cudaStream_t st)
 {
-    // As many tiles per warp as the most rows of an entry need: the decoded
-    // fragments serve all of them.
-    long long most = 0;
-    for (int e = 0; e < t.nb; ++e) most = most > t.n[e] ? most : t.n[e];
-    most = (most * c.group + 7) / 8;
-    const int nt = most < kMaxTiles ? (int)most : kMaxTiles;
+    int nt = 0;
+    const double shared = plan_units(c, t, true, nt);
+    if (t.units < t.nb && plan_units(c, t, false, nt) > shared) plan_units(c, t, true, nt);
     if (nt == 0) return cudaSuccess;
-    t.off[0] = 0;
-    for (int e = 0; e < t.nb; ++e) {
-        const long long C = t.ng[e] + (long long)((t.r[e] + 31) / 32 + (t.nk[e] + 31) / 32) * kRawWeight;
-        const long long tiles = ((long long)t.n[e] * c.group + 8 * nt - 1) / (8 * nt);
-        t.off[e + 1] = t.off[e] + tiles * c.v.H * (C > 0 ? C : 1);
-    }
-    if (t.off[t.nb] == 0) return cudaSuccess;
+    if (t.off[t.units] == 0) return cudaSuccess;
     // At least kPartItems items per part: a partial result costs as much.
-    t.split(std::max(1LL, std::min(split_warps(sms, nt), t.off[t.nb] / kPartItems)));
+    t.split(t.off[t.units], std::max(1LL, std::min(split_warps(sms, nt), t.off[t.units] / kPartItems)));
     // A small call whose segments lie in a few parts each is all latency, and
     // the last warp of a segment joins it (2 x 256 tokens: 12.4 us a call
     // against 14.5); else a launch of its own does, with 32 warps per segment
     // (24 x 8K tokens: 61 us against 65 with the last warp, 8 x 4K of 32 heads
     // 52 against 57, 4000 tokens alone 19 against 99).
     long long longest = 0;
-    for (int e = 0; e < t.nb; ++e) {
-        const long long tiles = ((long long)t.n[e] * c.group + 8 * nt - 1) / (8 * nt);
-        if (tiles > 0) longest = std::max(longest, (t.off[e + 1] - t.off[e]) / (tiles * c.v.H));
+    for (int u = 0; u < t.units; ++u) {
+        const long long tiles = ((long long)t.toks[u] * c.group + 8 * nt - 1) / (8 * nt);
+        if (tiles > 0) longest = std::max(longest, (t.off[u + 1] - t.off[u]) / (tiles * c.v.H));
     }
     const bool here = t.parts == 1 || (t.quo <= kPartItems && longest / t.quo < kJoinHere);
     if (c.v.D == 64) return c.v.dtype ? rows_n<64, 1>(c, t, nt, here, st) : rows_n<64, 0>(c, t, nt, here, st);

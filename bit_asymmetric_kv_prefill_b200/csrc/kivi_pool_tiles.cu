@@ -1078,7 +1078,7 @@ cudaError_t launch_pool_tiles(AttnCall &c, AttnTab &t, int sms, cudaStream_t st)
         t.off[e + 1] = t.off[e] + per_head * c.v.H;
     }
     if (t.off[t.nb] == 0) return cudaSuccess;
-    t.split(sms);
+    t.split(t.off[t.nb], sms);
     if (c.v.D == 64) return c.v.dtype ? tiles_t<64, 1>(c, t, st) : tiles_t<64, 0>(c, t, st);
     return c.v.dtype ? tiles_t<128, 1>(c, t, st) : tiles_t<128, 0>(c, t, st);
 }

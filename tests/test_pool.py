@@ -631,3 +631,72 @@ def test_a_serving_run():
     step([seqs[0], a, seqs[2], b], [1, 1, 64, 1], 30)
     for s in (seqs[0], seqs[2], a, b):
         _same_store(pool, s, *hist[s])
+
+
+@pytest.mark.gpu
+@FORMS
+@pytest.mark.parametrize("H,g,D,dtype,R,T,forks,tail,n", [
+    # tokens before the forks, forks of each, tokens that each fork takes before it attends, new tokens of each
+    (2, 4, 128, "bf16", 128, [700], [4], [0, 1, 30, 60], [1, 1, 1, 1]),
+    (8, 4, 128, "bf16", 128, [4000, 3000], [4, 4], [0, 0, 0, 0, 1, 2, 3, 100], [1] * 8),
+    (3, 1, 64, "fp16", 32, [333, 64, 5], [9, 30, 3], [k % 3 for k in range(42)], [1] * 42),
+    (2, 2, 128, "fp16", 64, [1000], [6], [0, 5, 63, 64, 1, 0], [3, 1, 0, 2, 5, 13]),
+    (1, 8, 64, "bf16", 96, [500], [5], [0] * 5, [1, 1, 1, 2, 1]),
+])
+def test_forks_that_attend_together(H, g, D, dtype, R, T, forks, tail, n, form):
+    """Forks hold the same pages and tokens of their own behind them; some have grown a page."""
+    dt = DT[dtype]
+    pool = _pool(H, D, dt, R, pages=200, sequences=64)
+    roots = pool.open(len(T))
+    K, V = _tokens(sum(T), H, D, dt, 8)
+    pool.extend(roots, K, V, T)
+    of = [i for i, f in enumerate(forks) for _ in range(f)]
+    twigs = pool.fork([roots[i] for i in of])
+    Kt, Vt = _tokens(sum(tail), H, D, dt, 9)
+    pool.extend(twigs, Kt, Vt, tail)
+    k, v = _tokens(sum(n), H, D, dt, 10)
+    q = torch.randn((sum(n), H * g, D), generator=torch.Generator(device="cuda").manual_seed(11), device="cuda").to(dt)
+    pool.debug(path=form)
+    for new in (True, False):
+        out = pool.attend(twigs, q, *((k, v) if new else (None, None)), n)
+        for i, x in enumerate(of):
+            h, a, b = sum(T[:x]), sum(tail[:i]), sum(n[:i])
+            rows = slice(b, b + n[i])
+            Kc, Vc, n_q = ref.cached(torch.cat([K[h:h + T[x]], Kt[a:a + tail[i]]]),
+                                     torch.cat([V[h:h + T[x]], Vt[a:a + tail[i]]]), R)
+            if n[i]:
+                ref.check(out[rows], *ref.attention(q[rows], Kc, Vc, n_q, *((k[rows], v[rows]) if new else ())), f"fork {i}")
+    assert pool.device_status() == 0
+
+
+@pytest.mark.gpu
+@FORMS
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_values_that_are_not_finite_stay_with_their_fork(dtype, form):
+    """An infinite value in one fork's residual or new token: its rows become NaN there, the others keep every bit."""
+    H, g, D, R, dt = 2, 4, 128, 64, DT[dtype]
+    pool = _pool(H, D, dt, R)
+    a, = pool.open()
+    K, V = _tokens(300, H, D, dt, 1)
+    pool.extend([a], K, V, [300])
+    pool.debug(path=form)
+    k, v = _tokens(4, H, D, dt, 2)
+    q = torch.randn((4, H * g, D), generator=torch.Generator(device="cuda").manual_seed(3), device="cuda").to(dt)
+    kt, vt = _tokens(4, H, D, dt, 4)
+
+    def run(vt, v):
+        twigs = pool.fork([a] * 4)
+        pool.extend(twigs, kt, vt, [1] * 4)
+        out = pool.attend(twigs, q, k, v, [1] * 4)
+        pool.free(twigs)
+        return out.view(4, H, g, D)
+
+    want = run(vt, v)
+    vt2, v2 = vt.clone(), v.clone()
+    vt2[1, 0, 5] = float("inf")
+    v2[2, 1, 77] = float("-inf")
+    got = run(vt2, v2)
+    assert not got[1, 0, :, 5].isfinite().any() and not got[2, 1, :, 77].isfinite().any()
+    got[1, 0, :, 5] = want[1, 0, :, 5]
+    got[2, 1, :, 77] = want[2, 1, :, 77]
+    assert torch.equal(got, want)
