@@ -701,27 +701,27 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
                 // is 0, and 0 times a value that is not finite would still
                 // spoil the row.  Such values leave the product; a row that
                 // sees one becomes NaN in that channel.
-                bool any = false;
-                constexpr uint32_t kExp = DT == KIVI_BF16 ? 0x7f80u : 0x7c00u;
-#pragma unroll 1
+                constexpr uint32_t kExp = DT == KIVI_BF16 ? 0x7f80u : 0x7c00u, kLow = DT == KIVI_BF16 ? 0x80u : 0x400u;
+                uint32_t bad = 0;   // an exponent of ones plus its lowest bit reaches the sign
+#pragma unroll 4
                 for (int k = 0; k < D / 8; ++k) {
-                    const int q = k * 32 + lane, row = q / (D / 8), ch = q % (D / 8);
-                    uint16_t *x = (uint16_t *)(sm_v + chunk_at<D>(row, ch));
-                    uint32_t w[4];
-                    *(uint4 *)w = *(const uint4 *)x;
-                    bool bad = false;
-#pragma unroll
-                    for (int z = 0; z < 4; ++z)
-                        bad = bad || (w[z] & kExp) == kExp || ((w[z] >> 16) & kExp) == kExp;
-                    if (bad)
+                    const int q = k * 32 + lane;
+                    const uint4 w = *(const uint4 *)(sm_v + chunk_at<D>(q / (D / 8), q % (D / 8)));
+                    bad |= ((w.x & (kExp * 0x10001u)) + kLow * 0x10001u) | ((w.y & (kExp * 0x10001u)) + kLow * 0x10001u)
+                           | ((w.z & (kExp * 0x10001u)) + kLow * 0x10001u) | ((w.w & (kExp * 0x10001u)) + kLow * 0x10001u);
+                }
+                if (__any_sync(0xffffffffu, (bad & 0x80008000u) != 0)) {
+#pragma unroll 1
+                    for (int k = 0; k < D / 8; ++k) {
+                        const int q = k * 32 + lane, row = q / (D / 8), ch = q % (D / 8);
+                        uint16_t *x = (uint16_t *)(sm_v + chunk_at<D>(row, ch));
+#pragma unroll 1
                         for (int z = 0; z < 8; ++z)
                             if ((x[z] & kExp) == kExp) {
                                 atomicMin(first + ch * 8 + z, row);
                                 x[z] = 0;
-                                any = true;
                             }
-                }
-                if (__any_sync(0xffffffffu, any)) {
+                    }
                     __syncwarp();
 #pragma unroll
                     for (int a = 0; a < NT; ++a)
@@ -1023,10 +1023,12 @@ size_t pool_rows_scratch(int D, int sms)
     return most;
 }
 
-// What an entry's (or unit's) groups cost with 1, 2 or 3 tiles a warp, measured
-// (24 x 8K tokens, 8 kv heads; 8, 16 and 24 rows): the decoding is shared, the
+// What a group costs with 1, 2 or 3 tiles a warp, relative (24 x 8K tokens, 8 kv
+// heads; 8, 16 and 24 rows: 61, 82 and 111 us): the decoding is shared, the
 // products are not, and two and three tiles run on 8 warps an SM, not 12.
-constexpr double kTileCost[kMaxTiles + 1] = {0.0, 1.0, 1.7, 2.5};
+// Four forks of each of 8 sequences together and apart: of 2K tokens 25.5
+// against 31.5 us a call, of 8K 43.6 against 70.7 us.
+constexpr double kTileCost[kMaxTiles + 1] = {0.0, 1.0, 1.35, 1.82};
 
 // Units of the entries, their rows and tokens, and the split's positions.
 // share: entries of the same pages go together as long as their rows fit one
