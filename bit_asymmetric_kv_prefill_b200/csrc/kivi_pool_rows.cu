@@ -922,8 +922,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas(NT))
 
 constexpr int kJoinParts = 8;   // parts per block
 
-// Adds the partial results of the segments that start in the block's parts and
-// end behind them.  Warp (y, f) takes every Y-th partial result of output
+// Adds the partial results, tile blockIdx.y, of the segments that start in the
+// block's parts and end behind them.  Warp (y, f) takes every Y-th partial result of output
 // fragment f, four at a time so that their loads overlap, and the Y sums are
 // added at the end: a fixed order.
 template <int D, int DT, int NT>
@@ -935,7 +935,7 @@ __global__ void __launch_bounds__(1024) pool_join_kernel(const __grid_constant__
     __shared__ int4 list[kJoinParts];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, tq = lane >> 2, cs = lane & 3;
     const int f = wid % NF, y0 = wid / NF;
-    const int w0 = blockIdx.x * kJoinParts;
+    const int w0 = blockIdx.x * kJoinParts, a = blockIdx.y;
     griddep_wait();
     griddep_launch();
     if (threadIdx.x < kJoinParts)
@@ -945,46 +945,42 @@ __global__ void __launch_bounds__(1024) pool_join_kernel(const __grid_constant__
     for (int k = 0; k < kJoinParts; ++k) {
         const int4 j = list[k];
         const int w = w0 + k, last = j.x, e = j.y;
-        if (last < 0) continue;
+        const int row = 8 * NT * j.z + 8 * a;
+        if (last < 0 || row / c.group >= t.toks[e]) continue;
+        Joined<1> s;
+        s.clear();
 #pragma unroll 1
-        for (int a = 0; a < NT; ++a) {
-            const int row = 8 * NT * j.z + 8 * a;
-            if (row / c.group >= t.toks[e]) break;
-            Joined<1> s;
-            s.clear();
-#pragma unroll 1
-            for (int x = w + y0; x <= last; x += 4 * Y) {
-                float q[4][1][4];
-                float4 ml[4];
+        for (int x = w + y0; x <= last; x += 4 * Y) {
+            float q[4][1][4];
+            float4 ml[4];
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    const bool real = x + z * Y <= last;
-                    const float *pa = partial<D, NT>(c, w, real ? x + z * Y : x, a);
-                    ml[z] = *(const float4 *)(pa + 8 * D + 4 * cs);
-                    if (!real) ml[z].y = ml[z].w = 0.0f;   // (counts as nothing seen)
+            for (int z = 0; z < 4; ++z) {
+                const bool real = x + z * Y <= last;
+                const float *pa = partial<D, NT>(c, w, real ? x + z * Y : x, a);
+                ml[z] = *(const float4 *)(pa + 8 * D + 4 * cs);
+                if (!real) ml[z].y = ml[z].w = 0.0f;   // (counts as nothing seen)
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) q[z][0][g] = pa[(4 * f + g) * 32 + lane];
-                }
-#pragma unroll
-                for (int z = 0; z < 4; ++z) s.add(q[z], ml[z]);
+                for (int g = 0; g < 4; ++g) q[z][0][g] = pa[(4 * f + g) * 32 + lane];
             }
 #pragma unroll
-            for (int g = 0; g < 4; ++g) sums[y0][f][g * 32 + lane] = s.o[0][g];
-            if (tq == 0) stats[y0][f][cs] = make_float4(s.m[0], s.l[0], s.m[1], s.l[1]);
-            __syncthreads();
-            if (y0 == 0) {
-#pragma unroll
-                for (int z = 1; z < Y; ++z) {
-                    float q[1][4];
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) q[0][g] = sums[z][f][g * 32 + lane];
-                    s.add(q, stats[z][f][cs]);
-                }
-                const float f0 = s.l[0] == 0.0f ? 0.0f : 1.0f / s.l[0], f1 = s.l[1] == 0.0f ? 0.0f : 1.0f / s.l[1];
-                store_rows<DT>(c, t, e, j.w, row + tq, 16 * f, s.o[0], f0, f1);
-            }
-            __syncthreads();
+            for (int z = 0; z < 4; ++z) s.add(q[z], ml[z]);
         }
+#pragma unroll
+        for (int g = 0; g < 4; ++g) sums[y0][f][g * 32 + lane] = s.o[0][g];
+        if (tq == 0) stats[y0][f][cs] = make_float4(s.m[0], s.l[0], s.m[1], s.l[1]);
+        __syncthreads();
+        if (y0 == 0) {
+#pragma unroll
+            for (int z = 1; z < Y; ++z) {
+                float q[1][4];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) q[0][g] = sums[z][f][g * 32 + lane];
+                s.add(q, stats[z][f][cs]);
+            }
+            const float f0 = s.l[0] == 0.0f ? 0.0f : 1.0f / s.l[0], f1 = s.l[1] == 0.0f ? 0.0f : 1.0f / s.l[1];
+            store_rows<DT>(c, t, e, j.w, row + tq, 16 * f, s.o[0], f0, f1);
+        }
+        __syncthreads();
     }
 }
 
@@ -997,8 +993,8 @@ cudaError_t rows_t(AttnCall &c, AttnTab &t, bool here, cudaStream_t st)
     if (e != cudaSuccess) return e;
     e = launch_dependent(kernel, dim3((t.parts + kRowWarps - 1) / kRowWarps), kRowWarps * 32, RowsSmem<D>::BYTES, st, c, t);
     if (e != cudaSuccess || here) return e;
-    return launch_dependent(pool_join_kernel<D, DT, NT>, dim3((t.parts + kJoinParts - 1) / kJoinParts), 1024, 0, st,
-                            c, t);
+    return launch_dependent(pool_join_kernel<D, DT, NT>, dim3((t.parts + kJoinParts - 1) / kJoinParts, NT), 1024, 0,
+                            st, c, t);
 }
 
 template <int D, int DT>
@@ -1031,15 +1027,14 @@ size_t pool_rows_scratch(int D, int sms)
 constexpr double kTileCost[kMaxTiles + 1] = {0.0, 1.0, 1.35, 1.82};
 
 // Units of the entries, their rows and tokens, and the split's positions.
-// share: entries of the same pages go together as long as their rows fit one
-// warp.  Returns the cost; nt: the tiles per warp.
-double plan_units(const AttnCall &c, AttnTab &t, bool share, int &nt)
+// Entries of the same pages go together as long as their rows are `rows` at the
+// most (up to those of one warp).  Returns the cost; nt: the tiles per warp.
+double plan_units(const AttnCall &c, AttnTab &t, int rows, int &nt)
 {
     t.units = 0;
-    long long most = 0;
+    long long most = 0, extra = 0;
     for (int e = 0; e < t.nb; ++e) {
-        const bool joins = share && e > 0 && t.same[e]
-                           && ((long long)t.toks[t.units - 1] + t.n[e]) * c.group <= 8 * kMaxTiles;
+        const bool joins = e > 0 && t.same[e] && ((long long)t.toks[t.units - 1] + t.n[e]) * c.group <= rows;
         if (!joins) {
             t.first[t.units] = e;
             t.toks[t.units] = t.raw[t.units] = 0;
@@ -1050,7 +1045,12 @@ double plan_units(const AttnCall &c, AttnTab &t, bool share, int &nt)
         t.raw[u] += (t.r[e] + 31) / 32 + (t.nk[e] + 31) / 32;
         most = std::max(most, (long long)t.toks[u]);
     }
+    // Uncoded blocks of a shared unit cost half as much again (all its rows go
+    // through every entry's).  Four forks of 8 x 500 tokens together 26.8 us,
+    // apart 20.3; two of them 14.4 and 18.3.
     t.first[t.units] = t.nb;
+    for (int u = 0; u < t.units; ++u)
+        if (t.first[u + 1] - t.first[u] > 1) extra += t.raw[u];
     // As many tiles per warp as the most rows of a unit need: the decoded
     // fragments serve all of them.
     most = (most * c.group + 7) / 8;
@@ -1062,15 +1062,25 @@ double plan_units(const AttnCall &c, AttnTab &t, bool share, int &nt)
         const long long tiles = ((long long)t.toks[u] * c.group + 8 * nt - 1) / (8 * nt);
         t.off[u + 1] = t.off[u] + tiles * c.v.H * (C > 0 ? C : 1);
     }
-    return kTileCost[nt] * (double)t.off[t.units];
+    return kTileCost[nt] * (double)(t.off[t.units] + extra * c.v.H);
 }
 
 // Fills the split (t.off and its parts) and launches.
 cudaError_t launch_pool_rows(AttnCall &c, AttnTab &t, int sms, cudaStream_t st)
 {
     int nt = 0;
-    const double shared = plan_units(c, t, true, nt);
-    if (t.units < t.nb && plan_units(c, t, false, nt) > shared) plan_units(c, t, true, nt);
+    double least = plan_units(c, t, 0, nt);
+    if (std::find(t.same, t.same + t.nb, true) != t.same + t.nb) {
+        int rows = 0;
+        for (int k = 1; k <= kMaxTiles; ++k) {
+            const double cost = plan_units(c, t, 8 * k, nt);
+            if (cost < least) {
+                least = cost;
+                rows = 8 * k;
+            }
+        }
+        plan_units(c, t, rows, nt);
+    }
     if (nt == 0) return cudaSuccess;
     if (t.off[t.units] == 0) return cudaSuccess;
     // At least kPartItems items per part: a partial result costs as much.
