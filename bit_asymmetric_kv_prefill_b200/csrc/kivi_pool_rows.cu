@@ -28,7 +28,11 @@
 // Tokens not yet coded take the same products in their own type, straight
 // from their rows.
 //
-// A warp owns a row tile and a range of the work: the (sequence, row tile, kv
+// Sequences that hold the same pages (forks) may form a unit: their rows lie in
+// one row tile and share the pass over the pages; the uncoded tokens of each are
+// masked for the others' rows.
+//
+// A warp owns a row tile and a range of the work: the (unit, row tile, kv
 // head) segments lie one after another, 1 per key group and kRawWeight per 32
 // uncoded tokens, and the total is cut into equal ranges (so no sequence
 // length leaves a warp idle).  A segment inside one range is finished by its
@@ -38,13 +42,13 @@
 // fragments are decoded in registers: the codes of the block are ordered so
 // that one masked word is two codes of a fragment register.
 //
-// Bound: issue.  A group (32 tokens, one kv head, 24 D bytes) costs a warp 574
-// instructions at 8 rows and D = 128 (ALU 42%, tensor pipe 31%, issue 54% of
+// Bound: issue.  A group (32 tokens, one kv head, 24 D bytes) costs a warp 556
+// instructions at 8 rows and D = 128 (ALU 43%, tensor pipe 32%, issue 54% of
 // the cycles with the 12 warps that the registers leave an SM); DRAM traffic is
 // the algorithmic bytes (1.015x).  Measured, D = 128: 24 x 8,192 tokens x 8 kv
-// heads of 4 query heads 58 us (2.6 TB/s); 32 x 8K-16K tokens 104 us (3.1 TB/s);
+// heads of 4 query heads 58 us (2.6 TB/s); 32 x 8K-16K tokens 102 us (3.1 TB/s);
 // 8 x 4,096 tokens x 32 heads of one 48 us; five tokens each (20 rows, three
-// tiles) after 16 x 4K-8K 67 us.  Query rows as the 16-row operand took 81 us
+// tiles) after 16 x 4K-8K 62 us; eight forks of 8 x 8K tokens 57 us (apart 126).  Query rows as the 16-row operand took 81 us
 // in the first of these cases.
 #include <algorithm>
 
@@ -923,9 +927,9 @@ __global__ void __launch_bounds__(kRowWarps * 32, row_ctas(NT))
 constexpr int kJoinParts = 8;   // parts per block
 
 // Adds the partial results, tile blockIdx.y, of the segments that start in the
-// block's parts and end behind them.  Warp (y, f) takes every Y-th partial result of output
-// fragment f, four at a time so that their loads overlap, and the Y sums are
-// added at the end: a fixed order.
+// block's parts and end behind them.  Warp (y, f) takes every Y-th partial
+// result of output fragment f, four at a time so that their loads overlap, and
+// the Y sums are added at the end: a fixed order.
 template <int D, int DT, int NT>
 __global__ void __launch_bounds__(1024) pool_join_kernel(const __grid_constant__ AttnCall c, const __grid_constant__ AttnTab t)
 {

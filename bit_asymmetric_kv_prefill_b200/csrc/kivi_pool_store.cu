@@ -9,10 +9,10 @@
 // All are dependent launches: each starts under the end of the launch before it
 // and waits for it before it touches memory.
 // Measured, 8 sequences of 1,000 tokens that take 1,000 to 2,000 more, 8 heads of
-// 128, bf16: quantizing 27 us (1.8 TB/s; issue 52%, ALU 59%: the threshold
-// arithmetic of kivi_quant.cu), gathering the 2.5K tokens each 25 us (2.8 TB/s;
-// one warp for keys and values of 32 tokens took 31: fewer, longer items leave
-// a longer tail), residual rows 4 us, forks 4 us (one block per residual took 9),
+// 128, bf16: quantizing 25 us (1.9 TB/s; issue 52%, ALU 59%: the threshold
+// arithmetic of kivi_quant.cu), gathering the 2.3K tokens each 23 us (4.0 TB/s
+// with the 76 MB of results partly in L2; one warp for keys and values of 32
+// tokens took a quarter longer: fewer, longer items leave a longer tail), residual rows 4 us, forks 4 us (one block per residual took 9),
 // table entries 2 us.
 #include <algorithm>
 

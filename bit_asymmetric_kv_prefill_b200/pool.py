@@ -114,7 +114,8 @@ class KiviPool:
                lengths=None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """Attention of the new tokens' queries q [sum(lengths), H_q, D] over
         the cached tokens of their sequence and, where K and V [sum(lengths),
-        H_kv, D] are given, the new tokens up to their own.  Returns
+        H_kv, D] are given, the new tokens up to their own.  Forks that still
+        hold the same pages are faster side by side in ``seqs``.  Returns
         [sum(lengths), H_q, D] in the pool's dtype."""
         n = len(seqs)
         if lengths is None:

@@ -469,6 +469,8 @@ KIVI_API kivi_status kivi_pool_extend(kivi_pool *p, const int *seqs, const int *
  *   out  DEVICE [rows, H_q, D] contiguous, 16-byte aligned, in the pool's
  *        dtype; must not overlap the inputs.
  * A key or value that is not finite affects only rows that see its token.
+ * Forks that still hold the same pages and follow one another in seqs share one
+ * pass over them.
  */
 KIVI_API kivi_status kivi_pool_attn(kivi_pool *p, const int *seqs, const int *n_new, int n,
                                     const kivi_rows *q, const kivi_rows *k, const kivi_rows *v,
