@@ -219,12 +219,15 @@ class _on_device:
 
 def _stream_ptr(stream) -> int:
     # The current stream's handle without a Stream object around it (3 us).
-    device = torch._C._cuda_getDevice()
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device)
-    if stream.device_index != device:
-        raise ValueError(f"stream must be a stream of cuda:{device}, got one of cuda:{stream.device_index}")
-    return stream.cuda_stream
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def _own_stream_ptr(stream) -> int:
+    """The same, for calls that make their tensors' device current: a stream of
+    another device is refused."""
+    if stream is not None and stream.device_index != torch._C._cuda_getDevice():
+        raise ValueError(f"stream is one of cuda:{stream.device_index}, the tensors are not")
+    return _stream_ptr(stream)
 
 
 def _empty_like(x, stream):
@@ -235,6 +238,15 @@ def _empty_like(x, stream):
         return torch.empty_like(x, memory_format=torch.contiguous_format)
     with torch.cuda.stream(stream):
         return torch.empty_like(x, memory_format=torch.contiguous_format)
+
+
+def _used_on(stream, *tensors):
+    """``stream`` still works on the tensors after the call: their memory, if
+    freed before it is done, waits for it."""
+    if stream is not None:
+        for x in tensors:
+            if x is not None:
+                x.record_stream(stream)
 
 
 class KiviCache:

@@ -8,7 +8,7 @@ from array import array
 
 import torch
 
-from . import PoolConfig, PoolRows, _check, _dtype_code, _empty_like, _on_device, _stream_ptr, lib
+from . import PoolConfig, PoolRows, _check, _dtype_code, _empty_like, _on_device, _own_stream_ptr, _used_on, lib
 
 
 def _ints(values, what):
@@ -85,14 +85,14 @@ class KiviPool:
         n = len(seqs)
         a = (ctypes.c_int * max(n, 1))()
         with _on_device(self.device.index):
-            _check(call(self._h, _ints(seqs, "seqs"), n, a, _stream_ptr(stream)), what)
+            _check(call(self._h, _ints(seqs, "seqs"), n, a, _own_stream_ptr(stream)), what)
         return a[:n]
 
     def compact(self, stream=None) -> int:
         """Move pages to the front of the pool; returns how many moved."""
         n = ctypes.c_int()
         with _on_device(self.device.index):
-            _check(lib().kivi_pool_compact(self._h, ctypes.byref(n), _stream_ptr(stream)), "kivi_pool_compact")
+            _check(lib().kivi_pool_compact(self._h, ctypes.byref(n), _own_stream_ptr(stream)), "kivi_pool_compact")
         return n.value
 
     # -- tokens -------------------------------------------------------------------
@@ -108,7 +108,8 @@ class KiviPool:
         k, v = self._rows(K, N, self.H_kv, "K"), self._rows(V, N, self.H_kv, "V")
         with _on_device(self.device.index):
             _check(lib().kivi_pool_extend(self._h, _ints(seqs, "seqs"), _ints(lengths, "lengths"), n, ctypes.byref(k),
-                                          ctypes.byref(v), _stream_ptr(stream)), "kivi_pool_extend")
+                                          ctypes.byref(v), _own_stream_ptr(stream)), "kivi_pool_extend")
+        _used_on(stream, K, V)
 
     def attend(self, seqs, q: torch.Tensor, K: torch.Tensor | None = None, V: torch.Tensor | None = None,
                lengths=None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -140,7 +141,8 @@ class KiviPool:
             raise ValueError(f"out must be a contiguous {self.dtype} {(N, H_q, self.D)} tensor on {self.device}")
         with _on_device(self.device.index):
             _check(lib().kivi_pool_attn(self._h, _ints(seqs, "seqs"), _ints(lengths, "lengths"), n, ctypes.byref(qr),
-                                        kr, vr, H_q, out.data_ptr(), _stream_ptr(stream)), "kivi_pool_attn")
+                                        kr, vr, H_q, out.data_ptr(), _own_stream_ptr(stream)), "kivi_pool_attn")
+        _used_on(stream, q, K, V, out)
         return out
 
     def gather(self, seqs, K: torch.Tensor | None = None, V: torch.Tensor | None = None, stream=None):
@@ -160,8 +162,9 @@ class KiviPool:
             if not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
         with _on_device(self.device.index):
-            _check(lib().kivi_pool_gather(self._h, ids, n, K.data_ptr(), V.data_ptr(), _stream_ptr(stream)),
+            _check(lib().kivi_pool_gather(self._h, ids, n, K.data_ptr(), V.data_ptr(), _own_stream_ptr(stream)),
                    "kivi_pool_gather")
+        _used_on(stream, K, V)
         return K, V
 
     # -- inspection ---------------------------------------------------------------

@@ -6,7 +6,7 @@ import ctypes
 
 import torch
 
-from . import RopeScaling, RopeTensor, _check, _dtype_code, _empty_like, _on_device, _stream_ptr, lib
+from . import RopeScaling, RopeTensor, _check, _dtype_code, _empty_like, _on_device, _own_stream_ptr, _used_on, lib
 
 PLAIN, LINEAR, BASE, YARN, BANDS = "plain", "linear", "base", "yarn", "bands"
 _KINDS = {PLAIN: 0, LINEAR: 1, BASE: 2, YARN: 3, BANDS: 4}
@@ -79,5 +79,6 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_f
                                 _side(k, k_out, (N, k.shape[1], D), dtype, device, "k")), 2
     with _on_device(device):
         _check(lib().kivi_rope(t, n, _dtype_code(dtype), N, D, positions.data_ptr(), pos64, inv_freq.data_ptr(), rot,
-                               interleaved, scale, inverse, fp32_angles, _stream_ptr(stream)), "kivi_rope")
+                               interleaved, scale, inverse, fp32_angles, _own_stream_ptr(stream)), "kivi_rope")
+    _used_on(stream, q, k, positions, inv_freq, q_out, k_out)
     return q_out, k_out

@@ -377,10 +377,25 @@ def test_new_results_belong_to_the_stream_that_writes_them():
         # The memory is free again, for its own stream only.
         new = [torch.empty(x, dtype=torch.float16, device="cuda") for x in shapes]
         assert at.isdisjoint(x.data_ptr() for x in new)
+    # Inputs that are freed before the stream has read them keep their memory until then.
+    size = (100, 4, D)
+    x, p = torch.zeros(size, dtype=torch.float16, device="cuda"), torch.arange(100, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)   # 0.1 s
+    for call in (lambda: kivi.rope(x, None, p, f, stream=s), lambda: pool.attend([a], x, lengths=[100], stream=s),
+                 lambda: pool.extend([a], x[:, :2], x[:, 2:], lengths=[100], stream=s)):
+        call()
+        at = x.data_ptr()
+        x = None
+        x = torch.zeros(size, dtype=torch.float16, device="cuda")
+        assert x.data_ptr() != at
+    s.synchronize()
+    assert pool.length(a) == (128, 12)
     other = types.SimpleNamespace(cuda_stream=0, device_index=torch.cuda.current_device() + 1)
     with pytest.raises(ValueError):
         pool.extend([a], K[:1], V[:1], [1], stream=other)
-    assert pool.length(a) == (32, 8)
+    assert pool.length(a) == (128, 12)
 
 
 # ---- attention (GPU) ------------------------------------------------------------------
