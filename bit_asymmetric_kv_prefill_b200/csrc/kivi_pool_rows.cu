@@ -20,7 +20,8 @@
 // the codes enter as they are (a masked word is a pair of fp16 subnormals
 // c 4^k 2^-24, exact, the power taken out at the end; fp16 pools: c - 1, with
 // z + s), the probabilities are
-// multiplied by the four groups' scales and rounded once to fp16, and the z of
+// multiplied by the four groups' scales and rounded once to fp16 (fp16 pools: p
+// and p s as two fp16 parts each), and the z of
 // the 32-channel groups are four rows of one more product.  p is kept
 // multiplied by 2^-E with E following the largest s seen, so that p s neither
 // overflows nor loses bits below 2^-24.
@@ -48,7 +49,7 @@
 // the algorithmic bytes (1.015x).  Measured, D = 128: 24 x 8,192 tokens x 8 kv
 // heads of 4 query heads 58 us (2.6 TB/s); 32 x 8K-16K tokens 102 us (3.1 TB/s);
 // 8 x 4,096 tokens x 32 heads of one 48 us; five tokens each (20 rows, three
-// tiles) after 16 x 4K-8K 62 us; eight forks of 8 x 8K tokens 57 us (apart 126).  Query rows as the 16-row operand took 81 us
+// tiles) after 16 x 4K-8K 79 us (fp16); eight forks of 8 x 8K tokens 57 us (apart 126).  Query rows as the 16-row operand took 81 us
 // in the first of these cases.
 #include <algorithm>
 
@@ -308,7 +309,10 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
     // in place of c cuts that by a third (error against 64 bits 3.3e-4 -> 2.6e-4
     // where the plain form has 2.1e-4) for one more instruction per code pair.
     // bf16 results do not show it.
-    constexpr bool kLessOne = DT == KIVI_F16;
+    // Where no token has most of the weight the roundings of p and p s would
+    // still show (3.6e-4 against the plain form's 2.1e-4), so both enter in two
+    // parts there (16 x 4K-8K tokens, five new each: 79 us; in one part 62).
+    constexpr bool kLessOne = DT == KIVI_F16, kTwo = kLessOne;
     // Kept in registers: as constants each use would load them anew, next to
     // the mask that the logic instruction already holds.
     uint32_t one[5];
@@ -461,14 +465,21 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
             softmax_step<D, NT>(st, oz, S, sc, (float)E);
             {
                 // P transposed: rows 8a + tq, token pairs 8p + 2cs.
-                uint32_t pt[NT][4];
+                uint32_t pt[NT][4], pl[NT][4];   // (pl: what pt leaves out)
 #pragma unroll
                 for (int a = 0; a < NT; ++a)
 #pragma unroll
-                    for (int f = 0; f < 2; ++f) {
-                        pt[a][2 * f] = transpose8(pack2<KIVI_F16>(S[a][f][0], S[a][f][1]));
-                        pt[a][2 * f + 1] = transpose8(pack2<KIVI_F16>(S[a][f][2], S[a][f][3]));
-                    }
+                    for (int f = 0; f < 2; ++f)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const float u = S[a][f][2 * x], w = S[a][f][2 * x + 1];
+                            const uint32_t p = pack2<KIVI_F16>(u, w);
+                            pt[a][2 * f + x] = transpose8(p);
+                            if constexpr (kTwo) {
+                                const float2 q = unpack2<KIVI_F16>(p);
+                                pl[a][2 * f + x] = transpose8(pack2<KIVI_F16>(u - q.x, w - q.y));
+                            }
+                        }
                 {
                     // Row tq of A: the zeros of channel group tq, row 8 + tq
                     // its scales, which c - 1 leaves out.  Row NJ holds ones:
@@ -485,6 +496,10 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
                     for (int a = 0; a < NT; ++a) {
                         mma<KIVI_F16>(oz[a], z[0].y, z[0].x, z[1].y, z[1].x, pt[a][0], pt[a][1]);
                         mma<KIVI_F16>(oz[a], z[2].y, z[2].x, z[3].y, z[3].x, pt[a][2], pt[a][3]);
+                        if constexpr (kTwo) {
+                            mma<KIVI_F16>(oz[a], z[0].y, z[0].x, z[1].y, z[1].x, pl[a][0], pl[a][1]);
+                            mma<KIVI_F16>(oz[a], z[2].y, z[2].x, z[3].y, z[3].x, pl[a][2], pl[a][3]);
+                        }
                     }
                 }
                 uint32_t vw[L::WPL];
@@ -493,11 +508,15 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
                     *(uint4 *)(vw + 4 * q) = *(const uint4 *)(blk + L::VC + (q * 32 + lane) * 16);
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) {
-                    uint32_t ps[NT][4];
+                    uint32_t ps[NT][4], sl[NT][4];
 #pragma unroll
                     for (int a = 0; a < NT; ++a)
 #pragma unroll
-                        for (int p = 0; p < 4; ++p) ps[a][p] = as_u(__hmul2(as_h2(pt[a][p]), as_h2(vs[p][j])));
+                        for (int p = 0; p < 4; ++p) {
+                            const __half2 u = as_h2(pt[a][p]), sc2 = as_h2(vs[p][j]), hi = __hmul2(u, sc2);
+                            ps[a][p] = as_u(hi);
+                            if constexpr (kTwo) sl[a][p] = as_u(__hfma2(as_h2(pl[a][p]), sc2, __hfma2(u, sc2, __hneg2(hi))));
+                        }
                     uint32_t w[4], x10[4];
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
@@ -516,8 +535,11 @@ __device__ __forceinline__ void run_items(const AttnCall &c, const AttnTab &t, c
                             const uint32_t a2 = kLessOne ? as_u(code_less_one(w1, x1, i, one)) : code_tiny(w1, x1, i);
                             const uint32_t a3 = kLessOne ? as_u(code_less_one(w1, x1, i + 1, one)) : code_tiny(w1, x1, i + 1);
 #pragma unroll
-                            for (int a = 0; a < NT; ++a)
+                            for (int a = 0; a < NT; ++a) {
                                 mma<KIVI_F16>(st.o[a][2 * j + ff], a0, a1, a2, a3, ps[a][2 * mm], ps[a][2 * mm + 1]);
+                                if constexpr (kTwo)
+                                    mma<KIVI_F16>(st.o[a][2 * j + ff], a0, a1, a2, a3, sl[a][2 * mm], sl[a][2 * mm + 1]);
+                            }
                         }
                     }
                 }
